@@ -1,4 +1,5 @@
-"""GB300-native Mixture-of-Experts FFN layer forward.
+"""GB300-native Mixture-of-Experts FFN layer forward, and the attention of the
+same decoder layer (``attention.py``).
 
 Thin Python binding (ctypes) over the C ABI of ``libmoe_gb300.so``
 (``include/moe.h``).  The functions here only check and marshal arguments:
@@ -15,7 +16,9 @@ import torch
 
 __all__ = ["MoEError", "lib", "workspace_size", "alloc_workspace", "route", "permute", "forward",
            "read_status", "read_diagnostics", "LIB_PATH", "nvfp4_tc_scales", "nvfp4_quantize",
-           "W4A4Weights", "w4a4_weights", "forward_w4a4", "forward_int8", "int8_struct"]
+           "W4A4Weights", "w4a4_weights", "forward_w4a4", "forward_int8", "int8_struct",
+           "attn_workspace_size", "alloc_attn_workspace", "rope_table", "rope_append", "attn_prefill",
+           "attn_prefill_paged", "attn_decode"]
 
 # MOE_GB300_LIB selects another build of the library (e.g. the index-checking
 # MOE_DEBUG_BOUNDS build); the default is the in-tree libmoe_gb300.so.
@@ -343,3 +346,10 @@ def read_diagnostics(workspace, stream=None) -> dict:
     buf = (ctypes.c_int32 * 4)()
     _check(lib().moe_read_diagnostics(_ptr(workspace), _stream(stream), buf), "moe_read_diagnostics")
     return dict(num_active=buf[0], num_large=buf[1], router_flagged=buf[2], router_fallback=buf[3])
+
+
+from . import attention as _attention  # noqa: E402  (uses the helpers above)
+from .attention import (alloc_attn_workspace, attn_decode, attn_prefill, attn_prefill_paged,  # noqa: E402,F401
+                        attn_workspace_size, rope_append, rope_table)
+
+_SIGNATURES.update(_attention.SIGNATURES)

@@ -1,0 +1,114 @@
+// Attention operators: argument structs of the kernels, the workspace of an
+// attention call and the host-side launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace moe {
+namespace attn {
+
+// ------------------------------------------------------------- workspace
+// Header of an attention call's workspace.  Its kernels report what they
+// found in one word per block, written by every block: nothing has to be
+// cleared before a call, so a call is not preceded by a clearing kernel.
+// `magic` sits where the layer calls keep their status word and holds a value
+// that no set of kStatus* bits can have.
+constexpr int kHeaderMagic = 0x41540000;
+constexpr int kFlagSets = 2;           // kernels of one call that report
+constexpr int kFlagsPerSet = 4096;     // blocks of one reporting kernel
+struct Header {
+  int magic;
+  int blocks[kFlagSets];               // words in use of each set
+  int pad[61];
+};
+static_assert(sizeof(Header) == sizeof(WsHeader), "header is one 256-byte slot");
+
+struct Layout {
+  size_t hdr, flags, total;
+};
+
+inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
+  (void)T; (void)n_seq; (void)Hq; (void)Hkv; (void)D;
+  Layout L{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
+  L.hdr = take(sizeof(Header));
+  L.flags = take(sizeof(int) * kFlagSets * kFlagsPerSet);
+  L.total = o;
+  return L;
+}
+
+// OR of the words that the kernels of the last call left (the stream is idle);
+// -1 when the copy fails
+int read_flags(const void* workspace);
+
+// Where a kernel of a call reports: its own set of words
+struct Report {
+  void* ws;
+  int set;
+  int blocks[kFlagSets];
+};
+
+// Every block of a reporting kernel calls this once (one thread), whatever it
+// found: the words of a call are complete when its kernels are.
+__device__ __forceinline__ void report(const Report& r, int bits) {
+  int* flags = reinterpret_cast<int*>(reinterpret_cast<char*>(r.ws) + sizeof(Header));
+  flags[r.set * kFlagsPerSet + blockIdx.x] = bits;
+  if (blockIdx.x == 0) {
+    Header* h = reinterpret_cast<Header*>(r.ws);
+    h->magic = kHeaderMagic;
+    for (int i = 0; i < kFlagSets; ++i) h->blocks[i] = r.blocks[i];
+  }
+}
+
+// ------------------------------------------------------------- arguments
+struct Heads {                // [tokens, heads, D], strides in elements
+  const uint16_t* data;
+  long long tok, head;
+};
+
+struct RopeArgs {
+  Heads q, k, v;
+  const float* q_norm;        // [D] or null
+  const float* k_norm;
+  float eps;
+  const float* table;         // [max_pos, rot]: cos | sin
+  int max_pos, rot, interleaved;
+  const int32_t* positions;
+  const int32_t* slots;
+  int T, Hq, Hkv, D, f16;
+  uint16_t* q_out;            // [T, Hq, D]
+  uint16_t* k_cache;          // [pages, Hkv, page_size, D]
+  uint16_t* v_cache;
+  int pages, page_shift;      // page_size = 1 << page_shift
+};
+
+// One attention call.  Packed keys: k, v, kv_starts.  Paged: k_cache,
+// v_cache, page_table, kv_lens.  Decode is n_seq rows of one token each
+// (q_starts null) with an optional shared prefix.
+struct AttnArgs {
+  Heads q, k, v;
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  const int32_t* page_table;  // [n_seq, table_pages], null when packed
+  const int32_t* prefix_table;
+  const int32_t* q_starts;
+  const int32_t* kv_starts;
+  const int32_t* kv_lens;
+  int table_pages, pages, page_shift;
+  int prefix_len;
+  int n_seq, T, Tk, Hq, Hkv, D, f16, causal;
+  float scale;
+  uint16_t* out;              // [T, Hq, D]
+  float* lse;                 // [T, Hq] or null
+};
+
+cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_attn(const AttnArgs& a, void* ws, const Layout& L, int num_sms, cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace moe

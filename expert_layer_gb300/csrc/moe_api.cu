@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "moe.h"
+#include "attn.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -510,6 +511,9 @@ int moe_read_status(const void* workspace, void* stream) {
   int st = 0;
   if (cudaMemcpy(&st, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return MOE_ERR_CUDA;
+  // an attention call leaves one word per block instead of one status word
+  if (st == attn::kHeaderMagic) st = attn::read_flags(workspace);
+  if (st < 0) return MOE_ERR_CUDA;
   if (st & kStatusTimeout) return MOE_ERR_DEVICE_TIMEOUT;
   if (st & (kStatusBadExpert | kStatusRange | kStatusBounds)) return MOE_ERR_DEVICE;
   return MOE_OK;

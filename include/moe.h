@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe_gb300.so: the forward pass of a Mixture-of-Experts
  * FFN layer (router, expert grouping, grouped SwiGLU experts, combine) on one
- * NVIDIA GB300 GPU (sm_103a).
+ * NVIDIA GB300 GPU (sm_103a), and the attention of the same decoder layer
+ * (paged key-value cache, rotary positions, prompts and single tokens).
  *
  * The layer follows the phases that the serving worklogs time inside the
  * fused-MoE path -- "MoE gate", then "topk, expert kernel, activation, sum"
@@ -341,6 +342,123 @@ int moe_forward_int8_profiled(const uint16_t *x, const uint16_t *gate_w, const f
  * faulted GPU.
  */
 int moe_debug_force_wait_timeout(int polls);
+
+/*
+ * ------------------------------------------------------------- attention
+ * The other half of a decoder layer that serves with this one: query / key
+ * norms and rotary positions with the append to a paged key-value cache, and
+ * the attention that reads it, for whole prompts and for single tokens.  (The
+ * pages name the attention backends and the paged cache of their serving
+ * stacks -- page "Decode 吞吐专项实验分析报告", section "七" -- but give no
+ * interface; this one is the library's own.)
+ *
+ * Notation: T query tokens (rows), Hq query heads, Hkv key-value heads,
+ * G = Hq / Hkv (query head h reads key-value head h / G), D head size.
+ * Element types: bf16 or f16 (`dtype`), the same for q, k, v, the cache and
+ * the outputs; every sum, softmax statistic and norm is fp32.
+ * Supported: D 64 or 128, Hq a multiple of Hkv with G <= 128, page sizes 16,
+ * 32, 64, 128 and 256, T * Hq < 2^31.
+ *
+ * Conventions as above, except that int32 index arrays (positions, slots,
+ * starts, lengths, page tables) need only 4-byte alignment and heads may be
+ * strided (moe_heads).  Index arrays are checked by the kernels: an entry out
+ * of range is recorded as MOE_ERR_DEVICE (moe_read_status), addresses no
+ * memory, and leaves the results of its sequence unspecified.
+ */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1 } moe_dtype;
+
+/* A view [tokens, heads, D] with contiguous D (host struct): strides in
+ * elements, multiples of 8; data 16-byte aligned. */
+typedef struct {
+  const void *data;
+  int64_t token_stride;
+  int64_t head_stride;
+} moe_heads;
+
+/* A paged key-value cache (host struct): k and v are dense [pages, Hkv,
+ * page_size, D], so that one head's page is one contiguous block.  A page
+ * table row lists a sequence's pages in order; token j of the sequence is row
+ * j % page_size of its page j / page_size.  Rows past a sequence's length are
+ * never used, whatever they hold. */
+typedef struct {
+  void *k;
+  void *v;
+  int32_t pages;
+  int32_t page_size;
+} moe_kv_cache;
+
+/* Bytes of workspace for any moe_rope_append / moe_attn_* call with up to T
+ * query rows and n_seq sequences.  Returns 0 for an invalid shape. */
+size_t moe_attn_workspace_size(int T, int n_seq, int Hq, int Hkv, int D);
+
+/*
+ * Query / key norms, rotary positions, and the append to the paged cache, in
+ * one pass over a projection's rows:
+ *   n(x) = x * weight / sqrt(mean(x^2) + eps)   over a head's D elements
+ *          (skipped where the weight pointer is NULL)
+ *   R(x) = rotation of the first `rot` elements by the position's angles:
+ *          pairs (i, i + rot/2), or (2i, 2i+1) with interleaved != 0;
+ *          (a, b) -> (a cos - b sin, b cos + a sin)
+ *   q_out[t, h]           = R(n(q[t, h]))                    [T, Hq, D]
+ *   cache.k[page, h, row] = R(n(k[t, h])),  page = slots[t] / page_size,
+ *   cache.v[page, h, row] = v[t, h],        row  = slots[t] % page_size
+ * fp32 throughout, each result rounded once to `dtype`.
+ *   table      [max_pos, rot] fp32: cos of the rot/2 angles, then their sines
+ *              (frequencies and any scaling for long contexts are the table's)
+ *   positions  [T] int32 in [0, max_pos);  slots [T] int32 in
+ *              [0, pages * page_size), or negative: q_out is written, the
+ *              cache is not.  Two tokens with one slot leave either's values.
+ *   q_norm, k_norm [D] fp32 or NULL;  rot a multiple of 16, 0 <= rot <= D.
+ * q_out may be q's own memory (same strides, that is dense).
+ */
+int moe_rope_append(const moe_heads *q, const moe_heads *k, const moe_heads *v, const float *q_norm,
+                    const float *k_norm, float eps, const float *table, int max_pos, int rot,
+                    int interleaved, const int32_t *positions, const int32_t *slots, int T, int Hq,
+                    int Hkv, int D, int dtype, void *q_out, const moe_kv_cache *cache,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention over packed sequences (whole prompts):
+ *   out[t, h] = sum_j p_j v[j, h/G],  p = softmax_j(scale * q[t, h] . k[j, h/G])
+ * over the keys j of row t's own sequence; with causal != 0 row i of a
+ * sequence of n rows and m keys sees the keys j <= i + (m - n).  A row that
+ * sees no key gets out = 0 and lse = -inf.
+ *   q_starts, kv_starts [n_seq + 1] int32, ascending from 0 to T and Tk: the
+ *            rows / keys of sequence s are [starts[s], starts[s+1])
+ *   out      [T, Hq, D] dense;  lse [T, Hq] fp32 or NULL: the natural log of
+ *            the softmax denominator, log sum_j exp(scale * q . k_j)
+ * Keys and values that a row does not see through the causal mask must be
+ * finite; those of other sequences and past the end may hold anything.
+ */
+int moe_attn_prefill(const moe_heads *q, const moe_heads *k, const moe_heads *v,
+                     const int32_t *q_starts, const int32_t *kv_starts, int n_seq, int T, int Tk,
+                     int Hq, int Hkv, int D, int dtype, int causal, float scale, void *out,
+                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * moe_attn_prefill with the keys and values in the paged cache (chunks of a
+ * long prompt, whose new tokens are in the cache already and read the ones
+ * before them): sequence s has kv_lens[s] keys on the pages
+ * page_table[s, 0 ..]; page_table is [n_seq, table_pages] int32.
+ */
+int moe_attn_prefill_paged(const moe_heads *q, const moe_kv_cache *cache, const int32_t *page_table,
+                           int table_pages, const int32_t *q_starts, const int32_t *kv_lens,
+                           int n_seq, int T, int Hq, int Hkv, int D, int dtype, int causal,
+                           float scale, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of one new token for each of B sequences over the paged cache.
+ * Row b's context is the shared prefix (prefix_len tokens on the pages
+ * prefix_table[0 ..], the same for every row; prefix_table may be NULL when
+ * prefix_len is 0) followed by its own kv_lens[b] tokens on
+ * page_table[b, 0 ..].  The prefix is read and multiplied once for the whole
+ * batch.  A row without any key gets out = 0, lse = -inf.
+ */
+int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t *page_table,
+                    int table_pages, const int32_t *kv_lens, const int32_t *prefix_table,
+                    int prefix_len, int B, int Hq, int Hkv, int D, int dtype, float scale, void *out,
+                    float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of a moe_status value. */
 const char *moe_error_string(int status);
