@@ -27,17 +27,28 @@ struct Header {
 };
 static_assert(sizeof(Header) == sizeof(WsHeader), "header is one 256-byte slot");
 
+// Rows of the partial results of calls whose key axis is split over blocks:
+// at most two tiles of 128 rows per block of a grid (attn_tc.cu), or one per
+// row and block where a call has fewer.  kMaxBlocks bounds the SMs of a GPU.
+constexpr long long kMaxBlocks = 160;
+constexpr long long kTileRows = 256;
+
 struct Layout {
-  size_t hdr, flags, total;
+  size_t hdr, flags, part_o, part_lse, total;
 };
 
 inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
-  (void)T; (void)n_seq; (void)Hq; (void)Hkv; (void)D;
+  (void)Hkv;
   Layout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
+  long long rows = (T * Hq < kTileRows ? T * Hq : kTileRows) * kMaxBlocks;
+  const long long single = (T < n_seq ? T : n_seq) * Hq;      // decode rows: one part each at least
+  if (rows < single) rows = single;
   L.hdr = take(sizeof(Header));
   L.flags = take(sizeof(int) * kFlagSets * kFlagsPerSet);
+  L.part_o = take(sizeof(float) * (size_t)rows * D);
+  L.part_lse = take(sizeof(float) * (size_t)rows);
   L.total = o;
   return L;
 }
@@ -108,7 +119,27 @@ struct AttnArgs {
 };
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);
-cudaError_t launch_attn(const AttnArgs& a, void* ws, const Layout& L, int num_sms, cudaStream_t stream);
+
+// attn_tc.cu -- tiles of 128 rows (tt tokens x G heads), two per block; slots:
+// tile slots of the batch (see find_seq)
+struct TcPlan {
+  int tt, slots;
+};
+inline TcPlan tc_plan(const AttnArgs& a) {
+  const int tt = 128 / (a.Hq / a.Hkv), per = 2 * tt;
+  return TcPlan{tt, a.q_starts ? a.T / per + a.n_seq : (a.T + per - 1) / per};
+}
+// Parts that a call splits each row's keys into (1: none, the result is final)
+constexpr int kBlocksPerSplit = 4;
+int tc_splits(const AttnArgs& a, int num_sms);
+cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& rep,
+                           int num_sms, cudaStream_t stream);
+
+// attn_merge.cu -- joins the parts of every row
+cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const float* part_o, const float* part_lse,
+                              cudaStream_t stream);
+
+cudaError_t launch_attn_rows(const AttnArgs& a, const Report& rep, int num_sms, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace moe

@@ -116,7 +116,15 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   a.f16 = dtype == MOE_F16;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  return cuda_status(launch_attn(a, workspace, L, sms, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (sms > kMaxBlocks) sms = kMaxBlocks;
+  const Report rep{workspace, 0, {0, 0}};
+  if (!a.q_starts) return cuda_status(launch_attn_rows(a, rep, sms, s));
+  const int splits = tc_splits(a, sms);
+  float* po = splits > 1 ? ws_ptr<float>(workspace, L.part_o) : nullptr;
+  float* pl = splits > 1 ? ws_ptr<float>(workspace, L.part_lse) : nullptr;
+  ATTN_TRY(cuda_status(launch_attn_tc(a, splits, po, pl, rep, sms, s)));
+  return splits > 1 ? cuda_status(launch_attn_merge(a, splits, po, pl, s)) : MOE_OK;
 }
 
 }  // namespace

@@ -91,10 +91,11 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, c
 
 }  // namespace
 
-cudaError_t launch_attn(const AttnArgs& a, void* ws, const Layout&, int num_sms, cudaStream_t stream) {
+cudaError_t launch_attn_rows(const AttnArgs& a, const Report& shape, int num_sms, cudaStream_t stream) {
   const long long blocks = ((long long)a.T * a.Hq + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = (int)(blocks < 8ll * num_sms ? blocks : 8ll * num_sms);
-  const Report rep{ws, 0, {grid, 0}};
+  Report rep = shape;
+  rep.blocks[rep.set] = grid;
   auto kern = a.D == 64 ? (a.f16 ? attn_rows_kernel<64, true> : attn_rows_kernel<64, false>)
                         : (a.f16 ? attn_rows_kernel<128, true> : attn_rows_kernel<128, false>);
   kern<<<grid, kThreads, 0, stream>>>(a, rep);

@@ -1,0 +1,744 @@
+// Attention of many rows on the tensor cores: whole prompts, chunks of them
+// over the paged cache, and the shared prefix of a decode batch.
+//
+// A tile is 128 rows of one key-value head: `tt` tokens x G query heads
+// (tt = 128 / G, row = token * G + head), so that the G heads of a group
+// share every key and value tile.  A block takes two tiles (2 tt tokens of one
+// sequence) through the visible keys in blocks of 128:
+//   S = Q K^T                      tcgen05.mma, fp32 in tensor memory
+//   m' = max(m, max_j c S_j)       c = scale log2(e)
+//   P = 2^{c S - m'},  l += sum P  fp32; P rounded to the element type for
+//   O += P V                       the second product (A from tensor memory)
+// with out = O / l and lse = (m + log2 l) ln 2 at the end.  The maximum in use
+// may lag the true one by up to 2^8 (P <= 256 in both types, l and O are
+// fp32): only when a row exceeds it by more is O rescaled, which after the
+// first blocks hardly happens.
+#include <cuda.h>
+
+#include "attn.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace attn {
+namespace {
+
+using namespace tcx;
+
+constexpr int kRows = 128;          // rows of a tile
+constexpr int kKeys = 128;          // keys of a block
+constexpr int kItems = 4;           // ring of work items
+constexpr int kSoftWarps = 8;       // two tiles x four warps, one row per thread
+constexpr int kThreads = (kSoftWarps + 4) * 32;
+// Registers per thread: 168 at launch (three warpgroups); the softmax
+// warpgroups, which hold a row of 128 logits, draw on the third one's.
+constexpr int kSoftRegs = 216, kLoadRegs = 72;
+static_assert(2 * kSoftRegs + kLoadRegs <= 3 * 168, "the shares come from the launch's registers");
+constexpr float kLag = 8.0f;        // log2 of how far the maximum in use may lag
+constexpr uint32_t kTmemCols = 512;
+
+template <int D>
+struct Shape {
+  static constexpr int kHalves = D / 64;                       // 128-byte wide swizzled columns
+  static constexpr int kHalfBytes = kRows * 128;               // 16 KB
+  static constexpr int kTileBytes = kHalves * kHalfBytes;      // a Q, K or V tile
+  static constexpr int kStages = D == 128 ? 5 : 10;            // ring of K and V tiles
+  static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr size_t kSmem = kBars + 1024 + 1024;
+};
+
+struct Item {
+  int row0;        // first token row of tile 0; -1: no more items
+  int tok[2];      // tokens of the two tiles
+  int n[2];        // key blocks of the two tiles
+  int head;        // key-value head
+  int b0;          // first key block
+  int len;         // keys of the sequence
+  int seen;        // keys that token row0 sees (causal; may be <= 0), else len
+  int split;
+};
+
+struct TcAttnArgs {
+  AttnArgs a;
+  int tt, slots, splits, items;
+  int box;                       // rows of a K / V box
+  float c;                       // |scale| log2 e, > 0
+  int negate;                    // scale < 0
+  float* part_o;                 // [splits, T, Hq, D], null when splits is 1
+  float* part_lse;               // [splits, T, Hq], log2
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (kF16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A wait of a warp that the tensor cores or the softmax depend on: bounded as
+// mbar_wait, without its sleeps.
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kSpinLimit; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Values [keys][D] as the B operand of O += P V: D-major ("transposed"),
+// 128-byte swizzle; the next 64 columns of D one half tile on (leading
+// offset), the next 8 keys 1024 bytes on (stride offset).
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr, uint32_t half_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+  d |= (uint64_t)(half_bytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accum));
+}
+// kind::f16 with fp32 accumulators; b_t: B is N-major
+template <bool kF16>
+__device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_t) {
+  return (1u << 4) | ((kF16 ? 0u : 1u) << 7) | ((kF16 ? 0u : 1u) << 10) | ((b_t ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ work items
+// Sequence s owns the tile slots base(s) .. base(s+1) - 1 with base(s) =
+// floor(q_starts[s] / (2 tt)) + s: at least as many as it has tiles, without a
+// prefix sum over the batch.  All lanes of the warp search together.
+__device__ __forceinline__ int find_seq(const AttnArgs& a, int per, int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.n_seq;                       // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int s = lo + lane * step;
+    const bool at = lane * step < n && a.q_starts[s] / per + s <= slot;
+    const int hit = 31 - __clz((int)(__ballot_sync(0xffffffffu, at) | 1u));
+    lo += hit * step;
+    n = min(step, n - hit * step);
+  }
+  return lo;
+}
+
+// Item `idx` (warp-uniform); false when its slot has no rows.  Later tiles of
+// a sequence see more keys: they come first.
+__device__ __forceinline__ bool make_item(const TcAttnArgs& t, int idx, Item& it, int& seq, int& k0) {
+  const AttnArgs& a = t.a;
+  it.split = idx % t.splits;
+  idx /= t.splits;
+  it.head = idx % a.Hkv;
+  const int slot = t.slots - 1 - idx / a.Hkv;
+  const int per = 2 * t.tt;
+  int q0 = 0, q1 = a.T, tile = slot;
+  seq = 0;
+  if (a.q_starts) {
+    seq = find_seq(a, per, slot);
+    q0 = a.q_starts[seq];
+    q1 = a.q_starts[seq + 1];
+    tile = slot - (q0 / per + seq);
+    if (q0 < 0 || q1 < q0 || q1 > a.T || tile < 0) return false;
+  }
+  const long long first = (long long)tile * per;
+  if (first >= q1 - q0) return false;
+  it.row0 = q0 + (int)first;
+  const int left = q1 - it.row0;
+  it.tok[0] = min(left, t.tt);
+  it.tok[1] = max(0, min(left - t.tt, t.tt));
+  k0 = 0;
+  if (a.prefix_table) {
+    it.len = a.prefix_len;
+  } else if (a.page_table) {
+    it.len = a.kv_lens[seq];
+    if (it.len < 0 || it.len > ((long long)a.table_pages << a.page_shift)) it.len = 0;
+  } else {
+    k0 = a.kv_starts[seq];
+    it.len = a.kv_starts[seq + 1] - k0;
+    if (k0 < 0 || it.len < 0 || k0 > a.Tk - it.len) k0 = 0, it.len = 0;
+  }
+  it.seen = a.causal ? it.len - (q1 - q0) + (int)first + 1 : it.len;
+  int nb[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    int v = a.causal ? it.seen + x * t.tt + it.tok[x] - 1 : it.len;   // keys the tile's last token sees
+    v = min(v, it.len);
+    nb[x] = it.tok[x] > 0 && v > 0 ? (v + kKeys - 1) / kKeys : 0;
+  }
+  const int all = max(nb[0], nb[1]);
+  it.b0 = (int)((long long)all * it.split / t.splits);
+  const int b1 = (int)((long long)all * (it.split + 1) / t.splits);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) it.n[x] = max(0, min(nb[x], b1) - it.b0);
+  return true;
+}
+
+// Index arrays of the call, checked once (block 0): what is out of order is
+// reported here and skipped or clamped where it is used.
+__device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
+  bool bad = false;
+  if (a.q_starts)
+    for (int s = threadIdx.x; s < a.n_seq; s += kThreads) {
+      const int q0 = a.q_starts[s], q1 = a.q_starts[s + 1];
+      bad |= q0 < 0 || q1 < q0 || q1 > a.T;
+      if (!a.page_table) {
+        const int k0 = a.kv_starts[s], k1 = a.kv_starts[s + 1];
+        bad |= k0 < 0 || k1 < k0 || k1 > a.Tk;
+      } else {
+        const int n = a.kv_lens[s];
+        bad |= n < 0 || n > ((long long)a.table_pages << a.page_shift);
+      }
+    }
+  return bad;
+}
+
+// ------------------------------------------------------------------ the kernel
+// warps 0-3, 4-7   softmax and epilogue of tile 0 and 1 (thread = row)
+// warp 8           work items, TMA loads of Q, K and V
+// warp 9           issues the MMAs (warps 10, 11 only complete the warpgroup): per key block O0 += P0 V, S0 = Q0 K',
+//                  O1 += P1 V, S1 = Q1 K' (K' the next block), so that each
+//                  tile's softmax runs while the other tile multiplies
+// Tensor memory: S0 | S1 | O0 | O1; P overwrites the first half of its S.
+// One thread issues every MMA, in order: a commit after S(j+1) also covers
+// O += P(j) V, so a softmax warp that has S(j+1) may rescale O without waiting.
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const TcAttnArgs t, const Report rep) {
+  using S = Shape<D>;
+  constexpr int NS = S::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* kv_empty = kv_full + NS;
+  uint64_t* q_full = kv_empty + NS;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* it_full = o_full + 2;
+  uint64_t* it_empty = it_full + kItems;
+  uint64_t* drain = it_empty + kItems;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  Item* ring = reinterpret_cast<Item*>(drain + 2);
+
+  const AttnArgs& a = t.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+    }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], 1); mbar_init(&it_empty[i], kSoftWarps + 1); }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  bool bad = blockIdx.x == 0 && bad_arrays(a);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    if (warp == kSoftWarps) {
+    // ------------------------------------------------------------ producer
+    uint32_t kv = 0, nq[2] = {0, 0}, ni = 0;    // loads issued, items published
+    bool ok = true;
+    const int boxes = kKeys / t.box;            // boxes of a full K or V tile (per 64 columns)
+    for (int r = 0; ok; ++r) {
+      // every other round in reverse: the blocks' sums of work stay close
+      const long long idx = (long long)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const bool end = (long long)r * gridDim.x >= t.items;
+      Item it;
+      int seq = 0, k0 = 0;
+      if (!end) {
+        if (idx >= t.items || !make_item(t, (int)idx, it, seq, k0)) continue;
+      } else {
+        it = Item{};
+        it.row0 = -1;
+      }
+      const int slot = ni % kItems;
+      if (!warp_wait(&it_empty[slot], ((ni / kItems) & 1) ^ 1)) { ok = false; break; }
+      if (lane == 0) {
+        ring[slot] = it;
+        mbar_arrive(&it_full[slot]);
+      }
+      ++ni;
+      if (end) break;
+      const int n = max(it.n[0], it.n[1]);
+      const int32_t* list = nullptr;
+      if (a.page_table) list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
+      // page of this lane's box in block b (lanes 0 .. boxes-1)
+      auto page_of = [&](int b) {
+        const int key = b * kKeys + lane * t.box;
+        if (!list || lane >= boxes || key >= it.len) return 0;
+        const int p = list[key >> a.page_shift];
+        if ((unsigned)p < (unsigned)a.pages) return p;
+        bad = true;
+        return 0;
+      };
+      int page = n > 0 ? page_of(it.b0) : 0;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (ok && it.n[x] > 0) {
+          ok = warp_wait(&q_empty[x], (nq[x] & 1) ^ 1);
+          if (ok && lane == 0) {
+            mbar_expect_tx(&q_full[x], (uint32_t)(S::kHalves * G * t.tt * 128));
+            for (int hh = 0; hh < S::kHalves; ++hh)
+              tma_load_3d(smem + x * S::kTileBytes + hh * S::kHalfBytes, &tmQ, hh * 64, it.head * G,
+                          it.row0 + x * t.tt, &q_full[x]);
+          }
+          if (ok) ++nq[x];
+        }
+      for (int j = 0; j < n && ok; ++j) {
+        const int b = it.b0 + j;
+        const int next = j + 1 < n ? page_of(b + 1) : 0;
+        // boxes that hold keys of the sequence; the rest of the tile is not read
+        const int nbox = min(boxes, (it.len - b * kKeys + t.box - 1) / t.box);
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w, ++kv) {
+          const int s = kv % NS;
+          ok = warp_wait(&kv_empty[s], ((kv / NS) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
+          __syncwarp();
+          if (lane < nbox) {
+            unsigned char* dst = smem + S::kRing + s * S::kTileBytes + lane * t.box * 128;
+            const int key = b * kKeys + lane * t.box;
+            const int row = list ? key & ((1 << a.page_shift) - 1) : k0 + key;
+            for (int hh = 0; hh < S::kHalves; ++hh)
+              tma_load_4d(dst + hh * S::kHalfBytes, w ? &tmV : &tmK, hh * 64, row, it.head, list ? page : 0,
+                          &kv_full[s]);
+          }
+        }
+        page = next;
+      }
+      if (*(volatile int*)abort_flag) ok = false;
+    }
+    if (!ok) {
+      // after a timeout: the loads already issued land before the block exits
+      if (lane == 0) {
+        atomicOr(abort_flag, 1);
+        for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) mbar_wait(&kv_full[i % NS], (i / NS) & 1);
+        for (int x = 0; x < 2; ++x)
+          if (nq[x]) mbar_wait(&q_full[x], (nq[x] - 1) & 1);
+      }
+      __syncwarp();
+    }
+    } else if (warp == kSoftWarps + 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
+      uint32_t kv = 0, ni = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      bool ok = true;
+      const uint32_t sQ = smem_u32(smem), sR = sQ + S::kRing;
+      // the addresses of a product's steps are formed where they are used:
+      // hoisted out of the loop they would not fit the registers
+      auto product_s = [&](int x, int s) {
+        uint32_t d = tmem + x * kKeys, q = sQ + x * S::kTileBytes, k = sR + s * S::kTileBytes;
+        asm volatile("" : "+r"(d), "+r"(q), "+r"(k));
+        const uint64_t dq = umma_desc(q), dk = umma_desc(k);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4;
+          umma_bf16_id(d, dq + off, dk + off, kIdS, kk ? 1u : 0u);
+        }
+        umma_commit(&s_full[x]);
+      };
+      auto product_o = [&](int x, int s, bool add) {
+        uint32_t d = tmem + 2 * kKeys + x * D, p = tmem + x * kKeys, v = sR + s * S::kTileBytes;
+        asm volatile("" : "+r"(d), "+r"(p), "+r"(v));
+        const uint64_t dv = umma_desc_v(v, S::kHalfBytes);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_ts(d, p + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO, add || kk ? 1u : 0u);
+      };
+      while (ok) {
+        const int slot = ni % kItems;
+        if (!mbar_wait(&it_full[slot], (ni / kItems) & 1)) { ok = false; break; }
+        const Item it = ring[slot];
+        mbar_arrive(&it_empty[slot]);
+        ++ni;
+        if (it.row0 < 0) break;
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        const uint32_t kv0 = kv;
+        kv += 2 * n;
+        auto stage = [&](int j, int w) { return (int)((kv0 + 2 * j + w) % NS); };
+        auto full = [&](int j, int w) { return spin_wait(&kv_full[stage(j, w)], ((kv0 + 2 * j + w) / NS) & 1); };
+        ok = full(0, 0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && it.n[x] > 0) {
+            ok = spin_wait(&q_full[x], nq[x]++ & 1);
+            if (!ok) continue;
+            tc_fence_after();
+            product_s(x, stage(0, 0));
+            if (it.n[x] == 1) umma_commit(&q_empty[x]);
+          }
+        if (!ok) break;
+        umma_commit(&kv_empty[stage(0, 0)]);
+        for (int j = 0; j < n && ok; ++j) {
+          ok = full(j, 1) && (j + 1 >= n || full(j + 1, 0));
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= it.n[x]) continue;
+            ok = spin_wait(&p_full[x], np[x]++ & 1);
+            if (!ok) continue;
+            tc_fence_after();
+            product_o(x, stage(j, 1), j > 0);
+            if (j + 1 < it.n[x]) {
+              product_s(x, stage(j + 1, 0));
+              if (j + 2 == it.n[x]) umma_commit(&q_empty[x]);
+            } else {
+              umma_commit(&o_full[x]);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&kv_empty[stage(j, 1)]);
+          if (j + 1 < n) umma_commit(&kv_empty[stage(j + 1, 0)]);
+        }
+        if (*(volatile int*)abort_flag) ok = false;
+      }
+      if (!ok) {
+        // after a timeout: the MMAs already issued finish before their memory is freed
+        atomicOr(abort_flag, 1);
+        umma_commit(drain);
+        mbar_wait(drain, 0);
+      }
+    }
+    __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ------------------------------------------------------------ softmax, epilogue
+    const int x = warp >> 2;                                   // tile
+    const int row = (warp & 3) * 32 + lane;                    // row of the tile
+    const int token = row / G, g = row - token * G;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + x * kKeys, tO = tmem + lanes + 2 * kKeys + x * D;
+    uint32_t ni = 0, ns = 0, no = 0, kv = 0;
+    bool ok = true;
+    while (ok) {
+      const int slot = ni % kItems;
+      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[slot], (ni / kItems) & 1))) { ok = false; break; }
+      const Item it = ring[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      ++ni;
+      if (it.row0 < 0) break;
+      const int n = x ? it.n[1] : it.n[0];
+      const uint32_t kv0 = kv;
+      kv += 2 * max(it.n[0], it.n[1]);
+      // keys that this row sees, and that the tile's first token sees
+      const int vis = a.causal ? min(it.seen + x * t.tt + token, it.len) : it.len;
+      const int vis0 = a.causal ? min(it.seen + x * t.tt, it.len) : it.len;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j, ++ns) {
+        if (!__all_sync(0xffffffffu, spin_wait(&s_full[x], ns & 1))) { ok = false; break; }
+        tc_fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
+        tmem_wait_ld();
+        const int b = it.b0 + j;
+        if (t.negate) {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) s[i] = -s[i];
+        }
+        if (vis0 < (b + 1) * kKeys) {
+          const int lim = vis - b * kKeys;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kKeys; i += 4)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[i + u]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * t.c;
+        const bool up = top > m + kLag;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2(m - top) : 1.0f;            // m = -inf: 0
+          if (up) m = top;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+              tmem_st16(tO + i, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float p0 = ex2(fmaf(s[64 * h + 2 * i], t.c, -off));
+            const float p1 = ex2(fmaf(s[64 * h + 2 * i + 1], t.c, -off));
+            sum[2 * (i & 1)] += p0;
+            sum[2 * (i & 1) + 1] += p1;
+            p[i] = pack2<kF16>(p0, p1);
+          }
+          tmem_st32(tS + 32 * h, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // The block that the keys end in: rows of its V tile past the end hold
+        // other data (or NaN), which a weight of 0 does not silence: clear them.
+        // The first tile that multiplies the block does it.
+        const int tail = it.len & (kKeys - 1);
+        if (tail && b == it.len / kKeys && (x == 0 || j >= it.n[0])) {
+          const uint32_t i = kv0 + 2 * j + 1;
+          if (!__all_sync(0xffffffffu, spin_wait(&kv_full[i % NS], (i / NS) & 1))) { ok = false; break; }
+          if (row >= tail) {
+            uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + row * 128);
+#pragma unroll
+            for (int u = 0; u < S::kHalves * 8; ++u)
+              v[(u / 8) * (S::kHalfBytes / 16) + u % 8] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      if (n > 0 && !__all_sync(0xffffffffu, spin_wait(&o_full[x], no++ & 1))) { ok = false; break; }
+      tc_fence_after();
+      const bool live = token < (x ? it.tok[1] : it.tok[0]);
+      const long long out_row = ((long long)(it.row0 + x * t.tt + token)) * a.Hq + it.head * G + g;
+      const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;     // l is NaN: so is the row
+      if (t.part_o) {
+        const long long part = (long long)it.split * a.T * a.Hq + out_row;
+        if (live) t.part_lse[part] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
+        if (n > 0)
+#pragma unroll 1
+          for (int i = 0; i < D; i += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + i, o);
+            tmem_wait_ld();
+            if (live)
+#pragma unroll
+              for (int u = 0; u < 32; u += 4)
+                *reinterpret_cast<float4*>(t.part_o + part * D + i + u) =
+                    make_float4(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv,
+                                __uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
+          }
+      } else {
+        if (live && a.lse) a.lse[out_row] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(tO + i, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = 0;
+          }
+          if (live)
+#pragma unroll
+            for (int u = 0; u < 32; u += 8) {
+              uint4 w;
+              w.x = pack2<kF16>(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
+              w.y = pack2<kF16>(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
+              w.z = pack2<kF16>(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
+              w.w = pack2<kF16>(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
+              *reinterpret_cast<uint4*>(a.out + out_row * D + i + u) = w;
+            }
+        }
+      }
+      tc_fence_before();
+      if (*(volatile int*)abort_flag) { ok = false; break; }
+    }
+    if (!ok && lane == 0) atomicOr(abort_flag, 1);
+  }
+
+  tc_fence_before();
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) report(rep, (any ? kStatusBounds : 0) | (*abort_flag ? kStatusTimeout : 0));
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+// ------------------------------------------------------------------ host side
+// 4-D map over keys or values: {D, row, head, page}; box {64, rows, 1, 1}.
+bool kv_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* cache, const Heads& packed, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4], strides[3];
+  const void* base;
+  if (a.page_table) {
+    const cuuint64_t page = (cuuint64_t)a.D << a.page_shift;
+    dims[0] = a.D; dims[1] = 1ull << a.page_shift; dims[2] = a.Hkv; dims[3] = a.pages;
+    strides[0] = a.D * 2ull; strides[1] = page * 2; strides[2] = page * 2 * a.Hkv;
+    base = cache;
+  } else {
+    dims[0] = a.D; dims[1] = a.Tk > 0 ? a.Tk : 1; dims[2] = a.Hkv; dims[3] = 1;
+    const bool none = a.Tk == 0;       // no key is ever loaded: any valid address
+    strides[0] = none ? a.D * 2ull : packed.tok * 2ull;
+    strides[1] = none ? a.D * 2ull : packed.head * 2ull;
+    strides[2] = strides[0];
+    base = none ? a.q.data : packed.data;
+    if (none) dims[2] = 1;
+  }
+  const cuuint32_t boxd[4] = {64, (cuuint32_t)box, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxd, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D map over the queries: {D, head, token}; box {64, G, tt}.
+bool q_map(CUtensorMap* m, const AttnArgs& a, int tt) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
+  const cuuint64_t strides[2] = {a.q.head * 2ull, a.q.tok * 2ull};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(a.Hq / a.Hkv), (cuuint32_t)tt};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q.data), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kF16>
+cudaError_t launch(const TcAttnArgs& t, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const Report& rep, int grid, cudaStream_t stream) {
+  auto kern = attn_tc_kernel<D, kF16>;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+  if (err != cudaSuccess) return err;
+  kern<<<grid, kThreads, Shape<D>::kSmem, stream>>>(q, k, v, t, rep);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int tc_splits(const AttnArgs& a, int num_sms) {
+  const TcPlan p = tc_plan(a);
+  const long long units = (long long)p.slots * a.Hkv;
+  const long long keys = a.prefix_table ? a.prefix_len : a.page_table ? (long long)a.table_pages << a.page_shift : a.Tk;
+  const long long blocks = (keys + kKeys - 1) / kKeys;
+  long long s = num_sms / units;
+  if (s > blocks / kBlocksPerSplit) s = blocks / kBlocksPerSplit;
+  return s < 1 ? 1 : (int)s;
+}
+
+cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& shape,
+                           int num_sms, cudaStream_t stream) {
+  TcAttnArgs t{};
+  t.a = a;
+  const TcPlan p = tc_plan(a);
+  t.tt = p.tt;
+  t.slots = p.slots;
+  t.splits = splits;
+  const long long items = (long long)p.slots * a.Hkv * splits;
+  if (items >= (1ll << 31)) return cudaErrorInvalidValue;
+  t.items = (int)items;
+  t.box = a.page_table && (1 << a.page_shift) < kKeys ? 1 << a.page_shift : kKeys;
+  t.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
+  t.negate = a.scale < 0;
+  // a scale of 0 (or so small that it would flush): positive, so that a masked
+  // logit of -inf stays one, and every other still counts as 0
+  if (t.c < 1.2e-38f) t.c = 1.2e-38f;
+  t.part_o = part_o;
+  t.part_lse = part_lse;
+  CUtensorMap q, k, v;
+  if (!q_map(&q, a, t.tt) || !kv_map(&k, a, a.k_cache, a.k, t.box) || !kv_map(&v, a, a.v_cache, a.v, t.box))
+    return cudaErrorInvalidValue;
+  const int grid = (int)(items < num_sms ? items : num_sms);
+  Report rep = shape;
+  rep.blocks[rep.set] = grid;
+  if (a.D == 64)
+    return a.f16 ? launch<64, true>(t, q, k, v, rep, grid, stream) : launch<64, false>(t, q, k, v, rep, grid, stream);
+  return a.f16 ? launch<128, true>(t, q, k, v, rep, grid, stream) : launch<128, false>(t, q, k, v, rep, grid, stream);
+}
+
+}  // namespace attn
+}  // namespace moe
