@@ -34,7 +34,7 @@ constexpr long long kMaxBlocks = 160;
 constexpr long long kTileRows = 256;
 
 struct Layout {
-  size_t hdr, flags, part_o, part_lse, total;
+  size_t hdr, flags, part_o, part_lse, slot_o, slot_lse, base, total;
 };
 
 inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
@@ -42,13 +42,17 @@ inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long 
   Layout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
+  const long long single = (T < n_seq ? T : n_seq) * Hq;    // rows of a decode batch
   long long rows = (T * Hq < kTileRows ? T * Hq : kTileRows) * kMaxBlocks;
-  const long long single = (T < n_seq ? T : n_seq) * Hq;      // decode rows: one part each at least
   if (rows < single) rows = single;
+  rows += single;                            // decode: one part more for each row's own keys
   L.hdr = take(sizeof(Header));
   L.flags = take(sizeof(int) * kFlagSets * kFlagsPerSet);
   L.part_o = take(sizeof(float) * (size_t)rows * D);
   L.part_lse = take(sizeof(float) * (size_t)rows);
+  L.slot_o = take(sizeof(float) * 2 * kMaxBlocks * 16 * D);
+  L.slot_lse = take(sizeof(float) * 2 * kMaxBlocks * 16);
+  L.base = take(sizeof(long long) * (size_t)(n_seq + 1));
   L.total = o;
   return L;
 }
@@ -132,6 +136,7 @@ inline TcPlan tc_plan(const AttnArgs& a) {
 // Parts that a call splits each row's keys into (1: none, the result is final)
 constexpr int kBlocksPerSplit = 4;
 int tc_splits(const AttnArgs& a, int num_sms);
+int tc_grid(const AttnArgs& a, int splits, int num_sms);
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& rep,
                            int num_sms, cudaStream_t stream);
 
@@ -139,7 +144,30 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const float* part_o, const float* part_lse,
                               cudaStream_t stream);
 
-cudaError_t launch_attn_rows(const AttnArgs& a, const Report& rep, int num_sms, cudaStream_t stream);
+// attn_decode.cu -- one token per sequence.  Parts of rows in the workspace:
+// per row (tc_*: `splits` parts of the prefix [splits, T * Hq], then the row's
+// own keys, row_*, null without a prefix), per block (two slots of 16 rows: a
+// unit that began in an earlier block, and one that goes on in the next), and
+// each sequence's first slice on the line.
+struct DecodeParts {
+  float* tc_o;
+  float* tc_lse;
+  float* row_o;
+  float* row_lse;
+  float* slot_o;
+  float* slot_lse;
+  long long* base;
+};
+// Blocks that share a line of `total` slices: a slice for each warp, or a
+// unit for each block, as far as the grid goes
+__host__ __device__ inline int decode_blocks(long long total, long long units, int grid) {
+  long long n = (total + 7) / 8;
+  if (n < units) n = units;
+  if (n > total) n = total;
+  return (int)(n < 1 ? 1 : n < grid ? n : grid);
+}
+cudaError_t launch_attn_decode(const AttnArgs& a, int splits, const DecodeParts& p, const Report& rep, int num_sms,
+                               cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace moe

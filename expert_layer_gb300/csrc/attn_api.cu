@@ -100,6 +100,28 @@ int check_device(int* num_sms) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+// One token per sequence: the shared prefix's parts on the tensor cores (the
+// whole batch is one sequence of rows for it), then the rows' own keys.
+int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream_t s) {
+  DecodeParts p{};
+  p.tc_o = ws_ptr<float>(ws, L.part_o);
+  p.tc_lse = ws_ptr<float>(ws, L.part_lse);
+  p.slot_o = ws_ptr<float>(ws, L.slot_o);
+  p.slot_lse = ws_ptr<float>(ws, L.slot_lse);
+  p.base = ws_ptr<long long>(ws, L.base);
+  Report rep{ws, 0, {0, sms}};
+  int splits = 0;
+  if (a.prefix_len > 0) {
+    splits = tc_splits(a, sms);
+    rep.blocks[0] = tc_grid(a, splits, sms);
+    ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, sms, s)));
+    p.row_o = p.tc_o + (long long)splits * a.T * a.Hq * a.D;
+    p.row_lse = p.tc_lse + (long long)splits * a.T * a.Hq;
+  }
+  rep.set = 1;
+  return cuda_status(launch_attn_decode(a, splits, p, rep, sms, s));
+}
+
 // The checks shared by the three attention calls, in the order of the others
 // of the library: shape, empty batch, pointers, workspace, device.
 int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, void* workspace,
@@ -119,7 +141,7 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sms > kMaxBlocks) sms = kMaxBlocks;
   const Report rep{workspace, 0, {0, 0}};
-  if (!a.q_starts) return cuda_status(launch_attn_rows(a, rep, sms, s));
+  if (!a.q_starts) return run_decode(a, L, workspace, sms, s);
   const int splits = tc_splits(a, sms);
   float* po = splits > 1 ? ws_ptr<float>(workspace, L.part_o) : nullptr;
   float* pl = splits > 1 ? ws_ptr<float>(workspace, L.part_lse) : nullptr;

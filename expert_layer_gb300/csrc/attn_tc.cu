@@ -16,7 +16,7 @@
 #include <cuda.h>
 
 #include "attn.h"
-#include "tc_ptx.cuh"
+#include "attn_ptx.cuh"
 
 namespace moe {
 namespace attn {
@@ -68,23 +68,6 @@ struct TcAttnArgs {
   float* part_lse;               // [splits, T, Hq], log2
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-template <bool kF16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (kF16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -111,30 +94,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// A wait of a warp that the tensor cores or the softmax depend on: bounded as
-// mbar_wait, without its sleeps.
-__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kSpinLimit; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return false;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
 
 // Values [keys][D] as the B operand of O += P V: D-major ("transposed"),
 // 128-byte swizzle; the next 64 columns of D one half tile on (leading
@@ -647,33 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// 4-D map over keys or values: {D, row, head, page}; box {64, rows, 1, 1}.
-bool kv_map(CUtensorMap* m, const AttnArgs& a, const uint16_t* cache, const Heads& packed, int box) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[4], strides[3];
-  const void* base;
-  if (a.page_table) {
-    const cuuint64_t page = (cuuint64_t)a.D << a.page_shift;
-    dims[0] = a.D; dims[1] = 1ull << a.page_shift; dims[2] = a.Hkv; dims[3] = a.pages;
-    strides[0] = a.D * 2ull; strides[1] = page * 2; strides[2] = page * 2 * a.Hkv;
-    base = cache;
-  } else {
-    dims[0] = a.D; dims[1] = a.Tk > 0 ? a.Tk : 1; dims[2] = a.Hkv; dims[3] = 1;
-    const bool none = a.Tk == 0;       // no key is ever loaded: any valid address
-    strides[0] = none ? a.D * 2ull : packed.tok * 2ull;
-    strides[1] = none ? a.D * 2ull : packed.head * 2ull;
-    strides[2] = strides[0];
-    base = none ? a.q.data : packed.data;
-    if (none) dims[2] = 1;
-  }
-  const cuuint32_t boxd[4] = {64, (cuuint32_t)box, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, boxd, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 3-D map over the queries: {D, head, token}; box {64, G, tt}.
 bool q_map(CUtensorMap* m, const AttnArgs& a, int tt) {
   EncodeTiledFn fn = encode_fn();
@@ -710,6 +642,11 @@ int tc_splits(const AttnArgs& a, int num_sms) {
   return s < 1 ? 1 : (int)s;
 }
 
+int tc_grid(const AttnArgs& a, int splits, int num_sms) {
+  const long long items = (long long)tc_plan(a).slots * a.Hkv * splits;
+  return (int)(items < num_sms ? items : num_sms);
+}
+
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& shape,
                            int num_sms, cudaStream_t stream) {
   TcAttnArgs t{};
@@ -732,7 +669,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   CUtensorMap q, k, v;
   if (!q_map(&q, a, t.tt) || !kv_map(&k, a, a.k_cache, a.k, t.box) || !kv_map(&v, a, a.v_cache, a.v, t.box))
     return cudaErrorInvalidValue;
-  const int grid = (int)(items < num_sms ? items : num_sms);
+  const int grid = tc_grid(a, splits, num_sms);
   Report rep = shape;
   rep.blocks[rep.set] = grid;
   if (a.D == 64)
