@@ -140,10 +140,6 @@ int tc_grid(const AttnArgs& a, int splits, int num_sms);
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& rep,
                            int num_sms, cudaStream_t stream);
 
-// attn_merge.cu -- joins the parts of every row
-cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const float* part_o, const float* part_lse,
-                              cudaStream_t stream);
-
 // attn_decode.cu -- one token per sequence.  Parts of rows in the workspace:
 // per row (tc_*: `splits` parts of the prefix [splits, T * Hq], then the row's
 // own keys, row_*, null without a prefix), per block (two slots of 16 rows: a
@@ -158,16 +154,20 @@ struct DecodeParts {
   float* slot_lse;
   long long* base;
 };
-// Blocks that share a line of `total` slices: a slice for each warp, or a
-// unit for each block, as far as the grid goes
-__host__ __device__ inline int decode_blocks(long long total, long long units, int grid) {
-  long long n = (total + 7) / 8;
-  if (n < units) n = units;
-  if (n > total) n = total;
+// Blocks that share a line of `total` slices: at least a slice for each of
+// their eight warps, as far as the grid goes
+__host__ __device__ inline int decode_blocks(long long total, int grid) {
+  const long long n = (total + 7) / 8;
   return (int)(n < 1 ? 1 : n < grid ? n : grid);
 }
-cudaError_t launch_attn_decode(const AttnArgs& a, int splits, const DecodeParts& p, const Report& rep, int num_sms,
+// Units of at most 16 heads per key-value head
+inline int decode_chunks(const AttnArgs& a) { return (a.Hq / a.Hkv + 15) / 16; }
+cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& rep, int num_sms,
                                cudaStream_t stream);
+
+// attn_merge.cu -- joins the parts of every row (decode_grid 0: prefill)
+cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
+                              cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace moe

@@ -119,7 +119,8 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
     p.row_lse = p.tc_lse + (long long)splits * a.T * a.Hq;
   }
   rep.set = 1;
-  return cuda_status(launch_attn_decode(a, splits, p, rep, sms, s));
+  ATTN_TRY(cuda_status(launch_attn_decode(a, splits > 0, p, rep, sms, s)));
+  return cuda_status(launch_attn_merge(a, splits, p, sms, s));
 }
 
 // The checks shared by the three attention calls, in the order of the others
@@ -143,10 +144,12 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   const Report rep{workspace, 0, {0, 0}};
   if (!a.q_starts) return run_decode(a, L, workspace, sms, s);
   const int splits = tc_splits(a, sms);
-  float* po = splits > 1 ? ws_ptr<float>(workspace, L.part_o) : nullptr;
-  float* pl = splits > 1 ? ws_ptr<float>(workspace, L.part_lse) : nullptr;
-  ATTN_TRY(cuda_status(launch_attn_tc(a, splits, po, pl, rep, sms, s)));
-  return splits > 1 ? cuda_status(launch_attn_merge(a, splits, po, pl, s)) : MOE_OK;
+  if (splits == 1) return cuda_status(launch_attn_tc(a, 1, nullptr, nullptr, rep, sms, s));
+  DecodeParts p{};
+  p.tc_o = ws_ptr<float>(workspace, L.part_o);
+  p.tc_lse = ws_ptr<float>(workspace, L.part_lse);
+  ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, sms, s)));
+  return cuda_status(launch_attn_merge(a, splits, p, 0, s));
 }
 
 }  // namespace

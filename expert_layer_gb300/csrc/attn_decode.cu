@@ -7,11 +7,13 @@
 // lengths as different as 1 and 100,000 load the GPU evenly; a unit that
 // spans blocks leaves one part per block and the merge kernel joins them.
 //
-// Bound: HBM (4 D bytes per key and key-value head against 4 G D flops).  In a
-// block every warp works alone on slices w, w + 8, ... of the unit with its
-// own softmax state, m, l and O in registers, and keeps its own ring of
-// slices filled by TMA, across units: no barrier until the unit's end, where
-// the eight states are joined.
+// Bound: HBM (4 D bytes per key and key-value head against 4 G D flops).  A
+// block's range is cut once more over its eight warps, each of which works
+// alone on consecutive slices with its softmax state, m, l and O in
+// registers, and keeps a ring of slices filled by TMA, across units: no
+// barrier until the block's end.  A unit that lies within a warp's range is
+// finished there; what a warp holds of a unit that crosses its range goes to
+// shared memory, where the block joins it at its end.
 //   S = Q K^T, O += P V   mma.sync m16n8k16, rows = heads (8 or 16 of 16)
 #include "attn.h"
 #include "attn_ptx.cuh"
@@ -23,27 +25,39 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlice = 16;          // keys
-constexpr int kStages = 3;          // slices in flight per warp
+constexpr int kWindow = kThreads;   // sequences whose lengths a block keeps in shared memory
 constexpr float kLag = 8.0f;        // log2 of how far the maximum in use may lag
 
-template <int D>
+template <int D, bool kWide>
 struct Shape {
+  static constexpr int kRows = kWide ? 16 : 8;                     // heads of a unit
   static constexpr int kHalves = D / 64;
   static constexpr int kHalfBytes = kSlice * 128;                  // 2 KB: 16 keys x 64 elements
   static constexpr int kTileBytes = kHalves * kHalfBytes;          // K or V of a slice
   static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = D == 64 ? 5 : kWide ? 2 : 3;      // slices in flight per warp
   static constexpr int kRing = kStages * kStageBytes;              // of one warp
-  static constexpr int kJoin = kWarps * kRing;                     // O of 8 rows, every warp
-  static constexpr int kStats = kJoin + kWarps * 8 * D * 4;        // m and l of 16 rows, every warp
-  static constexpr int kBars = kStats + kWarps * 16 * 2 * 4;
-  static constexpr int kScan = kBars + kWarps * kStages * 8;
-  static constexpr size_t kSmem = kScan + 256 + 1024;
+  static constexpr int kPart = kRows * D * 4;                      // O of one unit
+  static_assert(kPart <= kRing, "a warp's last part takes the place of its ring");
+  static constexpr int kFirst = kWarps * kRing;                    // O of the warps' first parts
+  static constexpr int kStats = kFirst + kWarps * kPart;           // m and l of the rows, two parts per warp
+  static constexpr int kOpen = kStats + kWarps * 2 * kRows * 8;       // the units that the parts belong to
+  static constexpr int kBars = kOpen + kWarps * 2 * 32;
+  static constexpr int kLens = kBars + kWarps * kStages * 8;
+  static constexpr int kScan = kLens + kWindow * 4;
+  static constexpr size_t kSmem = kScan + 128;
 };
+static_assert(Shape<128, false>::kSmem <= 232448 && Shape<128, true>::kSmem <= 232448, "227 KB a block");
 
-// The units of one block: a cursor over (sequence, unit of the sequence),
+// The units of a range: a cursor over (sequence, unit of the sequence),
 // empty sequences left out.  `pos` is the unit's first slice on the line.
 struct Cursor {
   int b, u, len, slices;
+  long long pos;
+};
+// A unit that a warp holds a part of (b < 0: none)
+struct Open {
+  int b, u, slices, pad;
   long long pos;
 };
 
@@ -80,14 +94,24 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
 }
 __device__ __forceinline__ int slices_of(int len) { return (len + kSlice - 1) / kSlice; }
 
+// Lengths of the sequences from b0 on, the first kWindow of them in shared memory
+struct Lens {
+  const AttnArgs* a;
+  const int* window;
+  int b0;
+  __device__ __forceinline__ int operator()(int b) const {
+    return b - b0 < kWindow ? window[b - b0] : seq_len(*a, b);
+  }
+};
+
 // To the next unit that has slices (or past the last sequence).
-__device__ __forceinline__ void advance(const DecodeArgs& t, Cursor& c, int units) {
+__device__ __forceinline__ void advance(const Lens& lens, Cursor& c, int units) {
   c.pos += c.slices;
   if (++c.u < units) return;
   c.u = 0;
   c.slices = 0;
-  while (++c.b < t.a.n_seq) {
-    c.len = seq_len(t.a, c.b);
+  while (++c.b < lens.a->n_seq) {
+    c.len = lens(c.b);
     c.slices = slices_of(c.len);
     if (c.slices) break;
   }
@@ -97,13 +121,13 @@ template <int D, bool kF16, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const DecodeArgs t, const Report rep) {
-  using S = Shape<D>;
+  using S = Shape<D, kWide>;
   constexpr int kRowSets = kWide ? 2 : 1;            // rows g and (wide) g + 8 of a thread
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* join = reinterpret_cast<float*>(smem + S::kJoin);
-  float* stats = reinterpret_cast<float*>(smem + S::kStats);
+  constexpr int kStages = S::kStages;
+  extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
+  float2* stats = reinterpret_cast<float2*>(smem + S::kStats);         // [warp][part][row]: m, l
+  Open* open = reinterpret_cast<Open*>(smem + S::kOpen);               // [warp][part]
+  int* window = reinterpret_cast<int*>(smem + S::kLens);
   long long* scan = reinterpret_cast<long long*>(smem + S::kScan);     // [8] warp sums, then the start
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -111,11 +135,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * kStages;
   unsigned char* ring = smem + warp * S::kRing;
   bool bad = false, late = false;
+  pdl_trigger();     // the merge kernel may become resident; it waits for this grid's end
 
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    open[2 * warp].b = open[2 * warp + 1].b = -1;
   }
 
   // --- the line of slices: every thread sums a run of sequences
@@ -124,8 +150,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long mine = 0;
   for (int s = s0; s < s1; ++s) {
     const int n = a.kv_lens[s];
-    if (blockIdx.x == 0 && (n < 0 || n > ((long long)a.table_pages << a.page_shift))) bad = true;
-    mine += (long long)slices_of(seq_len(a, s)) * units;
+    const bool fits = n >= 0 && n <= ((long long)a.table_pages << a.page_shift);
+    if (blockIdx.x == 0 && !fits) bad = true;
+    mine += (long long)slices_of(fits ? n : 0) * units;
+    if (run == 1) window[s] = fits ? n : 0;
   }
   long long incl = mine;
 #pragma unroll
@@ -150,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == kThreads - 1) t.p.base[a.n_seq] = total;
   }
-  const int blocks = decode_blocks(total, (long long)a.n_seq * units, gridDim.x);
+  const int blocks = decode_blocks(total, gridDim.x);
   const long long start = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
   const bool work = (int)blockIdx.x < blocks && start < end;
   if (work && start >= before && start < before + mine) {
@@ -166,42 +194,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
+  Lens lens{&a, window, 0};
+  if (work && run > 1) {
+    lens.b0 = (int)scan[kWarps];
+    const int s = lens.b0 + threadIdx.x;
+    window[threadIdx.x] = s < a.n_seq ? seq_len(a, s) : 0;
+    __syncthreads();
+  }
 
-  if (work) {
+  // --- this warp's range
+  const long long ws = total * ((long long)blockIdx.x * kWarps + warp) / ((long long)blocks * kWarps);
+  const long long we = total * ((long long)blockIdx.x * kWarps + warp + 1) / ((long long)blocks * kWarps);
+  if (work && ws < we) {
     Cursor cur;
     cur.b = (int)scan[kWarps];
-    cur.len = seq_len(a, cur.b);
-    cur.slices = slices_of(cur.len);
-    cur.u = (int)((start - scan[kWarps + 1]) / cur.slices);
-    cur.pos = scan[kWarps + 1] + (long long)cur.u * cur.slices;
+    cur.pos = scan[kWarps + 1];
+    while (true) {                               // the sequence that ws lies in
+      cur.len = lens(cur.b);
+      cur.slices = slices_of(cur.len);
+      const long long n = (long long)cur.slices * units;
+      if (ws < cur.pos + n) break;
+      cur.pos += n;
+      ++cur.b;
+    }
+    cur.u = (int)((ws - cur.pos) / cur.slices);
+    cur.pos += (long long)cur.u * cur.slices;
 
-    // --- loads: the same walk, a few slices ahead
+    // --- loads: the same walk, kStages slices ahead
     Cursor ld = cur;
-    int ld_slice = (int)max(0ll, start - ld.pos) + warp;     // this warp's next slice of unit ld
+    int ld_slice = (int)(ws - ld.pos);
     uint32_t issued = 0;
+    const uint32_t count = (uint32_t)(we - ws);
     int page = 0;
-    // moves ld to this warp's next slice and fetches its page id; false: none left
-    auto locate = [&]() {
-      while (ld.pos < end) {
-        if (ld_slice < min((long long)ld.slices, end - ld.pos)) {
-          page = a.page_table[(long long)ld.b * a.table_pages + ((ld_slice * kSlice) >> a.page_shift)];
-          return true;
-        }
-        advance(t, ld, units);
-        ld_slice = warp;
+    // the page id of slice `ld_slice` of ld, one slice before its load
+    auto fetch = [&]() {
+      if (issued >= count) return;
+      if (ld_slice == ld.slices) {
+        advance(lens, ld, units);
+        ld_slice = 0;
       }
-      return false;
+      page = a.page_table[(long long)ld.b * a.table_pages + ((ld_slice * kSlice) >> a.page_shift)];
     };
-    bool more = locate();
+    fetch();
     auto issue = [&]() {
-      if (!more) return;
+      if (issued >= count) return;
       if (lane == 0) {
         if ((unsigned)page >= (unsigned)a.pages) {
           bad = true;
           page = 0;
         }
         const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
-        const int hk = ld.u / t.chunks;
+        const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
         unsigned char* dst = ring + st * S::kStageBytes;
         mbar_expect_tx(&bars[st], S::kStageBytes);
 #pragma unroll
@@ -212,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(dst + S::kTileBytes + hh * S::kHalfBytes, &tmV, hh * 64, row, hk, page, &bars[st]);
       }
       ++issued;
-      ld_slice += kWarps;
-      more = locate();
+      ++ld_slice;
+      fetch();
     };
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) issue();
@@ -224,26 +267,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v_row = (lane & 7) + (lane & 8), v_col = lane >> 4;
     const int quad = lane & 3, gq = lane >> 2;
     uint32_t used = 0;
-
-    while (cur.pos < end) {
-      const long long begin = max(0ll, start - cur.pos);
-      const int first = (int)begin, last = (int)min((long long)cur.slices, end - cur.pos);
-      const int hk = cur.u / t.chunks, h0 = hk * G + (cur.u - hk * t.chunks) * 16;
-      const int rows = min(16, hk * G + G - h0);
-      uint32_t q[D / 16][2 * kRowSets];
-      {
-        const uint16_t* src = a.q.data + (long long)cur.b * a.q.tok;
+    auto load_q = [&](const Cursor& c, uint32_t (&q)[D / 16][2 * kRowSets]) {
+      const int hk = t.chunks == 1 ? c.u : c.u / t.chunks;
+      const int h0 = hk * G + (c.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
+      const uint16_t* src = a.q.data + (long long)c.b * a.q.tok;
 #pragma unroll
-        for (int rs = 0; rs < kRowSets; ++rs) {
-          const int r = gq + 8 * rs;
-          const uint16_t* p = src + (long long)(h0 + (r < rows ? r : 0)) * a.q.head + 2 * quad;
+      for (int rs = 0; rs < kRowSets; ++rs) {
+        const int r = gq + 8 * rs;
+        const uint16_t* p = src + (long long)(h0 + (r < rows ? r : 0)) * a.q.head + 2 * quad;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            q[kk][rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16) ^ t.flip : 0u;
-            q[kk][kRowSets + rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16 + 8) ^ t.flip : 0u;
-          }
+        for (int kk = 0; kk < D / 16; ++kk) {
+          q[kk][rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16) ^ t.flip : 0u;
+          q[kk][kRowSets + rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16 + 8) ^ t.flip : 0u;
         }
       }
+    };
+    uint32_t q[D / 16][2 * kRowSets];
+    load_q(cur, q);
+
+    while (cur.pos < we) {
+      const int first = (int)max(0ll, ws - cur.pos), last = (int)min((long long)cur.slices, we - cur.pos);
+      Cursor nxt = cur;
+      advance(lens, nxt, units);
+      uint32_t qn[D / 16][2 * kRowSets];             // the next unit's, under way meanwhile
+      if (!kWide && nxt.pos < we) load_q(nxt, qn);
       float o[D / 8][4];
       float m[kRowSets], l[kRowSets];
 #pragma unroll
@@ -253,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int rs = 0; rs < kRowSets; ++rs) m[rs] = -INFINITY, l[rs] = 0.f;
 
-      for (int s = first + warp; s < last; s += kWarps) {
+#pragma unroll 1
+      for (int s = first; s < last; ++s) {
         const int st = used % kStages;
         if (!late && !__all_sync(0xffffffffu, spin_wait(&bars[st], (used / kStages) & 1))) late = true;
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
@@ -331,161 +379,143 @@ __global__ void __launch_bounds__(kThreads, 1)
         issue();
       }
 
-      // --- join the warps' states: row r is out = sum_w 2^{m_w - M} O_w / sum_w 2^{m_w - M} l_w
+      // --- the end of this warp's part of the unit
 #pragma unroll
       for (int rs = 0; rs < kRowSets; ++rs) {
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
-        if (quad == 0) {
-          stats[(warp * 16 + gq + 8 * rs) * 2] = m[rs];
-          stats[(warp * 16 + gq + 8 * rs) * 2 + 1] = l[rs];
-        }
       }
-      const bool whole = cur.pos >= start && cur.pos + cur.slices <= end;
-      const int slot = 2 * blockIdx.x + (cur.pos < start ? 0 : 1);
+      if (first == 0 && last == cur.slices) {
+        const int hk = t.chunks == 1 ? cur.u : cur.u / t.chunks;
+        const int h0 = hk * G + (cur.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
 #pragma unroll
-      for (int rs = 0; rs < kRowSets; ++rs) {
-        if (first + warp < last) {
+        for (int rs = 0; rs < kRowSets; ++rs) {
+          const int r = gq + 8 * rs;
+          if (r >= rows) continue;
+          const long long row = (long long)cur.b * a.Hq + h0 + r;
+          const float inv = 1.0f / l[rs], lse = m[rs] + lg2(l[rs]);
+          if (t.p.row_o) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<float2*>(t.p.row_o + row * D + 8 * i + 2 * quad) =
+                  make_float2(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+            if (quad == 0) t.p.row_lse[row] = lse;
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<uint32_t*>(a.out + row * D + 8 * i + 2 * quad) =
+                  pack2<kF16>(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+            if (a.lse && quad == 0) a.lse[row] = lse * 0.693147180559945f;
+          }
+        }
+      } else {
+        // part 0: the unit began before this warp's range; part 1: it goes on
+        // after it (every load of the ring has been consumed by then)
+        const int part = first > 0 ? 0 : 1;
+        float* dst = reinterpret_cast<float*>(part ? ring : smem + S::kFirst + warp * S::kPart);
+#pragma unroll
+        for (int rs = 0; rs < kRowSets; ++rs) {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(join + (warp * 8 + gq) * D + 8 * i + 2 * quad) =
+            *reinterpret_cast<float2*>(dst + (gq + 8 * rs) * D + 8 * i + 2 * quad) =
                 make_float2(o[i][2 * rs], o[i][2 * rs + 1]);
+          if (quad == 0) stats[(2 * warp + part) * S::kRows + gq + 8 * rs] = make_float2(m[rs], l[rs]);
         }
-        __syncthreads();
-        const int live = min(kWarps, last - first);            // warps that had a slice
-        for (int i = threadIdx.x; i < 8 * (D / 4); i += kThreads) {
-          const int r8 = i / (D / 4), r = r8 + 8 * rs, d = (i % (D / 4)) * 4;
-          if (r >= rows) continue;
-          float M = -INFINITY;
-          for (int w = 0; w < live; ++w) M = fmaxf(M, stats[(w * 16 + r) * 2]);
-          float sum = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = 0; w < live; ++w) {
-            const float f = M == -INFINITY ? 0.f : ex2(stats[(w * 16 + r) * 2] - M);
-            sum = fmaf(f, stats[(w * 16 + r) * 2 + 1], sum);
-            const float4 x = *reinterpret_cast<const float4*>(join + (w * 8 + r8) * D + d);
-            v.x = fmaf(f, x.x, v.x);
-            v.y = fmaf(f, x.y, v.y);
-            v.z = fmaf(f, x.z, v.z);
-            v.w = fmaf(f, x.w, v.w);
-          }
-          const float inv = 1.0f / sum;
-          v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-          const float lse = M + lg2(sum);
-          const long long row = (long long)cur.b * a.Hq + h0 + r;
-          if (whole && !t.p.row_o) {
-            uint2 w;
-            w.x = pack2<kF16>(v.x, v.y);
-            w.y = pack2<kF16>(v.z, v.w);
-            *reinterpret_cast<uint2*>(a.out + row * D + d) = w;
-            if (a.lse && d == 0) a.lse[row] = lse * 0.693147180559945f;
-          } else {
-            const long long at = whole ? row : (long long)slot * 16 + r;
-            *reinterpret_cast<float4*>((whole ? t.p.row_o : t.p.slot_o) + at * D + d) = v;
-            if (d == 0) (whole ? t.p.row_lse : t.p.slot_lse)[at] = lse;
-          }
-        }
-        __syncthreads();
+        if (lane == 0) open[2 * warp + part] = Open{cur.b, cur.u, cur.slices, 0, cur.pos};
       }
-      advance(t, cur, units);
+      cur = nxt;
+      if (kWide) {
+        if (cur.pos < we) load_q(cur, q);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2 * kRowSets; ++j) q[kk][j] = qn[kk][j];
+      }
     }
     // after a timeout: the loads already issued land before the block exits
     if (late && lane == 0)
       for (uint32_t i = issued > (uint32_t)kStages ? issued - kStages : 0; i < issued; ++i)
         mbar_wait(&bars[i % kStages], (i / kStages) & 1);
   }
-  const int any_bad = __syncthreads_or(bad), any_late = __syncthreads_or(late);
-  if (threadIdx.x == 0) report(rep, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
-}
+  __syncthreads();
 
-// ------------------------------------------------------------------ merge
-// Rows whose keys were split: `splits` parts of the shared prefix (row order),
-// and the row's own keys, which one block did whole (the row's part, or the
-// final result when there is no prefix) or several (their slots, in the order
-// of the blocks).  A warp per row.
-template <int D, bool kF16>
-__global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeArgs t, int splits, int grid) {
-  constexpr int N = D / 32;
-  pdl_wait();   // programmatic dependent launch: the parts are complete
-  const AttnArgs& a = t.a;
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)a.T * a.Hq;
-  const long long row = (long long)blockIdx.x * 4 + threadIdx.x / 32;
-  if (row >= rows) return;
-  const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), G = a.Hq / a.Hkv;
-  const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16, r = (h % G) % 16;
-  const long long total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
-  int c0 = 0, own = 0;                       // blocks c0 .. c0 + own - 1 hold the row's own keys
-  long long start0 = 0;
-  const long long ub = b0 + u * n;
-  if (n > 0) {
-    const long long blocks = decode_blocks(total, (long long)a.n_seq * units, grid);
-    c0 = (int)(((ub + 1) * blocks - 1) / total);
-    own = (int)(((ub + n) * blocks - 1) / total) - c0 + 1;
-    start0 = total * c0 / blocks;
-  }
-  if (splits == 0 && own == 1) return;       // final already
-  // part i < splits: the prefix; then the own parts
-  auto where = [&](int i, const float*& o, const float*& lse) {
-    if (i < splits || own == 1) {
-      const long long at = (long long)i * rows + row;   // the row's own part follows the prefix's
-      o = t.p.tc_o + at * D;
-      lse = t.p.tc_lse + at;
-    } else {
-      const int c = c0 + i - splits;
-      const long long at = (2ll * c + (c == c0 && ub >= start0 ? 1 : 0)) * 16 + r;
-      o = t.p.slot_o + at * D;
-      lse = t.p.slot_lse + at;
-    }
-  };
-  const int parts = splits + own;
-  float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) {
-    const float *o, *lse;
-    where(i, o, lse);
-    top = fmaxf(top, *lse);
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float acc[N], sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < N; ++j) acc[j] = 0.f;
-  if (top != -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const float *o, *lse;
-      where(i, o, lse);
-      const float w = ex2(*lse - top);
-      sum += w;
-      if (w != 0.f) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = fmaf(w, o[lane * N + j], acc[j]);
+  // --- join the warps' parts of units that cross their ranges: row r is
+  // out = sum_w 2^{m_w - M} O_w / sum_w 2^{m_w - M} l_w.  The parts of a unit
+  // follow one another in (warp, part) order.
+#pragma unroll 1
+  for (int e = 0; e < 2 * kWarps;) {
+    const Open op = open[e];
+    int f = e + 1;
+    if (op.b >= 0)
+      while (f < 2 * kWarps && (open[f].b < 0 || (open[f].b == op.b && open[f].u == op.u))) ++f;
+    if (op.b >= 0) {
+      const bool whole = op.pos >= start && op.pos + op.slices <= end;
+      const int slot = 2 * blockIdx.x + (op.pos < start ? 0 : 1);
+      const int hk = t.chunks == 1 ? op.u : op.u / t.chunks;
+      const int h0 = hk * G + (op.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
+      for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        float M = -INFINITY;
+        for (int p = e; p < f; ++p)
+          if (open[p].b >= 0) M = fmaxf(M, stats[p * S::kRows + r].x);
+        float sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = e; p < f; ++p) {
+          if (open[p].b < 0) continue;
+          const float2 ml = stats[p * S::kRows + r];
+          const float w = M == -INFINITY ? 0.f : ex2(ml.x - M);
+          sum = fmaf(w, ml.y, sum);
+          const unsigned char* at = p & 1 ? smem + (p >> 1) * S::kRing : smem + S::kFirst + (p >> 1) * S::kPart;
+          const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + r * D + d);
+          v.x = fmaf(w, x.x, v.x);
+          v.y = fmaf(w, x.y, v.y);
+          v.z = fmaf(w, x.z, v.z);
+          v.w = fmaf(w, x.w, v.w);
+        }
+        const float inv = 1.0f / sum;
+        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+        const float lse = M + lg2(sum);
+        const long long row = (long long)op.b * a.Hq + h0 + r;
+        if (whole && !t.p.row_o) {
+          uint2 w;
+          w.x = pack2<kF16>(v.x, v.y);
+          w.y = pack2<kF16>(v.z, v.w);
+          *reinterpret_cast<uint2*>(a.out + row * D + d) = w;
+          if (a.lse && d == 0) a.lse[row] = lse * 0.693147180559945f;
+        } else {
+          const long long at = whole ? row : (long long)slot * 16 + r;
+          *reinterpret_cast<float4*>((whole ? t.p.row_o : t.p.slot_o) + at * D + d) = v;
+          if (d == 0) (whole ? t.p.row_lse : t.p.slot_lse)[at] = lse;
+        }
       }
     }
+    e = f;
   }
-  const float inv = sum > 0.f ? 1.0f / sum : sum;       // no keys: 0; NaN stays
-#pragma unroll
-  for (int j = 0; j < N; ++j) a.out[row * D + lane * N + j] = kF16 ? f2h(acc[j] * inv) : f2bf(acc[j] * inv);
-  if (a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * 0.693147180559945f;
+  const int any_bad = __syncthreads_or(bad), any_late = __syncthreads_or(late);
+  if (threadIdx.x == 0) report(rep, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
+  // launched beside the prefix's kernel: this grid ends after it, so that the
+  // merge kernel, which waits for this one, finds the parts of both
+  pdl_wait();
 }
 
 template <int D, bool kF16, bool kWide>
-cudaError_t launch(const DecodeArgs& t, const CUtensorMap& k, const CUtensorMap& v, const Report& rep, int splits,
+cudaError_t launch(const DecodeArgs& t, const CUtensorMap& k, const CUtensorMap& v, const Report& rep, bool beside,
                    int grid, cudaStream_t stream) {
   auto kern = attn_decode_kernel<D, kF16, kWide>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+  constexpr size_t smem = Shape<D, kWide>::kSmem;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kThreads, Shape<D>::kSmem, stream>>>(k, v, t, rep);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  const long long rows = (long long)t.a.T * t.a.Hq;
-  return launch_pdl(decode_merge_kernel<D, kF16>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, t, splits,
-                    grid);
+  if (beside) return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, k, v, t, rep);
+  kern<<<grid, kThreads, smem, stream>>>(k, v, t, rep);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_decode(const AttnArgs& a, int splits, const DecodeParts& p, const Report& shape, int num_sms,
+// beside: the kernel before this one on the stream is the prefix's, on which
+// nothing here depends
+cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& shape, int num_sms,
                                cudaStream_t stream) {
   DecodeArgs t{};
   t.a = a;
@@ -493,7 +523,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int splits, const DecodeParts&
   if (t.c < 1.2e-38f) t.c = 1.2e-38f;      // a masked logit of -inf stays one
   t.flip = a.scale < 0 ? 0x80008000u : 0u;
   const int G = a.Hq / a.Hkv;
-  t.chunks = (G + 15) / 16;
+  t.chunks = decode_chunks(a);
   t.p = p;
   CUtensorMap k, v;
   if (!kv_map(&k, a, a.k_cache, a.k, kSlice) || !kv_map(&v, a, a.v_cache, a.v, kSlice)) return cudaErrorInvalidValue;
@@ -501,7 +531,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int splits, const DecodeParts&
   rep.blocks[rep.set] = num_sms;
   const bool wide = G > 8;
 #define DECODE_CASE(DD, F, W) \
-  if (a.D == DD && (a.f16 != 0) == F && wide == W) return launch<DD, F, W>(t, k, v, rep, splits, num_sms, stream);
+  if (a.D == DD && (a.f16 != 0) == F && wide == W) return launch<DD, F, W>(t, k, v, rep, beside, num_sms, stream);
   DECODE_CASE(64, false, false)
   DECODE_CASE(64, false, true)
   DECODE_CASE(64, true, false)

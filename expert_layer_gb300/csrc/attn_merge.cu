@@ -2,54 +2,141 @@
 // result o_i and log2-sum lse_i,
 //   out = sum_i w_i o_i / sum_i w_i,  w_i = 2^{lse_i - max lse},
 //   lse = max lse + log2 sum_i w_i.
-// A warp per row; a part without keys has lse_i = -inf and is not read.
+// A part without keys has lse_i = -inf; its o_i is not used.  The order of the
+// parts is fixed, so the result does not change from run to run.
+//
+// Bound: latency (a row's parts are a few KB, just written).  A block takes a
+// row, its four warps every fourth part each, with their loads in batches.
 #include "attn.h"
+#include "attn_ptx.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;
+
+struct MergeArgs {
+  AttnArgs a;
+  int splits;            // parts in row order: [splits, T * Hq]
+  DecodeParts p;
+  int chunks, grid;      // decode: units per key-value head, blocks of the kernel (0: prefill)
+};
 
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads) attn_merge_kernel(const AttnArgs a, int splits,
-                                                              const float* __restrict__ part_o,
-                                                              const float* __restrict__ part_lse) {
-  constexpr int N = D / 32;
+__global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t) {
+  constexpr int N = D / 32;            // elements per lane
+  __shared__ float s_o[kWarps][D];
+  __shared__ float2 s_ml[kWarps];
   pdl_wait();   // programmatic dependent launch: the parts are complete
-  const int lane = threadIdx.x & 31;
+  const AttnArgs& a = t.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long rows = (long long)a.T * a.Hq;
-  const long long r = (long long)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  if (r >= rows) return;
-  float top = -INFINITY;
-  for (int i = 0; i < splits; ++i) top = fmaxf(top, part_lse[i * rows + r]);
-  float o[N], sum = 0.f;
-#pragma unroll
-  for (int u = 0; u < N; ++u) o[u] = 0.f;
-  if (top != -INFINITY)
-    for (int i = 0; i < splits; ++i) {
-      const float w = exp2f(part_lse[i * rows + r] - top);
-      if (w == 0.f) continue;
-      sum += w;
-      const float* p = part_o + (i * rows + r) * D + lane * N;
-#pragma unroll
-      for (int u = 0; u < N; ++u) o[u] = fmaf(w, p[u], o[u]);
+#pragma unroll 1
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    // blocks c0 .. c0 + own - 1 of the decode kernel hold the row's own keys
+    int c0 = 0, own = 0, r = 0;
+    bool later = false;                // the first of them began the unit after its range's start
+    if (t.grid > 0) {
+      const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), G = a.Hq / a.Hkv;
+      const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
+      r = (h % G) % 16;
+      const long long total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
+      if (n > 0) {
+        const long long ub = b0 + u * n, blocks = decode_blocks(total, t.grid);
+        c0 = (int)(((ub + 1) * blocks - 1) / total);
+        own = (int)(((ub + n) * blocks - 1) / total) - c0 + 1;
+        later = ub >= total * c0 / blocks;
+      }
+      if (t.splits == 0 && own == 1) continue;       // final already
     }
-  const float inv = sum > 0.f ? 1.0f / sum : sum;     // no keys: 0; NaN stays
+    const int parts = t.splits + own;
+    float m = -INFINITY, sum = 0.f, acc[N];
 #pragma unroll
-  for (int u = 0; u < N; ++u) a.out[r * D + lane * N + u] = kF16 ? f2h(o[u] * inv) : f2bf(o[u] * inv);
-  if (a.lse && lane == 0) a.lse[r] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+    for (int j = 0; j < N; ++j) acc[j] = 0.f;
+#pragma unroll 1
+    for (int i0 = warp; i0 < parts; i0 += kWarps * kBatch) {
+      float lse[kBatch], o[kBatch][N];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kWarps;
+        lse[k] = -INFINITY;
+        if (i >= parts) continue;
+        const float *po, *pl;
+        if (i < t.splits || own == 1) {              // the row's own part follows the prefix's
+          const long long at = (long long)i * rows + row;
+          po = t.p.tc_o + at * D;
+          pl = t.p.tc_lse + at;
+        } else {
+          const int c = c0 + i - t.splits;
+          const long long at = (2ll * c + (c == c0 && later ? 1 : 0)) * 16 + r;
+          po = t.p.slot_o + at * D;
+          pl = t.p.slot_lse + at;
+        }
+        lse[k] = *pl;
+#pragma unroll
+        for (int j = 0; j < N; ++j) o[k][j] = po[lane * N + j];
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, lse[k]);
+      if (top == -INFINITY) continue;
+      const float f = ex2(m - top);
+      sum *= f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) acc[j] *= f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (lse[k] == -INFINITY) continue;
+        const float w = ex2(lse[k] - top);
+        sum += w;
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = fmaf(w, o[k][j], acc[j]);
+      }
+      m = top;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) s_o[warp][lane * N + j] = acc[j];
+    if (lane == 0) s_ml[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      float top = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w].x);
+      if (top != -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(s_ml[w].x - top);
+          l = fmaf(f, s_ml[w].y, l);
+          x = fmaf(f, s_o[w][2 * threadIdx.x], x);
+          y = fmaf(f, s_o[w][2 * threadIdx.x + 1], y);
+        }
+      }
+      const float inv = l > 0.f ? 1.0f / l : l;      // no keys: 0; NaN stays
+      reinterpret_cast<uint32_t*>(a.out + row * D)[threadIdx.x] = pack2<kF16>(x * inv, y * inv);
+      if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + lg2(l)) * 0.693147180559945f;
+    }
+    __syncthreads();
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const float* part_o, const float* part_lse,
+cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
                               cudaStream_t stream) {
+  MergeArgs t{};
+  t.a = a;
+  t.splits = splits;
+  t.p = p;
+  t.chunks = decode_chunks(a);
+  t.grid = decode_grid;
   const long long rows = (long long)a.T * a.Hq;
-  const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned grid = (unsigned)(rows < 2048 ? rows : 2048);
   auto kern = a.D == 64 ? (a.f16 ? attn_merge_kernel<64, true> : attn_merge_kernel<64, false>)
                         : (a.f16 ? attn_merge_kernel<128, true> : attn_merge_kernel<128, false>);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, a, splits, part_o, part_lse);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, t);
 }
 
 }  // namespace attn

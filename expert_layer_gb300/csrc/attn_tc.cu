@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
+  pdl_trigger();   // a merge kernel, or the decode kernel beside it, may become resident
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }

@@ -56,6 +56,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a,
   const long long items = (long long)a.T * chunks;
   const int half = a.rot / 2;
   bool bad = false;
+  float wq[8], wk[8];                                  // this lane's norm weights
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    wq[j] = a.q_norm ? a.q_norm[8 * gl + j] : 1.0f;
+    wk[j] = a.k_norm ? a.k_norm[8 * gl + j] : 1.0f;
+  }
   // the loop's trip count is the same for the lanes of a warp: shuffles below
   for (long long base = (long long)blockIdx.x * kGroups; base < items; base += (long long)gridDim.x * kGroups) {
     const long long item = base + threadIdx.x / kLanes;
@@ -116,16 +122,15 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a,
       uint4 o = raw[i];
       float x[8];
       unpack8<kF16>(raw[i], x);
-      const float* w = is_q ? a.q_norm : a.k_norm;
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d, kLanes);
-      if (w && !is_v) {
+      if (is_q ? a.q_norm != nullptr : a.k_norm != nullptr) {
         const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r * w[8 * gl + j];
+        for (int j = 0; j < 8; ++j) x[j] *= r * (is_q ? wq[j] : wk[j]);
       }
       float y[8];
 #pragma unroll
@@ -170,7 +175,10 @@ cudaError_t launch_type(const RopeArgs& a, void* ws, int num_sms, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream) {
-  return a.D == 64 ? launch_type<64, 1>(a, ws, num_sms, stream) : launch_type<128, 1>(a, ws, num_sms, stream);
+  // four heads to a group once that still gives every SM a full set of threads
+  const bool many = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8) / 4 >= 1024ll * num_sms;
+  if (a.D == 64) return many ? launch_type<64, 4>(a, ws, num_sms, stream) : launch_type<64, 1>(a, ws, num_sms, stream);
+  return many ? launch_type<128, 4>(a, ws, num_sms, stream) : launch_type<128, 1>(a, ws, num_sms, stream);
 }
 
 }  // namespace attn

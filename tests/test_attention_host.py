@@ -20,11 +20,11 @@ def lib():
 
 
 def H(ptr=1 << 20, tok=512, head=128):
-    return attention._Heads(ptr, tok, head)
+    return attention._HEADS(ptr, tok, head)
 
 
 def C(k=1 << 20, v=1 << 20, pages=8, size=16):
-    return attention._Cache(k, v, pages, size)
+    return attention._CACHE(k, v, pages, size)
 
 
 FAKE, MIS = P(1 << 20), P((1 << 20) + 2)      # never dereferenced: every case fails on the host
