@@ -35,6 +35,17 @@ __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
+// The same for a converged warp: every lane polls, the verdict is uniform.
+__device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, spin_wait(bar, parity));
+}
+// One lane of a converged warp (the same one every time)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "

@@ -361,88 +361,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else if (warp == kSoftWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
-      uint32_t kv = 0, ni = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      bool ok = true;
-      const uint32_t sQ = smem_u32(smem), sR = sQ + S::kRing;
-      // the addresses of a product's steps are formed where they are used:
-      // hoisted out of the loop they would not fit the registers
-      auto product_s = [&](int x, int s) {
-        uint32_t d = tmem + x * kKeys, q = sQ + x * S::kTileBytes, k = sR + s * S::kTileBytes;
-        asm volatile("" : "+r"(d), "+r"(q), "+r"(k));
-        const uint64_t dq = umma_desc(q), dk = umma_desc(k);
+    // The whole warp runs the loop on warp-uniform values (shuffled from lane
+    // 0), so that descriptors live in uniform registers; one elected lane
+    // issues.  With a single divergent thread each MMA took 70-85 cycles to
+    // issue and the loop, not the tensor core, set the pace.
+    constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sQ = __shfl_sync(0xffffffffu, smem_u32(smem), 0), sR = sQ + S::kRing;
+    int ks = 0;                      // ring stage and phase of the next K tile; V tiles alternate with K tiles
+    uint32_t kph = 0, ni = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+    bool ok = true;
+    auto product_s = [&](int x, int s) {
+      if (elect_one()) {
+        const uint64_t dq = umma_desc(sQ + x * S::kTileBytes), dk = umma_desc(sR + s * S::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4;
-          umma_bf16_id(d, dq + off, dk + off, kIdS, kk ? 1u : 0u);
+          umma_bf16_id(tm + x * kKeys, dq + off, dk + off, kIdS, kk ? 1u : 0u);
         }
         umma_commit(&s_full[x]);
-      };
-      auto product_o = [&](int x, int s, bool add) {
-        uint32_t d = tmem + 2 * kKeys + x * D, p = tmem + x * kKeys, v = sR + s * S::kTileBytes;
-        asm volatile("" : "+r"(d), "+r"(p), "+r"(v));
-        const uint64_t dv = umma_desc_v(v, S::kHalfBytes);
+      }
+      __syncwarp();
+    };
+    auto product_o = [&](int x, int s, uint32_t add) {
+      if (elect_one()) {
+        const uint64_t dv = umma_desc_v(sR + s * S::kTileBytes, S::kHalfBytes);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(d, p + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO, add || kk ? 1u : 0u);
-      };
-      while (ok) {
-        const int slot = ni % kItems;
-        if (!mbar_wait(&it_full[slot], (ni / kItems) & 1)) { ok = false; break; }
-        const Item it = ring[slot];
-        mbar_arrive(&it_empty[slot]);
-        ++ni;
-        if (it.row0 < 0) break;
-        const int n = max(it.n[0], it.n[1]);
-        if (n == 0) continue;
-        const uint32_t kv0 = kv;
-        kv += 2 * n;
-        auto stage = [&](int j, int w) { return (int)((kv0 + 2 * j + w) % NS); };
-        auto full = [&](int j, int w) { return spin_wait(&kv_full[stage(j, w)], ((kv0 + 2 * j + w) / NS) & 1); };
-        ok = full(0, 0);
+          umma_ts(tm + 2 * kKeys + x * D, tm + x * kKeys + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO,
+                  kk ? 1u : add);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
+    };
+    auto next = [&](int s, uint32_t ph, int by, int& s2, uint32_t& ph2) {
+      s2 = s + by;
+      ph2 = ph;
+      if (s2 >= NS) s2 -= NS, ph2 ^= 1;
+    };
+    while (ok) {
+      const int slot = ni % kItems;
+      ok = warp_spin(&it_full[slot], (ni / kItems) & 1);
+      if (!ok) break;
+      const int row0 = __shfl_sync(0xffffffffu, ring[slot].row0, 0);
+      const int n0 = __shfl_sync(0xffffffffu, ring[slot].n[0], 0);
+      const int n1 = __shfl_sync(0xffffffffu, ring[slot].n[1], 0);
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      __syncwarp();
+      ++ni;
+      if (row0 < 0) break;
+      const int n = max(n0, n1);
+      if (n == 0) continue;
+      ok = warp_spin(&kv_full[ks], kph);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ok && it.n[x] > 0) {
-            ok = spin_wait(&q_full[x], nq[x]++ & 1);
-            if (!ok) continue;
-            tc_fence_after();
-            product_s(x, stage(0, 0));
-            if (it.n[x] == 1) umma_commit(&q_empty[x]);
-          }
-        if (!ok) break;
-        umma_commit(&kv_empty[stage(0, 0)]);
-        for (int j = 0; j < n && ok; ++j) {
-          ok = full(j, 1) && (j + 1 >= n || full(j + 1, 0));
-          if (!ok) break;
+      for (int x = 0; x < 2; ++x) {
+        const int nx = x ? n1 : n0;
+        if (!ok || nx == 0) continue;
+        ok = warp_spin(&q_full[x], qph[x]);
+        qph[x] ^= 1;
+        if (!ok) continue;
+        tc_fence_after();
+        product_s(x, ks);
+        if (nx == 1) commit(&q_empty[x]);
+      }
+      if (!ok) break;
+      commit(&kv_empty[ks]);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        int vs, k2;                  // V of this block, K of the next
+        uint32_t vph, k2ph;
+        next(ks, kph, 1, vs, vph);
+        next(ks, kph, 2, k2, k2ph);
+        ok = warp_spin(&kv_full[vs], vph) && (j + 1 >= n || warp_spin(&kv_full[k2], k2ph));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= it.n[x]) continue;
-            ok = spin_wait(&p_full[x], np[x]++ & 1);
-            if (!ok) continue;
-            tc_fence_after();
-            product_o(x, stage(j, 1), j > 0);
-            if (j + 1 < it.n[x]) {
-              product_s(x, stage(j + 1, 0));
-              if (j + 2 == it.n[x]) umma_commit(&q_empty[x]);
-            } else {
-              umma_commit(&o_full[x]);
-            }
+        for (int x = 0; x < 2; ++x) {
+          const int nx = x ? n1 : n0;
+          if (!ok || j >= nx) continue;
+          ok = warp_spin(&p_full[x], pph[x]);
+          pph[x] ^= 1;
+          if (!ok) continue;
+          tc_fence_after();
+          product_o(x, vs, j > 0 ? 1u : 0u);
+          if (j + 1 < nx) {
+            product_s(x, k2);
+            if (j + 2 == nx) commit(&q_empty[x]);
+          } else {
+            commit(&o_full[x]);
           }
-          if (!ok) break;
-          umma_commit(&kv_empty[stage(j, 1)]);
-          if (j + 1 < n) umma_commit(&kv_empty[stage(j + 1, 0)]);
         }
-        if (*(volatile int*)abort_flag) ok = false;
+        if (!ok) break;
+        commit(&kv_empty[vs]);
+        if (j + 1 < n) commit(&kv_empty[k2]);
+        ks = k2;
+        kph = k2ph;
       }
-      if (!ok) {
-        // after a timeout: the MMAs already issued finish before their memory is freed
-        atomicOr(abort_flag, 1);
-        umma_commit(drain);
-        mbar_wait(drain, 0);
-      }
+      if (*(volatile int*)abort_flag) ok = false;
     }
-    __syncwarp();
+    if (!ok) {
+      // after a timeout: the MMAs already issued finish before their memory is freed
+      if (lane == 0) atomicOr(abort_flag, 1);
+      commit(drain);
+      if (lane == 0) mbar_wait(drain, 0);
+      __syncwarp();
+    }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
