@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int s = first; s < last; ++s) {
         const int st = used % kStages;
-        if (!late && !__all_sync(0xffffffffu, spin_wait(&bars[st], (used / kStages) & 1))) late = true;
+        if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true;
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // after a timeout: the loads already issued land before the block exits
     if (late && lane == 0)
       for (uint32_t i = issued > (uint32_t)kStages ? issued - kStages : 0; i < issued; ++i)
-        mbar_wait(&bars[i % kStages], (i / kStages) & 1);
+        spin_wait(&bars[i % kStages], (i / kStages) & 1);
   }
   __syncthreads();
 

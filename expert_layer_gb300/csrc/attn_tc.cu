@@ -9,10 +9,13 @@
 //   m' = max(m, max_j c S_j)       c = scale log2(e)
 //   P = 2^{c S - m'},  l += sum P  fp32; P rounded to the element type for
 //   O += P V                       the second product (A from tensor memory)
-// with out = O / l and lse = (m + log2 l) ln 2 at the end.  The maximum in use
-// may lag the true one by up to 2^8 (P <= 256 in both types, l and O are
-// fp32): only when a row exceeds it by more is O rescaled, which after the
-// first blocks hardly happens.
+// with out = O / l and lse = (m + log2 l) ln 2 at the end.  m is a scale, not
+// the exact maximum: a row takes the maximum of its first block, and P is
+// formed with it from then on, without looking at the logits first.  The sum of
+// P, needed anyway, says when a row has outgrown its scale (2^15: P stays within
+// f16, and bf16 rounds relative to P whatever its size); only then the row's
+// maximum is taken again and l and O are rescaled, which after the first blocks
+// hardly happens.
 #include <cuda.h>
 
 #include "attn.h"
@@ -31,9 +34,10 @@ constexpr int kSoftWarps = 8;       // two tiles x four warps, one row per threa
 constexpr int kThreads = (kSoftWarps + 4) * 32;
 // Registers per thread: 168 at launch (three warpgroups); the softmax
 // warpgroups, which hold a row of 128 logits, draw on the third one's.
-constexpr int kSoftRegs = 216, kLoadRegs = 72;
+constexpr int kSoftRegs = 208, kLoadRegs = 88;
 static_assert(2 * kSoftRegs + kLoadRegs <= 3 * 168, "the shares come from the launch's registers");
-constexpr float kLag = 8.0f;        // log2 of how far the maximum in use may lag
+constexpr int kHalf = kKeys / 2;
+constexpr float kMost = 32768.0f;   // sum of a row's P in half a block that asks for a new maximum
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -44,7 +48,7 @@ struct Shape {
   static constexpr int kStages = D == 128 ? 5 : 10;            // ring of K and V tiles
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
   static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr size_t kSmem = kBars + 1024 + 1024;
+  static constexpr size_t kSmem = kBars + 1024;
 };
 
 struct Item {
@@ -212,34 +216,39 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // ------------------------------------------------------------------ the kernel
 // warps 0-3, 4-7   softmax and epilogue of tile 0 and 1 (thread = row)
 // warp 8           work items, TMA loads of Q, K and V
-// warp 9           issues the MMAs (warps 10, 11 only complete the warpgroup): per key block O0 += P0 V, S0 = Q0 K',
-//                  O1 += P1 V, S1 = Q1 K' (K' the next block), so that each
-//                  tile's softmax runs while the other tile multiplies
+// warps 9, 10      issue the MMAs of tile 0 and 1 (warp 11 only completes the
+//                  warpgroup): per key block O += P V, half by half as P
+//                  comes, then S = Q K' of the next block; one tile's softmax
+//                  runs while the other multiplies.  A barrier costs an issuing warp ~200 cycles even
+//                  when it is complete (the MMAs' operands fill the
+//                  shared-memory pipe), which one warp for both tiles spent with
+//                  the tensor core idle.
 // Tensor memory: S0 | S1 | O0 | O1; P overwrites the first half of its S.
-// One thread issues every MMA, in order: a commit after S(j+1) also covers
-// O += P(j) V, so a softmax warp that has S(j+1) may rescale O without waiting.
+// One thread issues all MMAs of a tile, in order: a commit after S(j+1) also
+// covers O += P(j) V, so a softmax warp that has S(j+1) may rescale O without
+// waiting.
 template <int D, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcAttnArgs t, const Report rep) {
   using S = Shape<D>;
   constexpr int NS = S::kStages;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem =
-      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* kv_empty = kv_full + NS;
   uint64_t* q_full = kv_empty + NS;
   uint64_t* q_empty = q_full + 2;
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* it_full = o_full + 2;
+  uint64_t* o_full = p_full + 4;         // p_full: [tile][half]
+  uint64_t* h_done = o_full + 2;         // [tile]: the product with the first half of a block
+  uint64_t* turn = h_done + 2;           // [tile]: its softmax may begin a block
+  uint64_t* it_full = turn + 2;
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  Item* ring = reinterpret_cast<Item*>(drain + 2);
+  Item* ring = reinterpret_cast<Item*>(drain + 3);
 
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -247,21 +256,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();   // a merge kernel, or the decode kernel beside it, may become resident
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 1); }
+    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
+      mbar_init(&p_full[2 * x], 4);
+      mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&o_full[x], 1);
+      mbar_init(&h_done[x], 1);
+      mbar_init(&turn[x], 4);
     }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], 1); mbar_init(&it_empty[i], kSoftWarps + 1); }
-    mbar_init(drain, 1);
+    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], 1); mbar_init(&it_empty[i], kSoftWarps + 2); }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.row0 = -1;
       }
       const int slot = ni % kItems;
-      if (!warp_wait(&it_empty[slot], ((ni / kItems) & 1) ^ 1)) { ok = false; break; }
+      if (!warp_spin(&it_empty[slot], ((ni / kItems) & 1) ^ 1)) { ok = false; break; }
       if (lane == 0) {
         ring[slot] = it;
         mbar_arrive(&it_full[slot]);
@@ -315,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (ok && it.n[x] > 0) {
-          ok = warp_wait(&q_empty[x], (nq[x] & 1) ^ 1);
+          ok = warp_spin(&q_empty[x], (nq[x] & 1) ^ 1);
           if (ok && lane == 0) {
             mbar_expect_tx(&q_full[x], (uint32_t)(S::kHalves * G * t.tt * 128));
             for (int hh = 0; hh < S::kHalves; ++hh)
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int w = 0; w < 2; ++w, ++kv) {
           const int s = kv % NS;
-          ok = warp_wait(&kv_empty[s], ((kv / NS) & 1) ^ 1);
+          ok = warp_spin(&kv_empty[s], ((kv / NS) & 1) ^ 1);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
           __syncwarp();
@@ -353,43 +366,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       // after a timeout: the loads already issued land before the block exits
       if (lane == 0) {
         atomicOr(abort_flag, 1);
-        for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) mbar_wait(&kv_full[i % NS], (i / NS) & 1);
+        for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) spin_wait(&kv_full[i % NS], (i / NS) & 1);
         for (int x = 0; x < 2; ++x)
-          if (nq[x]) mbar_wait(&q_full[x], (nq[x] - 1) & 1);
+          if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
       }
       __syncwarp();
     }
-    } else if (warp == kSoftWarps + 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop on warp-uniform values (shuffled from lane
-    // 0), so that descriptors live in uniform registers; one elected lane
-    // issues.  With a single divergent thread each MMA took 70-85 cycles to
-    // issue and the loop, not the tensor core, set the pace.
+    } else if (warp <= kSoftWarps + 2) {
+    // ------------------------------------------------------------ MMA issuers
+    // The whole warp runs the loop on values that are uniform to the compiler
+    // (constants, loop counters, results of warp reductions); one elected lane
+    // issues.
     constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t sQ = __shfl_sync(0xffffffffu, smem_u32(smem), 0), sR = sQ + S::kRing;
+    const int x = __reduce_max_sync(0xffffffffu, warp - kSoftWarps - 1);      // tile
+    const uint32_t tS = x * kKeys, tO = 2 * kKeys + x * D;   // all 512 columns: the allocation starts at 0
+    const uint32_t sQ = smem_u32(smem) + x * S::kTileBytes, sR = smem_u32(smem) + S::kRing;
     int ks = 0;                      // ring stage and phase of the next K tile; V tiles alternate with K tiles
-    uint32_t kph = 0, ni = 0, qph[2] = {0, 0}, pph[2] = {0, 0};
+    uint32_t kph = 0, ni = 0, qph = 0, pph = 0;
     bool ok = true;
-    auto product_s = [&](int x, int s) {
+    auto product_s = [&](int s) {
       if (elect_one()) {
-        const uint64_t dq = umma_desc(sQ + x * S::kTileBytes), dk = umma_desc(sR + s * S::kTileBytes);
+        const uint64_t dq = umma_desc(sQ), dk = umma_desc(sR + s * S::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4;
-          umma_bf16_id(tm + x * kKeys, dq + off, dk + off, kIdS, kk ? 1u : 0u);
+          umma_bf16_id(tS, dq + off, dk + off, kIdS, kk ? 1u : 0u);
         }
         umma_commit(&s_full[x]);
       }
       __syncwarp();
     };
-    auto product_o = [&](int x, int s, uint32_t add) {
+    // one half (64 keys) of a block
+    auto product_o = [&](int half, int s, uint32_t add) {
       if (elect_one()) {
         const uint64_t dv = umma_desc_v(sR + s * S::kTileBytes, S::kHalfBytes);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(tm + 2 * kKeys + x * D, tm + x * kKeys + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO,
-                  kk ? 1u : add);
+        for (int i = 0; i < kKeys / 32; ++i) {
+          const int kk = half * (kKeys / 32) + i;
+          umma_ts(tO, tS + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO, kk ? 1u : add);
+        }
+        if (half == 0) umma_commit(&h_done[x]);
       }
       __syncwarp();
     };
@@ -406,26 +422,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = ni % kItems;
       ok = warp_spin(&it_full[slot], (ni / kItems) & 1);
       if (!ok) break;
-      const int row0 = __shfl_sync(0xffffffffu, ring[slot].row0, 0);
-      const int n0 = __shfl_sync(0xffffffffu, ring[slot].n[0], 0);
-      const int n1 = __shfl_sync(0xffffffffu, ring[slot].n[1], 0);
+      const int row0 = __reduce_max_sync(0xffffffffu, ring[slot].row0);
+      const int n0 = __reduce_max_sync(0xffffffffu, ring[slot].n[0]);
+      const int n1 = __reduce_max_sync(0xffffffffu, ring[slot].n[1]);
       if (lane == 0) mbar_arrive(&it_empty[slot]);
       __syncwarp();
       ++ni;
       if (row0 < 0) break;
-      const int n = max(n0, n1);
+      const int n = max(n0, n1), nx = x ? n1 : n0;
       if (n == 0) continue;
       ok = warp_spin(&kv_full[ks], kph);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int nx = x ? n1 : n0;
-        if (!ok || nx == 0) continue;
-        ok = warp_spin(&q_full[x], qph[x]);
-        qph[x] ^= 1;
-        if (!ok) continue;
+      if (ok && nx > 0) {
+        ok = warp_spin(&q_full[x], qph);
+        qph ^= 1;
         tc_fence_after();
-        product_s(x, ks);
-        if (nx == 1) commit(&q_empty[x]);
+        if (ok) product_s(ks);
+        if (ok && nx == 1) commit(&q_empty[x]);
       }
       if (!ok) break;
       commit(&kv_empty[ks]);
@@ -435,20 +447,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t vph, k2ph;
         next(ks, kph, 1, vs, vph);
         next(ks, kph, 2, k2, k2ph);
+        // also for blocks that only the other tile has: a stage is given back
+        // for the phase that it is in
         ok = warp_spin(&kv_full[vs], vph) && (j + 1 >= n || warp_spin(&kv_full[k2], k2ph));
+        if (ok && j < nx) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int nx = x ? n1 : n0;
-          if (!ok || j >= nx) continue;
-          ok = warp_spin(&p_full[x], pph[x]);
-          pph[x] ^= 1;
-          if (!ok) continue;
-          tc_fence_after();
-          product_o(x, vs, j > 0 ? 1u : 0u);
-          if (j + 1 < nx) {
-            product_s(x, k2);
+          for (int half = 0; half < 2; ++half) {
+            if (!ok) continue;
+            ok = warp_spin(&p_full[2 * x + half], pph);
+            tc_fence_after();
+            if (ok) product_o(half, vs, j > 0 ? 1u : 0u);
+          }
+          pph ^= 1;
+          if (ok && j + 1 < nx) {
+            product_s(k2);
             if (j + 2 == nx) commit(&q_empty[x]);
-          } else {
+          } else if (ok) {
             commit(&o_full[x]);
           }
         }
@@ -463,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
       // after a timeout: the MMAs already issued finish before their memory is freed
       if (lane == 0) atomicOr(abort_flag, 1);
-      commit(drain);
-      if (lane == 0) mbar_wait(drain, 0);
+      commit(&drain[x]);
+      if (lane == 0) spin_wait(&drain[x], 0);
       __syncwarp();
     }
     }
@@ -476,52 +490,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int token = row / G, g = row - token * G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + x * kKeys, tO = tmem + lanes + 2 * kKeys + x * D;
-    uint32_t ni = 0, ns = 0, no = 0, kv = 0;
+    uint32_t ni = 0, ns = 0, no = 0, nt = 0, kv = 0;
     bool ok = true;
     while (ok) {
       const int slot = ni % kItems;
-      if (!__all_sync(0xffffffffu, mbar_wait(&it_full[slot], (ni / kItems) & 1))) { ok = false; break; }
+      if (!warp_spin(&it_full[slot], (ni / kItems) & 1)) { ok = false; break; }
       const Item it = ring[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[slot]);
       ++ni;
       if (it.row0 < 0) break;
       const int n = x ? it.n[1] : it.n[0];
+      const int both = min(it.n[0], it.n[1]);      // blocks that the tiles take in turns
       const uint32_t kv0 = kv;
       kv += 2 * max(it.n[0], it.n[1]);
       // keys that this row sees, and that the tile's first token sees
       const int vis = a.causal ? min(it.seen + x * t.tt + token, it.len) : it.len;
       const int vis0 = a.causal ? min(it.seen + x * t.tt, it.len) : it.len;
+      const bool live = token < (x ? it.tok[1] : it.tok[0]);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {
-        if (!__all_sync(0xffffffffu, spin_wait(&s_full[x], ns & 1))) { ok = false; break; }
+        if (!warp_spin(&s_full[x], ns & 1)) { ok = false; break; }
         tc_fence_after();
-        float s[kKeys];
+        // Turns: left alone the two tiles fall into step, with the tensor core
+        // idle while both compute P and the reverse (8192 x 8192 keys, D = 128:
+        // 913 us).  With D = 128, where the MMAs take longer, a tile hands over
+        // when all its P is formed (702 us; after the first half 743), with
+        // D = 64 after the first half (611 us; after both 678).
+        if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
+        // the row's logits in two halves, the second on its way meanwhile
+        float s[2][kHalf];
+        tmem_ld64(tS, s[0]);
+        tmem_wait_ld64(s[0]);
+        tmem_ld64(tS + kHalf, s[1]);
+        const int b = it.b0 + j, lim = vis - b * kKeys;
+        const bool masked = vis0 < (b + 1) * kKeys;
+        auto prepare = [&](int half) {
+          if (t.negate) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * i]));
-        tmem_wait_ld();
-        const int b = it.b0 + j;
-        if (t.negate) {
+            for (int i = 0; i < kHalf; ++i) s[half][i] = -s[half][i];
+          }
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = -s[i];
-        }
-        if (vis0 < (b + 1) * kKeys) {
-          const int lim = vis - b * kKeys;
+            for (int i = 0; i < kHalf; ++i) s[half][i] = half * kHalf + i < lim ? s[half][i] : -INFINITY;
+          }
+        };
+        auto row_max = [&](int half) {
+          float mx[4] = {s[half][0], s[half][1], s[half][2], s[half][3]};
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = i < lim ? s[i] : -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int i = 4; i < kHalf - 4; i += 8)
 #pragma unroll
-        for (int i = 4; i < kKeys; i += 4)
+            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[half][i + k], s[half][i + k + 4]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[i + u]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * t.c;
-        const bool up = top > m + kLag;
-        if (__any_sync(0xffffffffu, up)) {
+          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[half][kHalf - 4 + k]);
+          return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * t.c;
+        };
+        const uint64_t c2 = pair(t.c, t.c);
+        uint32_t p[32];
+        // P of a half with the maximum in use; the sum of the row's
+        auto half_p = [&](int half) {
+          const float off = m == -INFINITY ? 0.f : -m;
+          const uint64_t off2 = pair(off, off);
+          uint64_t sum = 0, sum2 = 0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint64_t y = fma2(pair(s[half][2 * i], s[half][2 * i + 1]), c2, off2);
+            const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+            if (i & 1) sum2 = add2(sum2, pair(p0, p1));
+            else sum = add2(sum, pair(p0, p1));
+            p[i] = pack2<kF16>(p0, p1);
+          }
+          sum = add2(sum, sum2);
+          return lo(sum) + hi(sum);
+        };
+        // A new maximum for the rows that need one: l and O to its scale
+        auto raise = [&](float top, bool need, bool has_o) {
+          const bool up = need && top > m;
           const float f = up ? ex2(m - top) : 1.0f;            // m = -inf: 0
           if (up) m = top;
           l *= f;
-          if (j > 0) {
+          if (has_o) {
 #pragma unroll 1
             for (int i = 0; i < D; i += 16) {
               uint32_t o[16];
@@ -532,30 +580,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(tO + i, o);
             }
           }
+        };
+        prepare(0);
+        float sum = j > 0 ? half_p(0) : 0.f;
+        bool need = live && (sum > kMost || (m == -INFINITY && lim > 0));
+        if (j == 0 || __any_sync(0xffffffffu, need)) {
+          tmem_wait_ld64(s[1]);
+          prepare(1);
+          raise(fmaxf(row_max(0), row_max(1)), j == 0 || need, j > 0);
+          sum = half_p(0);
+        } else {
+          tmem_wait_ld64(s[1]);
+          prepare(1);
         }
-        const float off = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float p0 = ex2(fmaf(s[64 * h + 2 * i], t.c, -off));
-            const float p1 = ex2(fmaf(s[64 * h + 2 * i + 1], t.c, -off));
-            sum[2 * (i & 1)] += p0;
-            sum[2 * (i & 1) + 1] += p1;
-            p[i] = pack2<kF16>(p0, p1);
-          }
-          tmem_st32(tS + 32 * h, p);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += sum;
+        tmem_st32(tS, p);
         // The block that the keys end in: rows of its V tile past the end hold
         // other data (or NaN), which a weight of 0 does not silence: clear them.
-        // The first tile that multiplies the block does it.
+        // Each tile that multiplies the block does it.
         const int tail = it.len & (kKeys - 1);
-        if (tail && b == it.len / kKeys && (x == 0 || j >= it.n[0])) {
+        if (tail && b == it.len / kKeys) {
           const uint32_t i = kv0 + 2 * j + 1;
-          if (!__all_sync(0xffffffffu, spin_wait(&kv_full[i % NS], (i / NS) & 1))) { ok = false; break; }
+          if (!warp_spin(&kv_full[i % NS], (i / NS) & 1)) { ok = false; break; }
           if (row >= tail) {
             uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + row * 128);
 #pragma unroll
@@ -567,12 +613,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[2 * x]);
+        if (D == 64 && j < both && lane == 0) mbar_arrive(&turn[x ^ 1]);
+        sum = half_p(1);
+        if (D != 64 && j < both && lane == 0) mbar_arrive(&turn[x ^ 1]);
+        nt += j < both;
+        need = live && sum > kMost;
+        if (__any_sync(0xffffffffu, need)) {
+          // the product with the first half may be adding to O
+          if (!warp_spin(&h_done[x], ns & 1)) { ok = false; break; }
+          tc_fence_after();
+          raise(row_max(1), need, true);
+          sum = half_p(1);
+        }
+        l += sum;
+        tmem_st32(tS + 32, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * x + 1]);
       }
       if (!ok) break;
-      if (n > 0 && !__all_sync(0xffffffffu, spin_wait(&o_full[x], no++ & 1))) { ok = false; break; }
+      if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
       tc_fence_after();
-      const bool live = token < (x ? it.tok[1] : it.tok[0]);
       const long long out_row = ((long long)(it.row0 + x * t.tt + token)) * a.Hq + it.head * G + g;
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;     // l is NaN: so is the row
       if (t.part_o) {
@@ -624,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) report(rep, (any ? kStatusBounds : 0) | (*abort_flag ? kStatusTimeout : 0));
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
   }
