@@ -32,8 +32,8 @@ template <int D, bool kWide>
 struct Shape {
   static constexpr int kRows = kWide ? 16 : 8;                     // heads of a unit
   static constexpr int kHalves = D / 64;
-  static constexpr int kHalfBytes = kSlice * 128;                  // 2 KB: 16 keys x 64 elements
-  static constexpr int kTileBytes = kHalves * kHalfBytes;          // K or V of a slice
+  static constexpr int kGroup = kHalves * 1024;                    // 8 keys: kHalves swizzle atoms
+  static constexpr int kTileBytes = 2 * kGroup;                    // K or V of a slice
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = D == 64 ? 5 : kWide ? 2 : 3;      // slices in flight per warp
   static constexpr int kRing = kStages * kStageBytes;              // of one warp
@@ -247,12 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
         unsigned char* dst = ring + st * S::kStageBytes;
         mbar_expect_tx(&bars[st], S::kStageBytes);
-#pragma unroll
-        for (int hh = 0; hh < S::kHalves; ++hh)
-          tma_load_4d(dst + hh * S::kHalfBytes, &tmK, hh * 64, row, hk, page, &bars[st]);
-#pragma unroll
-        for (int hh = 0; hh < S::kHalves; ++hh)
-          tma_load_4d(dst + S::kTileBytes + hh * S::kHalfBytes, &tmV, hh * 64, row, hk, page, &bars[st]);
+        tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+        tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
       }
       ++issued;
       ++ld_slice;
@@ -265,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // V transposed: the same with keys fastest; rows are swizzled by key % 8
     const int k_row = (lane & 7) + ((lane & 16) >> 1), k_col = (lane >> 3) & 1;
     const int v_row = (lane & 7) + (lane & 8), v_col = lane >> 4;
+    const int k_at = (k_row >> 3) * S::kGroup + (k_row & 7) * 128, v_at = (v_row >> 3) * S::kGroup + (v_row & 7) * 128;
     const int quad = lane & 3, gq = lane >> 2;
     uint32_t used = 0;
     auto load_q = [&](const Cursor& c, uint32_t (&q)[D / 16][2 * kRowSets]) {
@@ -310,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t r[4];
           const int chunk = (kk & 3) * 2 + k_col;
-          ldsm4(kb + (kk >> 2) * S::kHalfBytes + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), r);
+          ldsm4(kb + (kk >> 2) * 1024 + k_at + ((chunk ^ (k_row & 7)) << 4), r);
           const uint32_t a1 = kWide ? q[kk][kRowSets - 1] : 0u, a3 = kWide ? q[kk][2 * kRowSets - 1] : 0u;
           mma<kF16>(sc[0], q[kk][0], a1, q[kk][kRowSets], a3, r[0], r[1]);
           mma<kF16>(sc[1], q[kk][0], a1, q[kk][kRowSets], a3, r[2], r[3]);
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < D / 16; ++i) {
           uint32_t r[4];
           const int chunk = (i & 3) * 2 + v_col;
-          ldsm4_t(vb + (i >> 2) * S::kHalfBytes + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), r);
+          ldsm4_t(vb + (i >> 2) * 1024 + v_at + ((chunk ^ (v_row & 7)) << 4), r);
           mma<kF16>(o[2 * i], p[0], p[1], p[2], p[3], r[0] & keep0, r[1] & keep1);
           mma<kF16>(o[2 * i + 1], p[0], p[1], p[2], p[3], r[2] & keep0, r[3] & keep1);
         }
@@ -526,7 +523,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts
   t.chunks = decode_chunks(a);
   t.p = p;
   CUtensorMap k, v;
-  if (!kv_map(&k, a, a.k_cache, a.k, kSlice) || !kv_map(&v, a, a.v_cache, a.v, kSlice)) return cudaErrorInvalidValue;
+  if (!pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice)) return cudaErrorInvalidValue;
   Report rep = shape;
   rep.blocks[rep.set] = num_sms;
   const bool wide = G > 8;

@@ -40,10 +40,15 @@ constexpr int kHalf = kKeys / 2;
 constexpr float kMost = 32768.0f;   // sum of a row's P in half a block that asks for a new maximum
 constexpr uint32_t kTmemCols = 512;
 
-template <int D>
+// Tiles in shared memory: rows of 64 elements in 1 KB swizzle atoms of 8.  Q,
+// and K and V from packed rows: one column of atoms after the other.  K and V
+// from pages: atoms of the same 8 rows side by side (pages_map).
+template <int D, bool kPaged>
 struct Shape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide swizzled columns
-  static constexpr int kHalfBytes = kRows * 128;               // 16 KB
+  static constexpr int kHalfBytes = kRows * 128;               // 16 KB: a column
+  static constexpr int kColumn = kPaged ? 1024 : kHalfBytes;   // from a K or V column to the next
+  static constexpr int kGroup = kPaged ? kHalves * 1024 : 1024;   // from 8 rows of K or V to the next
   static constexpr int kTileBytes = kHalves * kHalfBytes;      // a Q, K or V tile
   static constexpr int kStages = D == 128 ? 5 : 10;            // ring of K and V tiles
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
@@ -99,17 +104,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Keys [keys][D] as the B operand of S = Q K^T: K-major, 128-byte swizzle,
+// groups of 8 keys `group` bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_k(uint32_t saddr, uint32_t group) {
+  return (umma_desc(saddr) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)(group >> 4) << 32;
+}
 // Values [keys][D] as the B operand of O += P V: D-major ("transposed"),
-// 128-byte swizzle; the next 64 columns of D one half tile on (leading
-// offset), the next 8 keys 1024 bytes on (stride offset).
-__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr, uint32_t half_bytes) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
-  d |= (uint64_t)(half_bytes >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// 128-byte swizzle; the next 64 columns of D `column` bytes on (leading
+// offset), the next 8 keys `group` bytes on (stride offset).
+__device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr, uint32_t column, uint32_t group) {
+  return (umma_desc_k(saddr, group) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(column >> 4) << 16;
 }
 __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accum) {
@@ -227,11 +231,11 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // One thread issues all MMAs of a tile, in order: a commit after S(j+1) also
 // covers O += P(j) V, so a softmax warp that has S(j+1) may rescale O without
 // waiting.
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TcAttnArgs t, const Report rep) {
-  using S = Shape<D>;
+  using S = Shape<D, kPaged>;
   constexpr int NS = S::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
@@ -314,11 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (end) break;
       const int n = max(it.n[0], it.n[1]);
       const int32_t* list = nullptr;
-      if (a.page_table) list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
+      if (kPaged) list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
       // page of this lane's box in block b (lanes 0 .. boxes-1)
       auto page_of = [&](int b) {
         const int key = b * kKeys + lane * t.box;
-        if (!list || lane >= boxes || key >= it.len) return 0;
+        if (!kPaged || lane >= boxes || key >= it.len) return 0;
         const int p = list[key >> a.page_shift];
         if ((unsigned)p < (unsigned)a.pages) return p;
         bad = true;
@@ -350,12 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
           __syncwarp();
           if (lane < nbox) {
-            unsigned char* dst = smem + S::kRing + s * S::kTileBytes + lane * t.box * 128;
+            unsigned char* dst = smem + S::kRing + s * S::kTileBytes;
             const int key = b * kKeys + lane * t.box;
-            const int row = list ? key & ((1 << a.page_shift) - 1) : k0 + key;
-            for (int hh = 0; hh < S::kHalves; ++hh)
-              tma_load_4d(dst + hh * S::kHalfBytes, w ? &tmV : &tmK, hh * 64, row, it.head, list ? page : 0,
-                          &kv_full[s]);
+            if (kPaged) {
+              tma_load_5d(dst + lane * (t.box / 8) * S::kGroup, w ? &tmV : &tmK, 0, 0, 0,
+                          (key & ((1 << a.page_shift) - 1)) / 8, page * a.Hkv + it.head, &kv_full[s]);
+            } else {
+#pragma unroll
+              for (int hh = 0; hh < S::kHalves; ++hh)
+                tma_load_3d(dst + hh * S::kHalfBytes, w ? &tmV : &tmK, hh * 64, k0 + key, it.head, &kv_full[s]);
+            }
           }
         }
         page = next;
@@ -386,12 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto product_s = [&](int s) {
       if (elect_one()) {
-        const uint64_t dq = umma_desc(sQ), dk = umma_desc(sR + s * S::kTileBytes);
+        const uint64_t dq = umma_desc(sQ), dk = umma_desc_k(sR + s * S::kTileBytes, S::kGroup);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4;
-          umma_bf16_id(tS, dq + off, dk + off, kIdS, kk ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_id(tS, dq + (((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4),
+                       dk + (((kk / 4) * S::kColumn + (kk % 4) * 32) >> 4), kIdS, kk ? 1u : 0u);
         umma_commit(&s_full[x]);
       }
       __syncwarp();
@@ -399,11 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one half (64 keys) of a block
     auto product_o = [&](int half, int s, uint32_t add) {
       if (elect_one()) {
-        const uint64_t dv = umma_desc_v(sR + s * S::kTileBytes, S::kHalfBytes);
+        const uint64_t dv = umma_desc_v(sR + s * S::kTileBytes, S::kColumn, S::kGroup);
 #pragma unroll
         for (int i = 0; i < kKeys / 32; ++i) {
           const int kk = half * (kKeys / 32) + i;
-          umma_ts(tO, tS + kk * 8, dv + ((kk * 16 * 128) >> 4), kIdO, kk ? 1u : add);
+          umma_ts(tO, tS + kk * 8, dv + ((kk * 2 * S::kGroup) >> 4), kIdO, kk ? 1u : add);
         }
         if (half == 0) umma_commit(&h_done[x]);
       }
@@ -603,10 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t i = kv0 + 2 * j + 1;
           if (!warp_spin(&kv_full[i % NS], (i / NS) & 1)) { ok = false; break; }
           if (row >= tail) {
-            uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + row * 128);
+            uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + (row / 8) * S::kGroup +
+                                                (row % 8) * 128);
 #pragma unroll
-            for (int u = 0; u < S::kHalves * 8; ++u)
-              v[(u / 8) * (S::kHalfBytes / 16) + u % 8] = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < S::kHalves * 8; ++u) v[(u / 8) * (S::kColumn / 16) + u % 8] = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
@@ -696,25 +703,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ host side
 // 3-D map over the queries: {D, head, token}; box {64, G, tt}.
 bool q_map(CUtensorMap* m, const AttnArgs& a, int tt) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
   const cuuint64_t strides[2] = {a.q.head * 2ull, a.q.tok * 2ull};
   const cuuint32_t box[3] = {64, (cuuint32_t)(a.Hq / a.Hkv), (cuuint32_t)tt};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a.q.data), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(m, a.q.data, 3, dims, strides, box);
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPaged>
 cudaError_t launch(const TcAttnArgs& t, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    const Report& rep, int grid, cudaStream_t stream) {
-  auto kern = attn_tc_kernel<D, kF16>;
-  const cudaError_t err =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape<D>::kSmem);
+  auto kern = attn_tc_kernel<D, kF16, kPaged>;
+  constexpr size_t smem = Shape<D, kPaged>::kSmem;
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kThreads, Shape<D>::kSmem, stream>>>(q, k, v, t, rep);
+  kern<<<grid, kThreads, smem, stream>>>(q, k, v, t, rep);
   return cudaGetLastError();
 }
 
@@ -754,15 +756,27 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   if (t.c < 1.2e-38f) t.c = 1.2e-38f;
   t.part_o = part_o;
   t.part_lse = part_lse;
+  const bool paged = a.page_table != nullptr;
   CUtensorMap q, k, v;
-  if (!q_map(&q, a, t.tt) || !kv_map(&k, a, a.k_cache, a.k, t.box) || !kv_map(&v, a, a.v_cache, a.v, t.box))
+  if (!q_map(&q, a, t.tt)) return cudaErrorInvalidValue;
+  if (paged ? !pages_map(&k, a.k_cache, a, t.box) || !pages_map(&v, a.v_cache, a, t.box)
+            : !rows_map(&k, a.k, a, a.Tk, a.Hkv, kKeys) || !rows_map(&v, a.v, a, a.Tk, a.Hkv, kKeys))
     return cudaErrorInvalidValue;
   const int grid = tc_grid(a, splits, num_sms);
   Report rep = shape;
   rep.blocks[rep.set] = grid;
-  if (a.D == 64)
-    return a.f16 ? launch<64, true>(t, q, k, v, rep, grid, stream) : launch<64, false>(t, q, k, v, rep, grid, stream);
-  return a.f16 ? launch<128, true>(t, q, k, v, rep, grid, stream) : launch<128, false>(t, q, k, v, rep, grid, stream);
+#define TC_CASE(DD, F, P) \
+  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, rep, grid, stream);
+  TC_CASE(64, false, false)
+  TC_CASE(64, false, true)
+  TC_CASE(64, true, false)
+  TC_CASE(64, true, true)
+  TC_CASE(128, false, false)
+  TC_CASE(128, false, true)
+  TC_CASE(128, true, false)
+  TC_CASE(128, true, true)
+#undef TC_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace attn
