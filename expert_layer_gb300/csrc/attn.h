@@ -19,7 +19,7 @@ namespace attn {
 // that no set of kStatus* bits can have.
 constexpr int kHeaderMagic = 0x41540000;
 constexpr int kFlagSets = 2;           // kernels of one call that report
-constexpr int kFlagsPerSet = 4096;     // blocks of one reporting kernel
+constexpr int kFlagsFirst = 2048;      // blocks of set 0; those of set 1 follow, as many as a shape can have
 struct Header {
   int magic;
   int blocks[kFlagSets];               // words in use of each set
@@ -38,7 +38,6 @@ struct Layout {
 };
 
 inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
-  (void)Hkv;
   Layout L{};
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t r = o; o = align256(o + bytes); return r; };
@@ -47,7 +46,9 @@ inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long 
   if (rows < single) rows = single;
   rows += single;                            // decode: one part more for each row's own keys
   L.hdr = take(sizeof(Header));
-  L.flags = take(sizeof(int) * kFlagSets * kFlagsPerSet);
+  const long long per = 2 * (128 / (Hq / Hkv));               // tokens of an attn_tc.cu block
+  const long long items = (T / per + n_seq + 1) * Hkv;
+  L.flags = take(sizeof(int) * (kFlagsFirst + (items > kMaxBlocks ? items : kMaxBlocks)));
   L.part_o = take(sizeof(float) * (size_t)rows * D);
   L.part_lse = take(sizeof(float) * (size_t)rows);
   L.slot_o = take(sizeof(float) * 2 * kMaxBlocks * 16 * D);
@@ -68,12 +69,12 @@ struct Report {
   int blocks[kFlagSets];
 };
 
-// Every block of a reporting kernel calls this once (one thread), whatever it
-// found: the words of a call are complete when its kernels are.
-__device__ __forceinline__ void report(const Report& r, int bits) {
+// Every block of a reporting kernel does this (one thread), whatever it found:
+// the words of a call are complete when its kernels are.
+__device__ __forceinline__ void report(const Report& r, int block, int bits) {
   int* flags = reinterpret_cast<int*>(reinterpret_cast<char*>(r.ws) + sizeof(Header));
-  flags[r.set * kFlagsPerSet + blockIdx.x] = bits;
-  if (blockIdx.x == 0) {
+  flags[r.set * kFlagsFirst + block] = bits;
+  if (block == 0) {
     Header* h = reinterpret_cast<Header*>(r.ws);
     h->magic = kHeaderMagic;
     for (int i = 0; i < kFlagSets; ++i) h->blocks[i] = r.blocks[i];
@@ -136,9 +137,9 @@ inline TcPlan tc_plan(const AttnArgs& a) {
 // Parts that a call splits each row's keys into (1: none, the result is final)
 constexpr int kBlocksPerSplit = 4;
 int tc_splits(const AttnArgs& a, int num_sms);
-int tc_grid(const AttnArgs& a, int splits, int num_sms);
+int tc_items(const AttnArgs& a, int splits);      // blocks of the grid; -1: too many
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& rep,
-                           int num_sms, cudaStream_t stream);
+                           cudaStream_t stream);
 
 // attn_decode.cu -- one token per sequence.  Parts of rows in the workspace:
 // per row (tc_*: `splits` parts of the prefix [splits, T * Hq], then the row's

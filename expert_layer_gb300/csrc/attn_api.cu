@@ -18,12 +18,15 @@ int read_flags(const void* workspace) {
   if (cudaMemcpy(&h, workspace, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
   int bits = 0;
   for (int s = 0; s < kFlagSets; ++s) {
-    int n = h.blocks[s];
-    if (n < 0 || n > kFlagsPerSet) return -1;
-    int words[kFlagsPerSet];
-    const char* at = static_cast<const char*>(workspace) + sizeof(Header) + sizeof(int) * (size_t)s * kFlagsPerSet;
-    if (n > 0 && cudaMemcpy(words, at, sizeof(int) * n, cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
-    for (int i = 0; i < n; ++i) bits |= words[i];
+    if (h.blocks[s] < 0) return -1;
+    const int* at = reinterpret_cast<const int*>(static_cast<const char*>(workspace) + sizeof(Header)) + s * kFlagsFirst;
+    int words[1024];
+    for (int done = 0; done < h.blocks[s];) {
+      const int n = h.blocks[s] - done < 1024 ? h.blocks[s] - done : 1024;
+      if (cudaMemcpy(words, at + done, sizeof(int) * n, cudaMemcpyDeviceToHost) != cudaSuccess) return -1;
+      for (int i = 0; i < n; ++i) bits |= words[i];
+      done += n;
+    }
   }
   return bits;
 }
@@ -109,16 +112,17 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
   p.slot_o = ws_ptr<float>(ws, L.slot_o);
   p.slot_lse = ws_ptr<float>(ws, L.slot_lse);
   p.base = ws_ptr<long long>(ws, L.base);
-  Report rep{ws, 0, {0, sms}};
+  Report rep{ws, 0, {sms, 0}};
   int splits = 0;
   if (a.prefix_len > 0) {
     splits = tc_splits(a, sms);
-    rep.blocks[0] = tc_grid(a, splits, sms);
-    ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, sms, s)));
+    rep.set = 1;
+    rep.blocks[1] = tc_items(a, splits);
+    ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, s)));
     p.row_o = p.tc_o + (long long)splits * a.T * a.Hq * a.D;
     p.row_lse = p.tc_lse + (long long)splits * a.T * a.Hq;
   }
-  rep.set = 1;
+  rep.set = 0;
   ATTN_TRY(cuda_status(launch_attn_decode(a, splits > 0, p, rep, sms, s)));
   return cuda_status(launch_attn_merge(a, splits, p, sms, s));
 }
@@ -141,14 +145,14 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sms > kMaxBlocks) sms = kMaxBlocks;
-  const Report rep{workspace, 0, {0, 0}};
+  const Report rep{workspace, 1, {0, 0}};
   if (!a.q_starts) return run_decode(a, L, workspace, sms, s);
   const int splits = tc_splits(a, sms);
-  if (splits == 1) return cuda_status(launch_attn_tc(a, 1, nullptr, nullptr, rep, sms, s));
+  if (splits == 1) return cuda_status(launch_attn_tc(a, 1, nullptr, nullptr, rep, s));
   DecodeParts p{};
   p.tc_o = ws_ptr<float>(workspace, L.part_o);
   p.tc_lse = ws_ptr<float>(workspace, L.part_lse);
-  ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, sms, s)));
+  ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, s)));
   return cuda_status(launch_attn_merge(a, splits, p, 0, s));
 }
 

@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     e = f;
   }
   const int any_bad = __syncthreads_or(bad), any_late = __syncthreads_or(late);
-  if (threadIdx.x == 0) report(rep, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
+  if (threadIdx.x == 0) report(rep, blockIdx.x, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
   // launched beside the prefix's kernel: this grid ends after it, so that the
   // merge kernel, which waits for this one, finds the parts of both
   pdl_wait();

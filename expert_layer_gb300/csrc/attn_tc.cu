@@ -30,6 +30,7 @@ using namespace tcx;
 constexpr int kRows = 128;          // rows of a tile
 constexpr int kKeys = 128;          // keys of a block
 constexpr int kItems = 4;           // ring of work items
+constexpr int kAskAhead = 3;        // key blocks before an item's end at which the next one is asked for
 constexpr int kSoftWarps = 8;       // two tiles x four warps, one row per thread
 constexpr int kThreads = (kSoftWarps + 4) * 32;
 // Registers per thread: 168 at launch (three warpgroups); the softmax
@@ -50,9 +51,11 @@ struct Shape {
   static constexpr int kColumn = kPaged ? 1024 : kHalfBytes;   // from a K or V column to the next
   static constexpr int kGroup = kPaged ? kHalves * 1024 : 1024;   // from 8 rows of K or V to the next
   static constexpr int kTileBytes = kHalves * kHalfBytes;      // a Q, K or V tile
-  static constexpr int kStages = D == 128 ? 5 : 10;            // ring of K and V tiles
+  // ring of K and V tiles: 8192 causal with 3, 4, 5 stages of 32 KB: 440, 354, 358 us
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
-  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kOut = kRing + kStages * kTileBytes;    // 32 rows of 128 bytes per softmax warp
+  static constexpr int kBars = kOut + kSoftWarps * 32 * 128;
   static constexpr size_t kSmem = kBars + 1024;
 };
 
@@ -69,7 +72,7 @@ struct Item {
 
 struct TcAttnArgs {
   AttnArgs a;
-  int tt, slots, splits, items;
+  int tt, slots, splits;
   int box;                       // rows of a K / V box
   float c;                       // |scale| log2 e, > 0
   int negate;                    // scale < 0
@@ -198,12 +201,12 @@ __device__ __forceinline__ bool make_item(const TcAttnArgs& t, int idx, Item& it
   return true;
 }
 
-// Index arrays of the call, checked once (block 0): what is out of order is
-// reported here and skipped or clamped where it is used.
+// Index arrays of the call, checked once (by the warp that has item 0): what is
+// out of order is reported here and skipped or clamped where it is used.
 __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
   bool bad = false;
   if (a.q_starts)
-    for (int s = threadIdx.x; s < a.n_seq; s += kThreads) {
+    for (int s = threadIdx.x & 31; s < a.n_seq; s += 32) {
       const int q0 = a.q_starts[s], q1 = a.q_starts[s + 1];
       bad |= q0 < 0 || q1 < q0 || q1 > a.T;
       if (!a.page_table) {
@@ -250,9 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* it_full = turn + 2;
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* clc = drain + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clc + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  Item* ring = reinterpret_cast<Item*>(drain + 3);
+  Item* ring = reinterpret_cast<Item*>(clc + 2);
+  uint4* answer = reinterpret_cast<uint4*>(smem + S::kBars + 1024 - 16);
 
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -274,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], 1); mbar_init(&it_empty[i], kSoftWarps + 2); }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
+    mbar_init(clc, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  bool bad = blockIdx.x == 0 && bad_arrays(a);
+  bool bad = false;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -296,14 +302,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kv = 0, nq[2] = {0, 0}, ni = 0;    // loads issued, items published
     bool ok = true;
     const int boxes = kKeys / t.box;            // boxes of a full K or V tile (per 64 columns)
-    for (int r = 0; ok; ++r) {
-      // every other round in reverse: the blocks' sums of work stay close
-      const long long idx = (long long)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const bool end = (long long)r * gridDim.x >= t.items;
+    // The grid has a block per item; a running block takes over blocks that have
+    // not started (cluster launch control), so the items balance themselves.
+    // It asks for the next one while the last loads of an item are issued.
+    int idx = blockIdx.x;
+    uint32_t asked = 0;
+    auto ask = [&]() {
+      if (lane == 0) {
+        mbar_expect_tx(clc, 16);
+        asm volatile(
+            "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                smem_u32(answer)),
+            "r"(smem_u32(clc))
+            : "memory");
+      }
+      ++asked;
+    };
+    auto taken = [&]() {                          // the block asked for, -1: none is left
+      ok = warp_spin(clc, (asked - 1) & 1);
+      int next = -1;
+      asm volatile(
+          "{\n .reg .b128 r;\n .reg .pred p;\n .reg .b32 y, z, w;\n ld.shared.b128 r, [%1];\n"
+          " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+          " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n}\n"
+          : "+r"(next)
+          : "r"(smem_u32(answer))
+          : "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      return ok ? next : -1;
+    };
+    while (ok) {
+      const bool end = idx < 0;
       Item it;
       int seq = 0, k0 = 0;
       if (!end) {
-        if (idx >= t.items || !make_item(t, (int)idx, it, seq, k0)) continue;
+        if (idx != (int)blockIdx.x && lane == 0) report(rep, idx, 0);
+        if (idx == 0) bad |= bad_arrays(a);
+        if (!make_item(t, idx, it, seq, k0)) {
+          ask();
+          idx = taken();
+          continue;
+        }
       } else {
         it = Item{};
         it.row0 = -1;
@@ -329,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return 0;
       };
       int page = n > 0 ? page_of(it.b0) : 0;
+      if (n <= kAskAhead) ask();
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if (ok && it.n[x] > 0) {
@@ -344,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n && ok; ++j) {
         const int b = it.b0 + j;
         const int next = j + 1 < n ? page_of(b + 1) : 0;
+        if (j > 0 && n - j == kAskAhead) ask();
         // boxes that hold keys of the sequence; the rest of the tile is not read
         const int nbox = min(boxes, (it.len - b * kKeys + t.box - 1) / t.box);
 #pragma unroll 1
@@ -369,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         page = next;
       }
       if (*(volatile int*)abort_flag) ok = false;
+      if (ok) idx = taken();
     }
     if (!ok) {
       // after a timeout: the loads already issued land before the block exits
       if (lane == 0) {
         atomicOr(abort_flag, 1);
+        if (asked) spin_wait(clc, (asked - 1) & 1);
         for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) spin_wait(&kv_full[i % NS], (i / NS) & 1);
         for (int x = 0; x < 2; ++x)
           if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
@@ -643,46 +687,60 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
       tc_fence_after();
-      const long long out_row = ((long long)(it.row0 + x * t.tt + token)) * a.Hq + it.head * G + g;
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;     // l is NaN: so is the row
+      // A thread's row would go out in 16-byte pieces, each in a line of its
+      // own: 128 bytes of every row pass through shared memory (swizzled by
+      // row), and eight lanes then write a row's 128 bytes.
+      unsigned char* stage = smem + S::kOut + warp * 32 * 128;
+      const int at = live ? token * a.Hq + g : -1;              // row's place after the tile's first
+      const long long first = (long long)(it.row0 + x * t.tt) * a.Hq + it.head * G;
+      auto put = [&](int unit, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v; };
+      auto write = [&](unsigned char* out, long long row_bytes) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), to = __shfl_sync(0xffffffffu, at, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(out + (first + to) * row_bytes + (lane & 7) * 16) = v;
+        }
+        __syncwarp();
+      };
       if (t.part_o) {
-        const long long part = (long long)it.split * a.T * a.Hq + out_row;
-        if (live) t.part_lse[part] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
-        if (n > 0)
+        const long long part = (long long)it.split * a.T * a.Hq;
+        if (live) t.part_lse[part + first + at] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
+        if (n > 0)                       // a part without keys is not read
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             uint32_t o[32];
             tmem_ld32(tO + i, o);
             tmem_wait_ld();
-            if (live)
 #pragma unroll
-              for (int u = 0; u < 32; u += 4)
-                *reinterpret_cast<float4*>(t.part_o + part * D + i + u) =
-                    make_float4(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv,
-                                __uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
+            for (int u = 0; u < 8; ++u)
+              put(u, make_uint4(__float_as_uint(__uint_as_float(o[4 * u]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
+                                __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv)));
+            write(reinterpret_cast<unsigned char*>(t.part_o + part * D + i), D * 4);
           }
       } else {
-        if (live && a.lse) a.lse[out_row] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
+        if (live && a.lse) a.lse[first + at] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          uint32_t o[32];
+        for (int i = 0; i < D; i += 64) {
+          float o[64];
           if (n > 0) {
-            tmem_ld32(tO + i, o);
-            tmem_wait_ld();
+            tmem_ld64(tO + i, o);
+            tmem_wait_ld64(o);
           } else {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = 0;
+            for (int u = 0; u < 64; ++u) o[u] = 0.f;
           }
-          if (live)
 #pragma unroll
-            for (int u = 0; u < 32; u += 8) {
-              uint4 w;
-              w.x = pack2<kF16>(__uint_as_float(o[u]) * inv, __uint_as_float(o[u + 1]) * inv);
-              w.y = pack2<kF16>(__uint_as_float(o[u + 2]) * inv, __uint_as_float(o[u + 3]) * inv);
-              w.z = pack2<kF16>(__uint_as_float(o[u + 4]) * inv, __uint_as_float(o[u + 5]) * inv);
-              w.w = pack2<kF16>(__uint_as_float(o[u + 6]) * inv, __uint_as_float(o[u + 7]) * inv);
-              *reinterpret_cast<uint4*>(a.out + out_row * D + i + u) = w;
-            }
+          for (int u = 0; u < 8; ++u)
+            put(u, make_uint4(pack2<kF16>(o[8 * u] * inv, o[8 * u + 1] * inv),
+                              pack2<kF16>(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                              pack2<kF16>(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                              pack2<kF16>(o[8 * u + 6] * inv, o[8 * u + 7] * inv)));
+          write(reinterpret_cast<unsigned char*>(a.out + i), D * 2);
         }
       }
       tc_fence_before();
@@ -693,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   const int any = __syncthreads_or(bad);
-  if (threadIdx.x == 0) report(rep, (any ? kStatusBounds : 0) | (*abort_flag ? kStatusTimeout : 0));
+  if (threadIdx.x == 0) report(rep, blockIdx.x, (any ? kStatusBounds : 0) | (*abort_flag ? kStatusTimeout : 0));
   if (warp == kSoftWarps + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
@@ -732,22 +790,21 @@ int tc_splits(const AttnArgs& a, int num_sms) {
   return s < 1 ? 1 : (int)s;
 }
 
-int tc_grid(const AttnArgs& a, int splits, int num_sms) {
+int tc_items(const AttnArgs& a, int splits) {
   const long long items = (long long)tc_plan(a).slots * a.Hkv * splits;
-  return (int)(items < num_sms ? items : num_sms);
+  return items < (1ll << 31) ? (int)items : -1;
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& shape,
-                           int num_sms, cudaStream_t stream) {
+                           cudaStream_t stream) {
   TcAttnArgs t{};
   t.a = a;
   const TcPlan p = tc_plan(a);
   t.tt = p.tt;
   t.slots = p.slots;
   t.splits = splits;
-  const long long items = (long long)p.slots * a.Hkv * splits;
-  if (items >= (1ll << 31)) return cudaErrorInvalidValue;
-  t.items = (int)items;
+  const int items = tc_items(a, splits);
+  if (items < 0) return cudaErrorInvalidValue;
   t.box = a.page_table && (1 << a.page_shift) < kKeys ? 1 << a.page_shift : kKeys;
   t.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
   t.negate = a.scale < 0;
@@ -762,11 +819,10 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   if (paged ? !pages_map(&k, a.k_cache, a, t.box) || !pages_map(&v, a.v_cache, a, t.box)
             : !rows_map(&k, a.k, a, a.Tk, a.Hkv, kKeys) || !rows_map(&v, a.v, a, a.Tk, a.Hkv, kKeys))
     return cudaErrorInvalidValue;
-  const int grid = tc_grid(a, splits, num_sms);
   Report rep = shape;
-  rep.blocks[rep.set] = grid;
+  rep.blocks[rep.set] = items;
 #define TC_CASE(DD, F, P) \
-  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, rep, grid, stream);
+  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, rep, items, stream);
   TC_CASE(64, false, false)
   TC_CASE(64, false, true)
   TC_CASE(64, true, false)

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 4 : 1) rope_append_kern
     }
   }
   const int any = __syncthreads_or(bad);
-  if (threadIdx.x == 0) report(rep, any ? kStatusBounds : 0);
+  if (threadIdx.x == 0) report(rep, blockIdx.x, any ? kStatusBounds : 0);
 }
 
 template <int D, int kHeads, bool kF16>
@@ -158,7 +158,7 @@ cudaError_t launch(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream
   constexpr int kGroups = kThreads / (D / 8);
   const long long chunks = (a.Hq + kHeads - 1) / kHeads + 2 * ((a.Hkv + kHeads - 1) / kHeads);
   const long long blocks = (a.T * chunks + kGroups - 1) / kGroups;
-  const long long most = (long long)num_sms * 8 < kFlagsPerSet ? (long long)num_sms * 8 : kFlagsPerSet;
+  const long long most = (long long)num_sms * 8 < kFlagsFirst ? (long long)num_sms * 8 : kFlagsFirst;
   const int grid = (int)(blocks < most ? blocks : most);
   const Report rep{ws, 0, {grid, 0}};
   if (a.interleaved) rope_append_kernel<D, kHeads, kF16, true><<<grid, kThreads, 0, stream>>>(a, rep);
