@@ -10,12 +10,11 @@
 //   P = 2^{c S - m'},  l += sum P  fp32; P rounded to the element type for
 //   O += P V                       the second product (A from tensor memory)
 // with out = O / l and lse = (m + log2 l) ln 2 at the end.  m is a scale, not
-// the exact maximum: a row takes the maximum of its first block, and P is
+// the exact maximum: a row takes the maximum of its first few logits, and P is
 // formed with it from then on, without looking at the logits first.  The sum of
 // P, needed anyway, says when a row has outgrown its scale (2^15: P stays within
 // f16, and bf16 rounds relative to P whatever its size); only then the row's
-// maximum is taken again and l and O are rescaled, which after the first blocks
-// hardly happens.
+// maximum is taken again and l and O are rescaled, which hardly happens.
 #include <cuda.h>
 
 #include "attn.h"
@@ -38,7 +37,9 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kSoftRegs = 208, kLoadRegs = 88;
 static_assert(2 * kSoftRegs + kLoadRegs <= 3 * 168, "the shares come from the launch's registers");
 constexpr int kHalf = kKeys / 2;
-constexpr float kMost = 32768.0f;   // sum of a row's P in half a block that asks for a new maximum
+// A row asks for a new scale when a logit exceeds it by more than 2^9, which
+// the sum of P over half a block shows: 64 of them stay within 2^15.
+constexpr float kLag = 9.0f, kMost = 32768.0f;
 constexpr uint32_t kTmemCols = 512;
 
 // Tiles in shared memory: rows of 64 elements in 1 KB swizzle atoms of 8.  Q,
@@ -74,8 +75,8 @@ struct TcAttnArgs {
   AttnArgs a;
   int tt, slots, splits;
   int box;                       // rows of a K / V box
-  float c;                       // |scale| log2 e, > 0
-  int negate;                    // scale < 0
+  float c;                       // scale log2 e, not 0
+  float hidden;                  // a masked logit: c times it is -inf
   float* part_o;                 // [splits, T, Hq, D], null when splits is 1
   float* part_lse;               // [splits, T, Hq], log2
 };
@@ -569,120 +570,152 @@ __global__ void __launch_bounds__(kThreads, 1)
         // when all its P is formed (702 us; after the first half 743), with
         // D = 64 after the first half (611 us; after both 678).
         if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
-        // the row's logits in two halves, the second on its way meanwhile
-        float s[2][kHalf];
-        tmem_ld64(tS, s[0]);
-        tmem_wait_ld64(s[0]);
-        tmem_ld64(tS + kHalf, s[1]);
-        const int b = it.b0 + j, lim = vis - b * kKeys;
-        const bool masked = vis0 < (b + 1) * kKeys;
-        auto prepare = [&](int half) {
-          if (t.negate) {
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) s[half][i] = -s[half][i];
-          }
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < kHalf; ++i) s[half][i] = half * kHalf + i < lim ? s[half][i] : -INFINITY;
-          }
-        };
-        auto row_max = [&](int half) {
-          float mx[4] = {s[half][0], s[half][1], s[half][2], s[half][3]};
-#pragma unroll
-          for (int i = 4; i < kHalf - 4; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = max3(mx[k], s[half][i + k], s[half][i + k + 4]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], s[half][kHalf - 4 + k]);
-          return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * t.c;
-        };
+        const int b = it.b0 + j;
         const uint64_t c2 = pair(t.c, t.c);
-        uint32_t p[32];
-        // P of a half with the maximum in use; the sum of the row's
-        auto half_p = [&](int half) {
+        auto arrive = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
+        };
+        auto hand_over = [&](int half) {
+          if (half == (D == 64 ? 0 : 1) && j < both) {
+            ++nt;
+            if (lane == 0) mbar_arrive(&turn[x ^ 1]);
+          }
+        };
+        // Blocks that every row sees whole: both halves written out, without a
+        // look at the logits first.  What is rare (a mask, a row that outgrew its
+        // scale) takes the small loops below instead: code that does not stay in
+        // the instruction cache costs ~100 cycles per eight instructions (a first
+        // block took 3500 cycles with all of it written out).
+        int slow = 0;                       // first half that is left to the loops
+        if (vis0 >= (b + 1) * kKeys) {
+          if (__any_sync(0xffffffffu, live && m == -INFINITY)) {
+            // a first scale: the maximum of a few logits
+            float u[16];
+            tmem_ld16(tS, *reinterpret_cast<uint32_t(*)[16]>(u));
+            tmem_wait_ld();
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, u[k] * t.c);
+            if (m == -INFINITY) m = top;
+          }
           const float off = m == -INFINITY ? 0.f : -m;
           const uint64_t off2 = pair(off, off);
-          uint64_t sum = 0, sum2 = 0;
+          float s[2][kHalf];
+          uint32_t p[32];
+          auto half_p = [&](int half) {
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const uint64_t y = fma2(pair(s[half][2 * i], s[half][2 * i + 1]), c2, off2);
-            const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
-            if (i & 1) sum2 = add2(sum2, pair(p0, p1));
-            else sum = add2(sum, pair(p0, p1));
-            p[i] = pack2<kF16>(p0, p1);
-          }
-          sum = add2(sum, sum2);
-          return lo(sum) + hi(sum);
-        };
-        // A new maximum for the rows that need one: l and O to its scale
-        auto raise = [&](float top, bool need, bool has_o) {
-          const bool up = need && top > m;
-          const float f = up ? ex2(m - top) : 1.0f;            // m = -inf: 0
-          if (up) m = top;
-          l *= f;
-          if (has_o) {
-#pragma unroll 1
-            for (int i = 0; i < D; i += 16) {
-              uint32_t o[16];
-              tmem_ld16(tO + i, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-              tmem_st16(tO + i, o);
+            for (int k = 0; k < 32; ++k) {
+              const uint64_t y = fma2(pair(s[half][2 * k], s[half][2 * k + 1]), c2, off2);
+              const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+              sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+              p[k] = pack2<kF16>(p0, p1);
+            }
+            sum[0] = add2(sum[0], sum[1]);
+            return lo(sum[0]) + hi(sum[0]);
+          };
+          tmem_ld64(tS, s[0]);
+          tmem_wait_ld64(s[0]);
+          tmem_ld64(tS + kHalf, s[1]);      // on its way meanwhile
+          float sum = half_p(0);
+          tmem_wait_ld64(s[1]);
+          if (!__any_sync(0xffffffffu, live && sum > kMost)) {
+            l += sum;
+            tmem_st32(tS, p);
+            arrive(0);
+            hand_over(0);
+            sum = half_p(1);
+            slow = 1;
+            if (!__any_sync(0xffffffffu, live && sum > kMost)) {
+              hand_over(1);
+              l += sum;
+              tmem_st32(tS + 32, p);
+              arrive(1);
+              slow = 2;
             }
           }
-        };
-        prepare(0);
-        float sum = j > 0 ? half_p(0) : 0.f;
-        bool need = live && (sum > kMost || (m == -INFINITY && lim > 0));
-        if (j == 0 || __any_sync(0xffffffffu, need)) {
-          tmem_wait_ld64(s[1]);
-          prepare(1);
-          raise(fmaxf(row_max(0), row_max(1)), j == 0 || need, j > 0);
-          sum = half_p(0);
-        } else {
-          tmem_wait_ld64(s[1]);
-          prepare(1);
         }
-        l += sum;
-        tmem_st32(tS, p);
         // The block that the keys end in: rows of its V tile past the end hold
         // other data (or NaN), which a weight of 0 does not silence: clear them.
         // Each tile that multiplies the block does it.
-        const int tail = it.len & (kKeys - 1);
-        if (tail && b == it.len / kKeys) {
+        const int tail = it.len - b * kKeys;
+        if (tail < kKeys) {
           const uint32_t i = kv0 + 2 * j + 1;
           if (!warp_spin(&kv_full[i % NS], (i / NS) & 1)) { ok = false; break; }
           if (row >= tail) {
             uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + (row / 8) * S::kGroup +
                                                 (row % 8) * 128);
-#pragma unroll
+#pragma unroll 4
             for (int u = 0; u < S::kHalves * 8; ++u) v[(u / 8) * (S::kColumn / 16) + u % 8] = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * x]);
-        if (D == 64 && j < both && lane == 0) mbar_arrive(&turn[x ^ 1]);
-        sum = half_p(1);
-        if (D != 64 && j < both && lane == 0) mbar_arrive(&turn[x ^ 1]);
-        nt += j < both;
-        need = live && sum > kMost;
-        if (__any_sync(0xffffffffu, need)) {
-          // the product with the first half may be adding to O
-          if (!warp_spin(&h_done[x], ns & 1)) { ok = false; break; }
-          tc_fence_after();
-          raise(row_max(1), need, true);
-          sum = half_p(1);
+#pragma unroll 1
+        for (int half = slow; half < 2; ++half) {
+          const uint32_t at = tS + half * kHalf;
+          const int lim = vis - b * kKeys - half * kHalf;           // keys of the half that the row sees
+          float s[32];
+          auto load = [&](int i0) {                                  // c times 32 logits
+            tmem_ld32(at + i0, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s[k] = i0 + k < lim ? s[k] * t.c : -INFINITY;
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kHalf; i0 += 32) {
+            load(i0);
+            float mx[4] = {top, s[0], s[1], s[2]};
+#pragma unroll
+            for (int k = 3; k < 31; k += 4)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[k + u]);
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), fmaxf(mx[3], s[31]));
+          }
+          const bool up = live && top > m + kLag;                    // m = -inf: any key that is seen
+          if (__any_sync(0xffffffffu, up)) {
+            const float f = up ? ex2(m - top) : 1.0f;
+            if (up) m = top;
+            l *= f;
+            if (j + half > 0) {
+              // O += P V of the block before is complete (S of this one came
+              // after it), that of the first half may be under way
+              if (half && !warp_spin(&h_done[x], ns & 1)) ok = false;
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                tmem_st16(tO + i, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : m;
+          uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+          for (int i0 = 0; i0 < kHalf; i0 += 32) {
+            load(i0);
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float p0 = ex2(s[2 * k] - off), p1 = ex2(s[2 * k + 1] - off);
+              sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+              p[k] = pack2<kF16>(p0, p1);
+            }
+            tmem_st16(tS + half * 32 + i0 / 2, p);                   // over logits that were read
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          l += lo(sum[0]) + hi(sum[0]);
+          hand_over(half);
+          arrive(half);
         }
-        l += sum;
-        tmem_st32(tS + 32, p);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * x + 1]);
+        if (!ok) break;
       }
       if (!ok) break;
       if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
@@ -697,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto put = [&](int unit, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v; };
       auto write = [&](unsigned char* out, long long row_bytes) {
         __syncwarp();
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {
           const int r = 4 * i + (lane >> 3), to = __shfl_sync(0xffffffffu, at, r);
           const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
@@ -705,44 +738,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      if (t.part_o) {
-        const long long part = (long long)it.split * a.T * a.Hq;
-        if (live) t.part_lse[part + first + at] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
-        if (n > 0)                       // a part without keys is not read
+      const bool part = t.part_o != nullptr;
+      if (part) {
+        if (live) t.part_lse[(long long)it.split * a.T * a.Hq + first + at] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
+      } else if (live && a.lse) {
+        a.lse[first + at] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
+      }
+      unsigned char* out = part ? reinterpret_cast<unsigned char*>(t.part_o + (long long)it.split * a.T * a.Hq * D)
+                                : reinterpret_cast<unsigned char*>(a.out);
+      const int row_bytes = part ? D * 4 : D * 2, fill = part ? 2 : 4;   // pieces of 16 columns to 128 bytes
+      if (n > 0 || !part)                                                // a part without keys is not read
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + i, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              put(u, make_uint4(__float_as_uint(__uint_as_float(o[4 * u]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * u + 1]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * u + 2]) * inv),
-                                __float_as_uint(__uint_as_float(o[4 * u + 3]) * inv)));
-            write(reinterpret_cast<unsigned char*>(t.part_o + part * D + i), D * 4);
-          }
-      } else {
-        if (live && a.lse) a.lse[first + at] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
-#pragma unroll 1
-        for (int i = 0; i < D; i += 64) {
-          float o[64];
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t o[16];
           if (n > 0) {
-            tmem_ld64(tO + i, o);
-            tmem_wait_ld64(o);
+            tmem_ld16(tO + 16 * i, o);
+            tmem_wait_ld();
+          }
+          float v[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) v[u] = n > 0 ? __uint_as_float(o[u]) * inv : 0.f;
+          if (part) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              put(4 * (i & 1) + u, make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                                              __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3])));
           } else {
 #pragma unroll
-            for (int u = 0; u < 64; ++u) o[u] = 0.f;
+            for (int u = 0; u < 2; ++u)
+              put(2 * (i & 3) + u, make_uint4(pack2<kF16>(v[8 * u], v[8 * u + 1]), pack2<kF16>(v[8 * u + 2], v[8 * u + 3]),
+                                              pack2<kF16>(v[8 * u + 4], v[8 * u + 5]),
+                                              pack2<kF16>(v[8 * u + 6], v[8 * u + 7])));
           }
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            put(u, make_uint4(pack2<kF16>(o[8 * u] * inv, o[8 * u + 1] * inv),
-                              pack2<kF16>(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
-                              pack2<kF16>(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
-                              pack2<kF16>(o[8 * u + 6] * inv, o[8 * u + 7] * inv)));
-          write(reinterpret_cast<unsigned char*>(a.out + i), D * 2);
+          if ((i + 1) % fill == 0) write(out + (i / fill) * 128, row_bytes);
         }
-      }
       tc_fence_before();
       if (*(volatile int*)abort_flag) { ok = false; break; }
     }
@@ -806,11 +835,11 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   const int items = tc_items(a, splits);
   if (items < 0) return cudaErrorInvalidValue;
   t.box = a.page_table && (1 << a.page_shift) < kKeys ? 1 << a.page_shift : kKeys;
-  t.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
-  t.negate = a.scale < 0;
-  // a scale of 0 (or so small that it would flush): positive, so that a masked
-  // logit of -inf stays one, and every other still counts as 0
-  if (t.c < 1.2e-38f) t.c = 1.2e-38f;
+  t.c = a.scale * 1.4426950408889634f;
+  // a scale of 0 (or so small that it would flush): so that a masked logit
+  // stays one, and every other still counts as 0
+  if (t.c < 1.2e-38f && t.c > -1.2e-38f) t.c = 1.2e-38f;
+  t.hidden = t.c > 0 ? -INFINITY : INFINITY;
   t.part_o = part_o;
   t.part_lse = part_lse;
   const bool paged = a.page_table != nullptr;
