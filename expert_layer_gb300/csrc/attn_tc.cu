@@ -37,9 +37,7 @@ constexpr int kThreads = (kSoftWarps + 4) * 32;
 constexpr int kSoftRegs = 208, kLoadRegs = 88;
 static_assert(2 * kSoftRegs + kLoadRegs <= 3 * 168, "the shares come from the launch's registers");
 constexpr int kHalf = kKeys / 2;
-// A row asks for a new scale when a logit exceeds it by more than 2^9, which
-// the sum of P over half a block shows: 64 of them stay within 2^15.
-constexpr float kLag = 9.0f, kMost = 32768.0f;
+constexpr float kMost = 32768.0f;   // sum of a row's P over half a block that asks for a new scale
 constexpr uint32_t kTmemCols = 512;
 
 // Tiles in shared memory: rows of 64 elements in 1 KB swizzle atoms of 8.  Q,
@@ -584,50 +582,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&turn[x ^ 1]);
           }
         };
-        // Blocks that every row sees whole: both halves written out, without a
-        // look at the logits first.  What is rare (a mask, a row that outgrew its
-        // scale) takes the small loops below instead: code that does not stay in
-        // the instruction cache costs ~100 cycles per eight instructions (a first
-        // block took 3500 cycles with all of it written out).
-        int slow = 0;                       // first half that is left to the loops
-        if (vis0 >= (b + 1) * kKeys) {
-          if (__any_sync(0xffffffffu, live && m == -INFINITY)) {
-            // a first scale: the maximum of a few logits
-            float u[16];
-            tmem_ld16(tS, *reinterpret_cast<uint32_t(*)[16]>(u));
-            tmem_wait_ld();
-            float top = -INFINITY;
+        const int lim = vis - b * kKeys;    // keys of the block that the row sees: more in later rows
+        const int lim0 = __shfl_sync(0xffffffffu, lim, 0), lim1 = __shfl_sync(0xffffffffu, lim, 31);
+        if (__any_sync(0xffffffffu, live && m == -INFINITY && lim > 0)) {
+          // a first scale: the maximum of the first few logits
+          float u[16];
+          tmem_ld16(tS, *reinterpret_cast<uint32_t(*)[16]>(u));
+          tmem_wait_ld();
+          float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, u[k] * t.c);
-            if (m == -INFINITY) m = top;
-          }
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * t.c : -INFINITY);
+          if (m == -INFINITY) m = top;
+        }
+        // 64 logits to P with the scale in use; the sum
+        auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32]) {
           const float off = m == -INFINITY ? 0.f : -m;
           const uint64_t off2 = pair(off, off);
-          float s[2][kHalf];
-          uint32_t p[32];
-          auto half_p = [&](int half) {
-            uint64_t sum[2] = {0, 0};
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const uint64_t y = fma2(pair(s[half][2 * k], s[half][2 * k + 1]), c2, off2);
-              const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
-              sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-              p[k] = pack2<kF16>(p0, p1);
-            }
-            sum[0] = add2(sum[0], sum[1]);
-            return lo(sum[0]) + hi(sum[0]);
-          };
-          tmem_ld64(tS, s[0]);
-          tmem_wait_ld64(s[0]);
-          tmem_ld64(tS + kHalf, s[1]);      // on its way meanwhile
-          float sum = half_p(0);
-          tmem_wait_ld64(s[1]);
+          for (int k = 0; k < 32; ++k) {
+            const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), c2, off2);
+            const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+            sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+            p[k] = pack2<kF16>(p0, p1);
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          return lo(sum[0]) + hi(sum[0]);
+        };
+        // A block that the warp's rows see whole: both halves written out,
+        // without a look at the logits first and without branches (those of a
+        // mask cost 10% over 8192 keys).
+        int slow = 0;                       // first half that is left to the loop below
+        if (lim0 >= kKeys) {
+          float s0[kHalf], s1[kHalf];
+          uint32_t p[32];
+          tmem_ld64(tS, s0);
+          tmem_wait_ld64(s0);
+          tmem_ld64(tS + kHalf, s1);        // on its way meanwhile
+          float sum = form(s0, p);
+          tmem_wait_ld64(s1);
           if (!__any_sync(0xffffffffu, live && sum > kMost)) {
             l += sum;
             tmem_st32(tS, p);
             arrive(0);
             hand_over(0);
-            sum = half_p(1);
+            sum = form(s1, p);
             slow = 1;
             if (!__any_sync(0xffffffffu, live && sum > kMost)) {
               hand_over(1);
@@ -638,9 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // The block that the keys end in: rows of its V tile past the end hold
-        // other data (or NaN), which a weight of 0 does not silence: clear them.
-        // Each tile that multiplies the block does it.
+        // Blocks with masked keys, and rows that outgrew their scale: a loop
+        // over the halves, one piece of code.  (Code that does not stay in the
+        // instruction cache costs ~100 cycles per eight instructions: with the
+        // rare cases written out twice a first block took 3500 cycles.)
+        // Rows of V past the keys' end hold other data (or NaN), which a weight
+        // of 0 does not silence: clear them (each tile that multiplies them).
         const int tail = it.len - b * kKeys;
         if (tail < kKeys) {
           const uint32_t i = kv0 + 2 * j + 1;
@@ -655,63 +657,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll 1
         for (int half = slow; half < 2; ++half) {
-          const uint32_t at = tS + half * kHalf;
-          const int lim = vis - b * kKeys - half * kHalf;           // keys of the half that the row sees
-          float s[32];
-          auto load = [&](int i0) {                                  // c times 32 logits
-            tmem_ld32(at + i0, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tmem_wait_ld();
+          const int from = half * kHalf;
+          uint32_t p[32];
+          if (lim1 <= from) {                                        // no row sees a key of it
 #pragma unroll
-            for (int k = 0; k < 32; ++k) s[k] = i0 + k < lim ? s[k] * t.c : -INFINITY;
-          };
-          float top = -INFINITY;
+            for (int k = 0; k < 32; ++k) p[k] = 0;
+          } else {
+            float s[kHalf];
+            tmem_ld64(tS + from, s);
+            tmem_wait_ld64(s);
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k) s[k] = from + k < lim ? s[k] : t.hidden;
+            float sum;
 #pragma unroll 1
-          for (int i0 = 0; i0 < kHalf; i0 += 32) {
-            load(i0);
-            float mx[4] = {top, s[0], s[1], s[2]};
+            for (int pass = 0;; ++pass) {
+              sum = form(s, p);
+              const bool need = live && (sum > kMost || (m == -INFINITY && lim > from));
+              if (pass || !__any_sync(0xffffffffu, need)) break;
+              // a new scale for the rows that need one: their maximum
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 3; k < 31; k += 4)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], s[k + u]);
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), fmaxf(mx[3], s[31]));
-          }
-          const bool up = live && top > m + kLag;                    // m = -inf: any key that is seen
-          if (__any_sync(0xffffffffu, up)) {
-            const float f = up ? ex2(m - top) : 1.0f;
-            if (up) m = top;
-            l *= f;
-            if (j + half > 0) {
-              // O += P V of the block before is complete (S of this one came
-              // after it), that of the first half may be under way
-              if (half && !warp_spin(&h_done[x], ns & 1)) ok = false;
-              tc_fence_after();
+              for (int k = 0; k < kHalf; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k] * t.c);
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              const bool up = need && top > m;
+              const float f = up ? ex2(m - top) : 1.0f;              // m = -inf: 0
+              if (up) m = top;
+              l *= f;
+              if (j + half > 0) {
+                // O += P V of the block before is complete (S of this one came
+                // after it), that of the first half may be under way
+                if (half && !warp_spin(&h_done[x], ns & 1)) ok = false;
+                tc_fence_after();
 #pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                uint32_t o[16];
-                tmem_ld16(tO + i, o);
-                tmem_wait_ld();
+                for (int i = 0; i < D; i += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + i, o);
+                  tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
-                tmem_st16(tO + i, o);
+                  for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
+                  tmem_st16(tO + i, o);
+                }
               }
             }
+            l += sum;
           }
-          const float off = m == -INFINITY ? 0.f : m;
-          uint64_t sum[2] = {0, 0};
-#pragma unroll 1
-          for (int i0 = 0; i0 < kHalf; i0 += 32) {
-            load(i0);
-            uint32_t p[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float p0 = ex2(s[2 * k] - off), p1 = ex2(s[2 * k + 1] - off);
-              sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-              p[k] = pack2<kF16>(p0, p1);
-            }
-            tmem_st16(tS + half * 32 + i0 / 2, p);                   // over logits that were read
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          l += lo(sum[0]) + hi(sum[0]);
+          tmem_st32(tS + half * 32, p);
           hand_over(half);
           arrive(half);
         }
@@ -727,15 +717,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       unsigned char* stage = smem + S::kOut + warp * 32 * 128;
       const int at = live ? token * a.Hq + g : -1;              // row's place after the tile's first
       const long long first = (long long)(it.row0 + x * t.tt) * a.Hq + it.head * G;
+      int to[8];                                                // places of the rows that this lane writes
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
       auto put = [&](int unit, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v; };
-      auto write = [&](unsigned char* out, long long row_bytes) {
+      auto write = [&](unsigned char* out, int row_bytes) {
         __syncwarp();
-#pragma unroll 2
+        uint4 v[8];
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), to = __shfl_sync(0xffffffffu, at, r);
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (to >= 0) *reinterpret_cast<uint4*>(out + (first + to) * row_bytes + (lane & 7) * 16) = v;
+          const int r = 4 * i + (lane >> 3);
+          v[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (to[i] >= 0) *reinterpret_cast<uint4*>(out + (long long)to[i] * row_bytes) = v[i];
         __syncwarp();
       };
       const bool part = t.part_o != nullptr;
@@ -744,33 +740,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (live && a.lse) {
         a.lse[first + at] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
       }
-      unsigned char* out = part ? reinterpret_cast<unsigned char*>(t.part_o + (long long)it.split * a.T * a.Hq * D)
-                                : reinterpret_cast<unsigned char*>(a.out);
-      const int row_bytes = part ? D * 4 : D * 2, fill = part ? 2 : 4;   // pieces of 16 columns to 128 bytes
+      const int row_bytes = part ? D * 4 : D * 2;
+      unsigned char* out =
+          (part ? reinterpret_cast<unsigned char*>(t.part_o + (long long)it.split * a.T * a.Hq * D)
+                : reinterpret_cast<unsigned char*>(a.out)) + first * row_bytes + (lane & 7) * 16;
       if (n > 0 || !part)                                                // a part without keys is not read
 #pragma unroll 1
-        for (int i = 0; i < D / 16; ++i) {
-          uint32_t o[16];
+        for (int i = 0; i < D; i += 32) {
+          float v[32];
           if (n > 0) {
-            tmem_ld16(tO + 16 * i, o);
+            tmem_ld32(tO + i, *reinterpret_cast<uint32_t(*)[32]>(v));
             tmem_wait_ld();
-          }
-          float v[16];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) v[u] = n > 0 ? __uint_as_float(o[u]) * inv : 0.f;
-          if (part) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              put(4 * (i & 1) + u, make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
-                                              __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3])));
           } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-              put(2 * (i & 3) + u, make_uint4(pack2<kF16>(v[8 * u], v[8 * u + 1]), pack2<kF16>(v[8 * u + 2], v[8 * u + 3]),
-                                              pack2<kF16>(v[8 * u + 4], v[8 * u + 5]),
-                                              pack2<kF16>(v[8 * u + 6], v[8 * u + 7])));
+            for (int u = 0; u < 32; ++u) v[u] = 0.f;
           }
-          if ((i + 1) % fill == 0) write(out + (i / fill) * 128, row_bytes);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) v[u] *= inv;
+          if (part) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              put(u, make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
+                                __float_as_uint(v[4 * u + 3])));
+          } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              put((i & 32) / 8 + u, make_uint4(pack2<kF16>(v[8 * u], v[8 * u + 1]), pack2<kF16>(v[8 * u + 2], v[8 * u + 3]),
+                                               pack2<kF16>(v[8 * u + 4], v[8 * u + 5]),
+                                               pack2<kF16>(v[8 * u + 6], v[8 * u + 7])));
+            if (!(i & 32)) continue;
+          }
+          write(out + (part ? i * 4 : (i - 32) * 2), row_bytes);
         }
       tc_fence_before();
       if (*(volatile int*)abort_flag) { ok = false; break; }
