@@ -155,12 +155,31 @@ struct DecodeParts {
   float* slot_lse;
   long long* base;
 };
-// Blocks that share a line of `total` slices: at least a slice for each of
-// their eight warps, as far as the grid goes
-__host__ __device__ inline int decode_blocks(long long total, int grid) {
-  const long long n = (total + 7) / 8;
-  return (int)(n < 1 ? 1 : n < grid ? n : grid);
+// A unit costs its warp about as much as one 16-key slice besides its slices
+// (queries, the end of the softmax): 64 sequences of 1 to 8192 keys
+constexpr int kUnitCost = 1;
+__host__ __device__ inline long long divide(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
+// The line of all units' places, cut into equal ranges for the warps of as many
+// blocks as have a place for each of their eight warps (up to the grid).
+struct Line {
+  long long each;      // places per warp; the first `more` warps have one more
+  int blocks, more;
+  __host__ __device__ Line(long long total, int grid) {
+    const long long n = (total + 7) / 8;
+    blocks = (int)(n < 1 ? 1 : n < grid ? n : grid);
+    each = divide(total, blocks * 8);
+    more = (int)(total - each * (blocks * 8));
+  }
+  // first place of warp g (of all blocks')
+  __host__ __device__ long long at(int g) const { return each * g + (g < more ? g : more); }
+  // block of a place
+  __host__ __device__ int block_of(long long place) const {
+    const long long cut = (each + 1) * more;
+    return (int)(place < cut ? divide(place, each + 1) : more + divide(place - cut, each)) / 8;
+  }
+};
 // Units of at most 16 heads per key-value head
 inline int decode_chunks(const AttnArgs& a) { return (a.Hq / a.Hkv + 15) / 16; }
 cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& rep, int num_sms,

@@ -3,9 +3,10 @@
 // A unit is one sequence's token on one key-value head: its G query heads
 // (at most 16; larger groups make several units) share every key and value
 // that is read.  The keys of all units form one line of 16-key slices (a
-// slice lies within a page), cut into equal ranges for the blocks, so that
-// lengths as different as 1 and 100,000 load the GPU evenly; a unit that
-// spans blocks leaves one part per block and the merge kernel joins them.
+// slice lies within a page), a unit's slices after one place that stands for
+// the unit's own cost, cut into equal ranges for the blocks, so that lengths as
+// different as 1 and 100,000 load the GPU evenly; a unit that spans blocks
+// leaves one part per block and the merge kernel joins them.
 //
 // Bound: HBM (4 D bytes per key and key-value head against 4 G D flops).  A
 // block's range is cut once more over its eight warps, each of which works
@@ -50,7 +51,8 @@ struct Shape {
 static_assert(Shape<128, false>::kSmem <= 232448 && Shape<128, true>::kSmem <= 232448, "227 KB a block");
 
 // The units of a range: a cursor over (sequence, unit of the sequence),
-// empty sequences left out.  `pos` is the unit's first slice on the line.
+// empty sequences left out.  `pos` is the unit's place on the line; its slices
+// come kUnitCost later.
 struct Cursor {
   int b, u, len, slices;
   long long pos;
@@ -93,6 +95,8 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
   return n < 0 || n > ((long long)a.table_pages << a.page_shift) ? 0 : n;
 }
 __device__ __forceinline__ int slices_of(int len) { return (len + kSlice - 1) / kSlice; }
+// Places that a unit of `len` keys takes on the line
+__device__ __forceinline__ long long unit_weight(int len) { return len > 0 ? slices_of(len) + kUnitCost : 0; }
 
 // Lengths of the sequences from b0 on, the first kWindow of them in shared memory
 struct Lens {
@@ -106,7 +110,7 @@ struct Lens {
 
 // To the next unit that has slices (or past the last sequence).
 __device__ __forceinline__ void advance(const Lens& lens, Cursor& c, int units) {
-  c.pos += c.slices;
+  c.pos += c.slices + kUnitCost;
   if (++c.u < units) return;
   c.u = 0;
   c.slices = 0;
@@ -136,6 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* ring = smem + warp * S::kRing;
   bool bad = false, late = false;
   pdl_trigger();     // the merge kernel may become resident; it waits for this grid's end
+  if (threadIdx.x == 0) {
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
 
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = a.kv_lens[s];
     const bool fits = n >= 0 && n <= ((long long)a.table_pages << a.page_shift);
     if (blockIdx.x == 0 && !fits) bad = true;
-    mine += (long long)slices_of(fits ? n : 0) * units;
+    mine += unit_weight(fits ? n : 0) * units;
     if (run == 1) window[s] = fits ? n : 0;
   }
   long long incl = mine;
@@ -174,17 +182,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long at = before;
     for (int s = s0; s < s1; ++s) {
       t.p.base[s] = at;
-      at += (long long)slices_of(seq_len(a, s)) * units;
+      at += unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
     }
     if (threadIdx.x == kThreads - 1) t.p.base[a.n_seq] = total;
   }
-  const int blocks = decode_blocks(total, gridDim.x);
-  const long long start = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
-  const bool work = (int)blockIdx.x < blocks && start < end;
+  const Line line(total, gridDim.x);
+  const long long start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
+  const bool work = (int)blockIdx.x < line.blocks && start < end;
   if (work && start >= before && start < before + mine) {
     long long at = before;
     for (int s = s0; s < s1; ++s) {
-      const long long n = (long long)slices_of(seq_len(a, s)) * units;
+      const long long n = unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
       if (start < at + n) {
         scan[kWarps] = s;
         scan[kWarps + 1] = at;
@@ -203,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // --- this warp's range
-  const long long ws = total * ((long long)blockIdx.x * kWarps + warp) / ((long long)blocks * kWarps);
-  const long long we = total * ((long long)blockIdx.x * kWarps + warp + 1) / ((long long)blocks * kWarps);
+  const long long ws = line.at(blockIdx.x * kWarps + warp), we = line.at(blockIdx.x * kWarps + warp + 1);
   if (work && ws < we) {
     Cursor cur;
     cur.b = (int)scan[kWarps];
@@ -212,32 +219,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (true) {                               // the sequence that ws lies in
       cur.len = lens(cur.b);
       cur.slices = slices_of(cur.len);
-      const long long n = (long long)cur.slices * units;
+      const long long n = unit_weight(cur.len) * units;
       if (ws < cur.pos + n) break;
       cur.pos += n;
       ++cur.b;
     }
-    cur.u = (int)((ws - cur.pos) / cur.slices);
-    cur.pos += (long long)cur.u * cur.slices;
+    cur.u = (int)divide(ws - cur.pos, cur.slices + kUnitCost);
+    cur.pos += (long long)cur.u * (cur.slices + kUnitCost);
 
     // --- loads: the same walk, kStages slices ahead
     Cursor ld = cur;
-    int ld_slice = (int)(ws - ld.pos);
+    int ld_slice = (int)max(0ll, ws - ld.pos - kUnitCost);
     uint32_t issued = 0;
-    const uint32_t count = (uint32_t)(we - ws);
     int page = 0;
+    bool more;
     // the page id of slice `ld_slice` of ld, one slice before its load
     auto fetch = [&]() {
-      if (issued >= count) return;
       if (ld_slice == ld.slices) {
         advance(lens, ld, units);
         ld_slice = 0;
       }
-      page = a.page_table[(long long)ld.b * a.table_pages + ((ld_slice * kSlice) >> a.page_shift)];
+      more = ld.pos + kUnitCost + ld_slice < we;
+      if (more) page = a.page_table[(long long)ld.b * a.table_pages + ((ld_slice * kSlice) >> a.page_shift)];
     };
     fetch();
     auto issue = [&]() {
-      if (issued >= count) return;
+      if (!more) return;
       if (lane == 0) {
         if ((unsigned)page >= (unsigned)a.pages) {
           bad = true;
@@ -283,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_q(cur, q);
 
     while (cur.pos < we) {
-      const int first = (int)max(0ll, ws - cur.pos), last = (int)min((long long)cur.slices, we - cur.pos);
+      const int first = (int)max(0ll, ws - cur.pos - kUnitCost);
+      const int last = (int)min((long long)cur.slices, we - cur.pos - kUnitCost);
       Cursor nxt = cur;
       advance(lens, nxt, units);
       uint32_t qn[D / 16][2 * kRowSets];             // the next unit's, under way meanwhile
@@ -382,7 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
       }
-      if (first == 0 && last == cur.slices) {
+      if (last <= first) {
+        // none of its slices: the range ends before them
+      } else if (first == 0 && last == cur.slices) {
         const int hk = t.chunks == 1 ? cur.u : cur.u / t.chunks;
         const int h0 = hk * G + (cur.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
 #pragma unroll
@@ -441,53 +451,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   // out = sum_w 2^{m_w - M} O_w / sum_w 2^{m_w - M} l_w.  The parts of a unit
   // follow one another in (warp, part) order.
 #pragma unroll 1
-  for (int e = 0; e < 2 * kWarps;) {
+  for (int e = 0; e < 2 * kWarps; e = e == 0 ? 1 : e + 2) {      // part 0 of the first warp, part 1 of every warp
     const Open op = open[e];
-    int f = e + 1;
-    if (op.b >= 0)
-      while (f < 2 * kWarps && (open[f].b < 0 || (open[f].b == op.b && open[f].u == op.u))) ++f;
-    if (op.b >= 0) {
-      const bool whole = op.pos >= start && op.pos + op.slices <= end;
-      const int slot = 2 * blockIdx.x + (op.pos < start ? 0 : 1);
-      const int hk = t.chunks == 1 ? op.u : op.u / t.chunks;
-      const int h0 = hk * G + (op.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
-      for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        float M = -INFINITY;
-        for (int p = e; p < f; ++p)
-          if (open[p].b >= 0) M = fmaxf(M, stats[p * S::kRows + r].x);
-        float sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = e; p < f; ++p) {
-          if (open[p].b < 0) continue;
-          const float2 ml = stats[p * S::kRows + r];
-          const float w = M == -INFINITY ? 0.f : ex2(ml.x - M);
-          sum = fmaf(w, ml.y, sum);
+    if (op.b < 0) continue;
+    const int w0 = e >> 1;
+    const Open other = open[2 * (lane & (kWarps - 1))];          // part 0 of the warps after it
+    const int parts = 1 + __popc(__ballot_sync(0xffffffffu, lane < kWarps && lane > w0 && other.b == op.b &&
+                                                                other.u == op.u));
+    const long long begin = op.pos + kUnitCost;
+    const bool whole = begin >= start && begin + op.slices <= end;
+    const int slot = 2 * blockIdx.x + (begin < start ? 0 : 1);
+    const int hk = t.chunks == 1 ? op.u : op.u / t.chunks;
+    const int h0 = hk * G + (op.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+      float2 ml[kWarps];
+      float4 x[kWarps];
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < parts) {
+          const int p = k == 0 ? e : 2 * (w0 + k);
           const unsigned char* at = p & 1 ? smem + (p >> 1) * S::kRing : smem + S::kFirst + (p >> 1) * S::kPart;
-          const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + r * D + d);
-          v.x = fmaf(w, x.x, v.x);
-          v.y = fmaf(w, x.y, v.y);
-          v.z = fmaf(w, x.z, v.z);
-          v.w = fmaf(w, x.w, v.w);
+          ml[k] = stats[p * S::kRows + r];
+          x[k] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + r * D + d);
         }
-        const float inv = 1.0f / sum;
-        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-        const float lse = M + lg2(sum);
-        const long long row = (long long)op.b * a.Hq + h0 + r;
-        if (whole && !t.p.row_o) {
-          uint2 w;
-          w.x = pack2<kF16>(v.x, v.y);
-          w.y = pack2<kF16>(v.z, v.w);
-          *reinterpret_cast<uint2*>(a.out + row * D + d) = w;
-          if (a.lse && d == 0) a.lse[row] = lse * 0.693147180559945f;
-        } else {
-          const long long at = whole ? row : (long long)slot * 16 + r;
-          *reinterpret_cast<float4*>((whole ? t.p.row_o : t.p.slot_o) + at * D + d) = v;
-          if (d == 0) (whole ? t.p.row_lse : t.p.slot_lse)[at] = lse;
-        }
+        M = fmaxf(M, ml[k].x);
+      }
+      float sum = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float w = M == -INFINITY ? 0.f : ex2(ml[k].x - M);
+        sum = fmaf(w, ml[k].y, sum);
+        v.x = fmaf(w, x[k].x, v.x);
+        v.y = fmaf(w, x[k].y, v.y);
+        v.z = fmaf(w, x[k].z, v.z);
+        v.w = fmaf(w, x[k].w, v.w);
+      }
+      const float inv = 1.0f / sum;
+      v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+      const float lse = M + lg2(sum);
+      const long long row = (long long)op.b * a.Hq + h0 + r;
+      if (whole && !t.p.row_o) {
+        uint2 w;
+        w.x = pack2<kF16>(v.x, v.y);
+        w.y = pack2<kF16>(v.z, v.w);
+        *reinterpret_cast<uint2*>(a.out + row * D + d) = w;
+        if (a.lse && d == 0) a.lse[row] = lse * 0.693147180559945f;
+      } else {
+        const long long at = whole ? row : (long long)slot * 16 + r;
+        *reinterpret_cast<float4*>((whole ? t.p.row_o : t.p.slot_o) + at * D + d) = v;
+        if (d == 0) (whole ? t.p.row_lse : t.p.slot_lse)[at] = lse;
       }
     }
-    e = f;
   }
   const int any_bad = __syncthreads_or(bad), any_late = __syncthreads_or(late);
   if (threadIdx.x == 0) report(rep, blockIdx.x, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));

@@ -38,17 +38,16 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
   for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
     // blocks c0 .. c0 + own - 1 of the decode kernel hold the row's own keys
     int c0 = 0, own = 0, r = 0;
-    bool later = false;                // the first of them began the unit after its range's start
     if (t.grid > 0) {
       const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), G = a.Hq / a.Hkv;
       const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
       r = (h % G) % 16;
-      const long long total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
+      const long long total = t.p.base[a.n_seq], b0 = t.p.base[b], n = divide(t.p.base[b + 1] - b0, units);
       if (n > 0) {
-        const long long ub = b0 + u * n, blocks = decode_blocks(total, t.grid);
-        c0 = (int)(((ub + 1) * blocks - 1) / total);
-        own = (int)(((ub + n) * blocks - 1) / total) - c0 + 1;
-        later = ub >= total * c0 / blocks;
+        const Line line(total, t.grid);
+        const long long at = b0 + u * n;
+        c0 = line.block_of(at + kUnitCost);
+        own = line.block_of(at + n - 1) - c0 + 1;
       }
       if (t.splits == 0 && own == 1) continue;       // final already
     }
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
           pl = t.p.tc_lse + at;
         } else {
           const int c = c0 + i - t.splits;
-          const long long at = (2ll * c + (c == c0 && later ? 1 : 0)) * 16 + r;
+          const long long at = (2ll * c + (c == c0 ? 1 : 0)) * 16 + r;
           po = t.p.slot_o + at * D;
           pl = t.p.slot_lse + at;
         }

@@ -105,6 +105,9 @@ __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, spin_wait(bar, parity));
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 // One lane of a converged warp (the same one every time)
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;

@@ -261,6 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
+  if (threadIdx.x == 0) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
+  }
   pdl_trigger();   // a merge kernel, or the decode kernel beside it, may become resident
 
   if (threadIdx.x == 0) {
