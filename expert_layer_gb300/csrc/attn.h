@@ -34,7 +34,7 @@ constexpr long long kMaxBlocks = 160;
 constexpr long long kTileRows = 256;
 
 struct Layout {
-  size_t hdr, flags, part_o, part_lse, slot_o, slot_lse, base, total;
+  size_t hdr, flags, part_o, part_lse, slot_o, slot_lse, tail, base, total;
 };
 
 inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
@@ -53,7 +53,8 @@ inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long 
   L.part_lse = take(sizeof(float) * (size_t)rows);
   L.slot_o = take(sizeof(float) * 2 * kMaxBlocks * 16 * D);
   L.slot_lse = take(sizeof(float) * 2 * kMaxBlocks * 16);
-  L.base = take(sizeof(long long) * (size_t)(n_seq + 1));
+  L.tail = take(sizeof(int4) * kMaxBlocks);
+  L.base = take(sizeof(int) * (size_t)(n_seq + 1));
   L.total = o;
   return L;
 }
@@ -144,8 +145,10 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
 // attn_decode.cu -- one token per sequence.  Parts of rows in the workspace:
 // per row (tc_*: `splits` parts of the prefix [splits, T * Hq], then the row's
 // own keys, row_*, null without a prefix), per block (two slots of 16 rows: a
-// unit that began in an earlier block, and one that goes on in the next), and
-// each sequence's first slice on the line.
+// unit that began in an earlier block, and one that goes on in the next), the
+// unit that each block's range ends in, {sequence, unit, blocks from this one
+// on, 0} (0 blocks: none), and each sequence's first place on the line (only
+// with a prefix).
 struct DecodeParts {
   float* tc_o;
   float* tc_lse;
@@ -153,35 +156,40 @@ struct DecodeParts {
   float* row_lse;
   float* slot_o;
   float* slot_lse;
-  long long* base;
+  int4* tail;
+  int32_t* base;
 };
 // A unit costs its warp about as much as one 16-key slice besides its slices
 // (queries, the end of the softmax): 64 sequences of 1 to 8192 keys
 constexpr int kUnitCost = 1;
-__host__ __device__ inline long long divide(long long a, long long b) {
-  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
-}
 // The line of all units' places, cut into equal ranges for the warps of as many
-// blocks as have a place for each of their eight warps (up to the grid).
+// blocks as have a place for each of their eight warps (up to the grid).  Its
+// length is below 2^31 (decode_fits), which keeps the start of the kernel free
+// of 64-bit divisions: code that runs once is fetched from L2 as it runs.
 struct Line {
-  long long each;      // places per warp; the first `more` warps have one more
+  int each;            // places per warp; the first `more` warps have one more
   int blocks, more;
-  __host__ __device__ Line(long long total, int grid) {
-    const long long n = (total + 7) / 8;
-    blocks = (int)(n < 1 ? 1 : n < grid ? n : grid);
-    each = divide(total, blocks * 8);
-    more = (int)(total - each * (blocks * 8));
+  __host__ __device__ Line(int total, int grid) {
+    const int n = total / 8 + (total % 8 != 0);
+    blocks = n < 1 ? 1 : n < grid ? n : grid;
+    each = total / (blocks * 8);
+    more = total - each * (blocks * 8);
   }
   // first place of warp g (of all blocks')
-  __host__ __device__ long long at(int g) const { return each * g + (g < more ? g : more); }
+  __host__ __device__ int at(int g) const { return each * g + (g < more ? g : more); }
   // block of a place
-  __host__ __device__ int block_of(long long place) const {
-    const long long cut = (each + 1) * more;
-    return (int)(place < cut ? divide(place, each + 1) : more + divide(place - cut, each)) / 8;
+  __host__ __device__ int block_of(int place) const {
+    const int cut = (each + 1) * more;
+    return (place < cut ? place / (each + 1) : more + (place - cut) / each) / 8;
   }
 };
 // Units of at most 16 heads per key-value head
 inline int decode_chunks(const AttnArgs& a) { return (a.Hq / a.Hkv + 15) / 16; }
+// The longest line that the page table allows
+inline bool decode_fits(const AttnArgs& a) {
+  const long long slices = ((((long long)a.table_pages << a.page_shift) + 15) / 16 + kUnitCost) * a.Hkv * decode_chunks(a);
+  return slices < (1ll << 31) && slices * a.n_seq < (1ll << 31);
+}
 cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& rep, int num_sms,
                                cudaStream_t stream);
 

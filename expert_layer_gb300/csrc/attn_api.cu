@@ -111,7 +111,8 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
   p.tc_lse = ws_ptr<float>(ws, L.part_lse);
   p.slot_o = ws_ptr<float>(ws, L.slot_o);
   p.slot_lse = ws_ptr<float>(ws, L.slot_lse);
-  p.base = ws_ptr<long long>(ws, L.base);
+  p.tail = ws_ptr<int4>(ws, L.tail);
+  p.base = ws_ptr<int32_t>(ws, L.base);
   Report rep{ws, 0, {sms, 0}};
   int splits = 0;
   if (a.prefix_len > 0) {
@@ -261,6 +262,7 @@ int moe_attn_decode(const moe_heads* q, const moe_kv_cache* cache, const int32_t
   a.page_table = page_table; a.table_pages = table_pages; a.kv_lens = kv_lens;
   a.prefix_table = prefix_table; a.prefix_len = prefix_len;
   a.n_seq = B; a.T = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.scale = scale;
+  if (!decode_fits(a)) return MOE_ERR_UNSUPPORTED;
   return run_attn(a, q, dtype, out, lse, workspace, workspace_bytes, stream);
 }
 

@@ -43,7 +43,7 @@ struct Shape {
   static constexpr int kFirst = kWarps * kRing;                    // O of the warps' first parts
   static constexpr int kStats = kFirst + kWarps * kPart;           // m and l of the rows, two parts per warp
   static constexpr int kOpen = kStats + kWarps * 2 * kRows * 8;       // the units that the parts belong to
-  static constexpr int kBars = kOpen + kWarps * 2 * 32;
+  static constexpr int kBars = kOpen + kWarps * 2 * 16;
   static constexpr int kLens = kBars + kWarps * kStages * 8;
   static constexpr int kScan = kLens + kWindow * 4;
   static constexpr size_t kSmem = kScan + 128;
@@ -54,13 +54,11 @@ static_assert(Shape<128, false>::kSmem <= 232448 && Shape<128, true>::kSmem <= 2
 // empty sequences left out.  `pos` is the unit's place on the line; its slices
 // come kUnitCost later.
 struct Cursor {
-  int b, u, len, slices;
-  long long pos;
+  int b, u, len, slices, pos;
 };
 // A unit that a warp holds a part of (b < 0: none)
 struct Open {
-  int b, u, slices, pad;
-  long long pos;
+  int b, u, slices, pos;
 };
 
 struct DecodeArgs {
@@ -96,7 +94,7 @@ __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
 }
 __device__ __forceinline__ int slices_of(int len) { return (len + kSlice - 1) / kSlice; }
 // Places that a unit of `len` keys takes on the line
-__device__ __forceinline__ long long unit_weight(int len) { return len > 0 ? slices_of(len) + kUnitCost : 0; }
+__device__ __forceinline__ int unit_weight(int len) { return len > 0 ? slices_of(len) + kUnitCost : 0; }
 
 // Lengths of the sequences from b0 on, the first kWindow of them in shared memory
 struct Lens {
@@ -132,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* stats = reinterpret_cast<float2*>(smem + S::kStats);         // [warp][part][row]: m, l
   Open* open = reinterpret_cast<Open*>(smem + S::kOpen);               // [warp][part]
   int* window = reinterpret_cast<int*>(smem + S::kLens);
-  long long* scan = reinterpret_cast<long long*>(smem + S::kScan);     // [8] warp sums, then the start
+  int* scan = reinterpret_cast<int*>(smem + S::kScan);     // [8] warp sums, then the start
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv, units = a.Hkv * t.chunks;
@@ -155,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // --- the line of slices: every thread sums a run of sequences
   const int run = (a.n_seq + kThreads - 1) / kThreads;
   const int s0 = min(a.n_seq, (int)threadIdx.x * run), s1 = min(a.n_seq, s0 + run);
-  long long mine = 0;
+  int mine = 0;
   for (int s = s0; s < s1; ++s) {
     const int n = a.kv_lens[s];
     const bool fits = n >= 0 && n <= ((long long)a.table_pages << a.page_shift);
@@ -163,23 +161,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     mine += unit_weight(fits ? n : 0) * units;
     if (run == 1) window[s] = fits ? n : 0;
   }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, d);
+    const int v = __shfl_up_sync(0xffffffffu, incl, d);
     if (lane >= d) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
   before += incl - mine;
-  if (blockIdx.x == 0) {                     // the merge kernel reads where each sequence lies
-    long long at = before;
+  if (blockIdx.x == 0 && t.p.row_o) {        // with a prefix the merge kernel reads where each sequence lies
+    int at = before;
     for (int s = s0; s < s1; ++s) {
       t.p.base[s] = at;
       at += unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
@@ -187,12 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == kThreads - 1) t.p.base[a.n_seq] = total;
   }
   const Line line(total, gridDim.x);
-  const long long start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
+  const int start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
   const bool work = (int)blockIdx.x < line.blocks && start < end;
   if (work && start >= before && start < before + mine) {
-    long long at = before;
+    int at = before;
     for (int s = s0; s < s1; ++s) {
-      const long long n = unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
+      const int n = unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
       if (start < at + n) {
         scan[kWarps] = s;
         scan[kWarps + 1] = at;
@@ -204,32 +202,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   Lens lens{&a, window, 0};
   if (work && run > 1) {
-    lens.b0 = (int)scan[kWarps];
+    lens.b0 = scan[kWarps];
     const int s = lens.b0 + threadIdx.x;
     window[threadIdx.x] = s < a.n_seq ? seq_len(a, s) : 0;
     __syncthreads();
   }
 
   // --- this warp's range
-  const long long ws = line.at(blockIdx.x * kWarps + warp), we = line.at(blockIdx.x * kWarps + warp + 1);
+  const int ws = line.at(blockIdx.x * kWarps + warp), we = line.at(blockIdx.x * kWarps + warp + 1);
   if (work && ws < we) {
     Cursor cur;
-    cur.b = (int)scan[kWarps];
+    cur.b = scan[kWarps];
     cur.pos = scan[kWarps + 1];
     while (true) {                               // the sequence that ws lies in
       cur.len = lens(cur.b);
       cur.slices = slices_of(cur.len);
-      const long long n = unit_weight(cur.len) * units;
+      const int n = unit_weight(cur.len) * units;
       if (ws < cur.pos + n) break;
       cur.pos += n;
       ++cur.b;
     }
-    cur.u = (int)divide(ws - cur.pos, cur.slices + kUnitCost);
-    cur.pos += (long long)cur.u * (cur.slices + kUnitCost);
+    cur.u = (ws - cur.pos) / (cur.slices + kUnitCost);
+    cur.pos += cur.u * (cur.slices + kUnitCost);
 
     // --- loads: the same walk, kStages slices ahead
     Cursor ld = cur;
-    int ld_slice = (int)max(0ll, ws - ld.pos - kUnitCost);
+    int ld_slice = max(0, ws - ld.pos - kUnitCost);
     uint32_t issued = 0;
     int page = 0;
     bool more;
@@ -290,8 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_q(cur, q);
 
     while (cur.pos < we) {
-      const int first = (int)max(0ll, ws - cur.pos - kUnitCost);
-      const int last = (int)min((long long)cur.slices, we - cur.pos - kUnitCost);
+      const int first = max(0, ws - cur.pos - kUnitCost), last = min(cur.slices, we - cur.pos - kUnitCost);
       Cursor nxt = cur;
       advance(lens, nxt, units);
       uint32_t qn[D / 16][2 * kRowSets];             // the next unit's, under way meanwhile
@@ -428,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float2(o[i][2 * rs], o[i][2 * rs + 1]);
           if (quad == 0) stats[(2 * warp + part) * S::kRows + gq + 8 * rs] = make_float2(m[rs], l[rs]);
         }
-        if (lane == 0) open[2 * warp + part] = Open{cur.b, cur.u, cur.slices, 0, cur.pos};
+        if (lane == 0) open[2 * warp + part] = Open{cur.b, cur.u, cur.slices, cur.pos};
       }
       cur = nxt;
       if (kWide) {
@@ -447,9 +444,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
+  // --- rows without keys (with a prefix the merge kernel writes every row)
+  if (!t.p.row_o)
+    for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x)
+      if ((run == 1 ? window[s] : seq_len(a, s)) == 0) {
+        for (int i = threadIdx.x; i < a.Hq * (D / 8); i += kThreads)
+          reinterpret_cast<uint4*>(a.out + (long long)s * a.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int i = threadIdx.x; i < a.Hq; i += kThreads) a.lse[(long long)s * a.Hq + i] = -INFINITY;
+      }
+
   // --- join the warps' parts of units that cross their ranges: row r is
   // out = sum_w 2^{m_w - M} O_w / sum_w 2^{m_w - M} l_w.  The parts of a unit
   // follow one another in (warp, part) order.
+  int4 tail = make_int4(0, 0, 0, 0);             // the unit that goes on in the next block
 #pragma unroll 1
   for (int e = 0; e < 2 * kWarps; e = e == 0 ? 1 : e + 2) {      // part 0 of the first warp, part 1 of every warp
     const Open op = open[e];
@@ -458,9 +466,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Open other = open[2 * (lane & (kWarps - 1))];          // part 0 of the warps after it
     const int parts = 1 + __popc(__ballot_sync(0xffffffffu, lane < kWarps && lane > w0 && other.b == op.b &&
                                                                 other.u == op.u));
-    const long long begin = op.pos + kUnitCost;
+    const int begin = op.pos + kUnitCost;
     const bool whole = begin >= start && begin + op.slices <= end;
     const int slot = 2 * blockIdx.x + (begin < start ? 0 : 1);
+    if (begin >= start && !whole)
+      tail = make_int4(op.b, op.u, line.block_of(begin + op.slices - 1) - (int)blockIdx.x + 1, 0);
     const int hk = t.chunks == 1 ? op.u : op.u / t.chunks;
     const int h0 = hk * G + (op.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
@@ -509,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const int any_bad = __syncthreads_or(bad), any_late = __syncthreads_or(late);
+  if (threadIdx.x == 0) t.p.tail[blockIdx.x] = tail;
   if (threadIdx.x == 0) report(rep, blockIdx.x, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
   // launched beside the prefix's kernel: this grid ends after it, so that the
   // merge kernel, which waits for this one, finds the parts of both

@@ -20,11 +20,13 @@ constexpr int kBatch = 4;
 
 struct MergeArgs {
   AttnArgs a;
-  int splits;            // parts in row order: [splits, T * Hq]
+  int splits;            // parts in row order: [splits, T * Hq]; 0: decode without a prefix
   DecodeParts p;
   int chunks, grid;      // decode: units per key-value head, blocks of the kernel (0: prefill)
 };
 
+// Work: the rows, or, without parts in row order, the 16 rows of the unit that
+// each of the decode kernel's blocks leaves to the next one.
 template <int D, bool kF16>
 __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t) {
   constexpr int N = D / 32;            // elements per lane
@@ -33,23 +35,32 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
   pdl_wait();   // programmatic dependent launch: the parts are complete
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = (long long)a.T * a.Hq;
+  const int G = a.Hq / a.Hkv;
+  const long long rows = (long long)a.T * a.Hq, todo = t.splits ? rows : 16ll * t.grid;
 #pragma unroll 1
-  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+  for (long long i = blockIdx.x; i < todo; i += gridDim.x) {
     // blocks c0 .. c0 + own - 1 of the decode kernel hold the row's own keys
     int c0 = 0, own = 0, r = 0;
-    if (t.grid > 0) {
-      const int b = (int)(row / a.Hq), h = (int)(row % a.Hq), G = a.Hq / a.Hkv;
+    long long row = i;
+    if (!t.splits) {
+      c0 = (int)(i >> 4);
+      r = (int)(i & 15);
+      const int4 u = t.p.tail[c0];
+      const int hk = u.y / t.chunks, h = (u.y - hk * t.chunks) * 16 + r;
+      if (u.z == 0 || h >= G) continue;
+      own = u.z;
+      row = (long long)u.x * a.Hq + hk * G + h;
+    } else if (t.grid > 0) {
+      const int b = (int)(row / a.Hq), h = (int)(row - (long long)b * a.Hq);
       const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
       r = (h % G) % 16;
-      const long long total = t.p.base[a.n_seq], b0 = t.p.base[b], n = divide(t.p.base[b + 1] - b0, units);
+      const int total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
       if (n > 0) {
         const Line line(total, t.grid);
-        const long long at = b0 + u * n;
+        const int at = b0 + u * n;
         c0 = line.block_of(at + kUnitCost);
         own = line.block_of(at + n - 1) - c0 + 1;
       }
-      if (t.splits == 0 && own == 1) continue;       // final already
     }
     const int parts = t.splits + own;
     float m = -INFINITY, sum = 0.f, acc[N];
@@ -64,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
         lse[k] = -INFINITY;
         if (i >= parts) continue;
         const float *po, *pl;
-        if (i < t.splits || own == 1) {              // the row's own part follows the prefix's
+        if (i < t.splits || (t.splits && own == 1)) {      // the row's own part follows the prefix's
           const long long at = (long long)i * rows + row;
           po = t.p.tc_o + at * D;
           pl = t.p.tc_lse + at;
@@ -131,8 +142,8 @@ cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& 
   t.p = p;
   t.chunks = decode_chunks(a);
   t.grid = decode_grid;
-  const long long rows = (long long)a.T * a.Hq;
-  const unsigned grid = (unsigned)(rows < 2048 ? rows : 2048);
+  const long long todo = splits ? (long long)a.T * a.Hq : 16ll * decode_grid;
+  const unsigned grid = (unsigned)(todo < 2560 ? todo : 2560);
   auto kern = a.D == 64 ? (a.f16 ? attn_merge_kernel<64, true> : attn_merge_kernel<64, false>)
                         : (a.f16 ? attn_merge_kernel<128, true> : attn_merge_kernel<128, false>);
   return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, t);

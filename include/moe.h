@@ -454,6 +454,7 @@ int moe_attn_prefill_paged(const moe_heads *q, const moe_kv_cache *cache, const 
  * prefix_len is 0) followed by its own kv_lens[b] tokens on
  * page_table[b, 0 ..].  The prefix is read and multiplied once for the whole
  * batch.  A row without any key gets out = 0, lse = -inf.
+ * B * (table_pages * page_size / 16 + 1) * Hkv * ceil(G / 16) must stay below 2^31.
  */
 int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t *page_table,
                     int table_pages, const int32_t *kv_lens, const int32_t *prefix_table,

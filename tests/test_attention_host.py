@@ -124,6 +124,7 @@ def test_decode_refusals(lib):
     assert decode(lib, lens=None) == INVALID
     assert decode(lib, Hq=6, Hkv=4) == INVALID
     assert decode(lib, D=32) == UNSUPPORTED
+    assert decode(lib, wide=1 << 30, cache=C(pages=1 << 20)) == UNSUPPORTED   # 2^31 slices of 16 keys
     assert decode(lib, n=0) == WORKSPACE
 
 
