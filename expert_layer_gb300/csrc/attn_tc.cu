@@ -75,7 +75,8 @@ struct TcAttnArgs {
   int box;                       // rows of a K / V box
   float c;                       // scale log2 e, not 0
   float hidden;                  // a masked logit: c times it is -inf
-  float* part_o;                 // [splits, T, Hq, D], null when splits is 1
+  int out_box;                   // 32 rows of a tile are whole heads of whole tokens
+  float* part_o;                 // [splits, T, Hq, D], null when the result is final
   float* part_lse;               // [splits, T, Hq], log2
 };
 
@@ -236,7 +237,8 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 template <int D, bool kF16, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const TcAttnArgs t, const Report rep) {
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const TcAttnArgs t,
+                   const Report rep) {
   using S = Shape<D, kPaged>;
   constexpr int NS = S::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
@@ -265,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_map(&tmQ);
     prefetch_map(&tmK);
     prefetch_map(&tmV);
+    prefetch_map(&tmO);
   }
   pdl_trigger();   // a merge kernel, or the decode kernel beside it, may become resident
 
@@ -716,71 +719,91 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
       tc_fence_after();
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;     // l is NaN: so is the row
-      // A thread's row would go out in 16-byte pieces, each in a line of its
-      // own: 128 bytes of every row pass through shared memory (swizzled by
-      // row), and eight lanes then write a row's 128 bytes.
+      // 128 bytes of every row at a time pass through shared memory, swizzled as
+      // a copy box is.  A warp whose 32 rows are whole heads of whole tokens, all
+      // of this sequence, sends them with one bulk copy; others write them
+      // eight lanes to a row (a thread's own row in 16-byte pieces would touch a
+      // line with each).
       unsigned char* stage = smem + S::kOut + warp * 32 * 128;
       const int at = live ? token * a.Hq + g : -1;              // row's place after the tile's first
       const long long first = (long long)(it.row0 + x * t.tt) * a.Hq + it.head * G;
-      int to[8];                                                // places of the rows that this lane writes
-#pragma unroll
-      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
-      auto put = [&](int unit, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v; };
-      auto write = [&](unsigned char* out, int row_bytes) {
-        __syncwarp();
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          v[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (to[i] >= 0) *reinterpret_cast<uint4*>(out + (long long)to[i] * row_bytes) = v[i];
-        __syncwarp();
-      };
       const bool part = t.part_o != nullptr;
       if (part) {
         if (live) t.part_lse[(long long)it.split * a.T * a.Hq + first + at] = l > 0.f ? m + lg2(l) : l == 0.f ? -INFINITY : l;
       } else if (live && a.lse) {
         a.lse[first + at] = l > 0.f ? (m + lg2(l)) * 0.693147180559945f : l == 0.f ? -INFINITY : l;
       }
-      const int row_bytes = part ? D * 4 : D * 2;
-      unsigned char* out =
-          (part ? reinterpret_cast<unsigned char*>(t.part_o + (long long)it.split * a.T * a.Hq * D)
-                : reinterpret_cast<unsigned char*>(a.out)) + first * row_bytes + (lane & 7) * 16;
-      if (n > 0 || !part)                                                // a part without keys is not read
+      const bool boxed = t.out_box && __all_sync(0xffffffffu, live);
+      const int head0 = it.head * G + __shfl_sync(0xffffffffu, g, 0);
+      const int token0 = it.row0 + x * t.tt + __shfl_sync(0xffffffffu, token, 0) + (part ? it.split * a.T : 0);
+      auto put = [&](int unit, uint4 v) { *reinterpret_cast<uint4*>(stage + lane * 128 + ((unit ^ (lane & 7)) << 4)) = v; };
+      auto write = [&](int column, int row_bytes) {             // of the output, bytes of its rows
+        if (boxed) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) store_box(&tmO, stage, column, head0, token0);
+          return;
+        }
+        __syncwarp();
+        unsigned char* out =
+            (part ? reinterpret_cast<unsigned char*>(t.part_o + (long long)it.split * a.T * a.Hq * D)
+                  : reinterpret_cast<unsigned char*>(a.out)) +
+            first * row_bytes + column * (row_bytes / D) + (lane & 7) * 16;
+#pragma unroll 4
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), to = __shfl_sync(0xffffffffu, at, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(out + (long long)to * row_bytes) = v;
+        }
+        __syncwarp();
+      };
+      auto stage_free = [&]() {                                 // the bulk copies have read it
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+      };
+      if (part) {
+        if (n > 0)                                              // a part without keys is not read
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
-          float v[32];
-          if (n > 0) {
+          for (int i = 0; i < D; i += 32) {
+            float v[32];
             tmem_ld32(tO + i, *reinterpret_cast<uint32_t(*)[32]>(v));
             tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) v[u] = 0.f;
-          }
-#pragma unroll
-          for (int u = 0; u < 32; ++u) v[u] *= inv;
-          if (part) {
+            stage_free();
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-              put(u, make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
-                                __float_as_uint(v[4 * u + 3])));
+              put(u, make_uint4(__float_as_uint(v[4 * u] * inv), __float_as_uint(v[4 * u + 1] * inv),
+                                __float_as_uint(v[4 * u + 2] * inv), __float_as_uint(v[4 * u + 3] * inv)));
+            write(i, D * 4);
+          }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < D; i += 64) {
+          float v[64];
+          if (n > 0) {
+            tmem_ld64(tO + i, v);
+            tmem_wait_ld64(v);
           } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              put((i & 32) / 8 + u, make_uint4(pack2<kF16>(v[8 * u], v[8 * u + 1]), pack2<kF16>(v[8 * u + 2], v[8 * u + 3]),
-                                               pack2<kF16>(v[8 * u + 4], v[8 * u + 5]),
-                                               pack2<kF16>(v[8 * u + 6], v[8 * u + 7])));
-            if (!(i & 32)) continue;
+            for (int u = 0; u < 64; ++u) v[u] = 0.f;
           }
-          write(out + (part ? i * 4 : (i - 32) * 2), row_bytes);
+          uint4 w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            w[u] = make_uint4(pack2<kF16>(v[8 * u] * inv, v[8 * u + 1] * inv),
+                              pack2<kF16>(v[8 * u + 2] * inv, v[8 * u + 3] * inv),
+                              pack2<kF16>(v[8 * u + 4] * inv, v[8 * u + 5] * inv),
+                              pack2<kF16>(v[8 * u + 6] * inv, v[8 * u + 7] * inv));
+          stage_free();
+#pragma unroll
+          for (int u = 0; u < 8; ++u) put(u, w[u]);
+          write(i, D * 2);
         }
+      }
       tc_fence_before();
       if (*(volatile int*)abort_flag) { ok = false; break; }
     }
     if (!ok && lane == 0) atomicOr(abort_flag, 1);
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -801,14 +824,29 @@ bool q_map(CUtensorMap* m, const AttnArgs& a, int tt) {
   return encode(m, a.q.data, 3, dims, strides, box);
 }
 
+// 3-D map over the output, or over the parts in fp32: boxes of 32 rows x 128
+// bytes, heads fastest.
+int box_heads(const AttnArgs& a) {
+  const int G = a.Hq / a.Hkv;
+  return G < 32 ? G : G % 32 == 0 ? 32 : 33;
+}
+bool out_map(CUtensorMap* m, const AttnArgs& a, float* part_o, int splits) {
+  const cuuint64_t size = part_o ? 4 : 2, heads = box_heads(a);
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T * (part_o ? splits : 1)};
+  const cuuint64_t strides[2] = {a.D * size, (cuuint64_t)a.Hq * a.D * size};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)heads, (cuuint32_t)(32 / heads)};
+  return encode(m, part_o ? (const void*)part_o : a.out, 3, dims, strides, box,
+                part_o ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+}
+
 template <int D, bool kF16, bool kPaged>
 cudaError_t launch(const TcAttnArgs& t, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                   const Report& rep, int grid, cudaStream_t stream) {
+                   const CUtensorMap& o, const Report& rep, int grid, cudaStream_t stream) {
   auto kern = attn_tc_kernel<D, kF16, kPaged>;
   constexpr size_t smem = Shape<D, kPaged>::kSmem;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kThreads, smem, stream>>>(q, k, v, t, rep);
+  kern<<<grid, kThreads, smem, stream>>>(q, k, v, o, t, rep);
   return cudaGetLastError();
 }
 
@@ -848,15 +886,18 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.part_o = part_o;
   t.part_lse = part_lse;
   const bool paged = a.page_table != nullptr;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o = {};
   if (!q_map(&q, a, t.tt)) return cudaErrorInvalidValue;
+  // (parts of all splits are one tensor of splits * T tokens)
+  t.out_box = 32 % box_heads(a) == 0 && (long long)a.T * splits < (1ll << 31);
+  if (t.out_box && !out_map(&o, a, part_o, splits)) return cudaErrorInvalidValue;
   if (paged ? !pages_map(&k, a.k_cache, a, t.box) || !pages_map(&v, a.v_cache, a, t.box)
             : !rows_map(&k, a.k, a, a.Tk, a.Hkv, kKeys) || !rows_map(&v, a.v, a, a.Tk, a.Hkv, kKeys))
     return cudaErrorInvalidValue;
   Report rep = shape;
   rep.blocks[rep.set] = items;
 #define TC_CASE(DD, F, P) \
-  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, rep, items, stream);
+  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, o, rep, items, stream);
   TC_CASE(64, false, false)
   TC_CASE(64, false, true)
   TC_CASE(64, true, false)
