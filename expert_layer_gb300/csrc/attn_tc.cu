@@ -355,6 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         it = Item{};
         it.row0 = -1;
       }
+      const int32_t* list = nullptr;
+      if (kPaged) list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
+      // page of this lane's box in block b (lanes 0 .. boxes-1)
+      auto fetch = [&](int b) {
+        const int key = b * kKeys + lane * t.box;
+        return kPaged && lane < boxes && key < it.len ? list[key >> a.page_shift] : 0;
+      };
+      auto checked = [&](int p) {
+        if (!kPaged || (unsigned)p < (unsigned)a.pages) return p;
+        bad = true;
+        return 0;
+      };
+      int page = it.n[0] + it.n[1] > 0 && !end ? fetch(it.b0) : 0;       // under way while Q is loaded
       const int slot = ni % kItems;
       if (!warp_spin(&it_empty[slot], ((ni / kItems) & 1) ^ 1)) { ok = false; break; }
       if (lane == 0) {
@@ -364,18 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ni;
       if (end) break;
       const int n = max(it.n[0], it.n[1]);
-      const int32_t* list = nullptr;
-      if (kPaged) list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
-      // page of this lane's box in block b (lanes 0 .. boxes-1)
-      auto page_of = [&](int b) {
-        const int key = b * kKeys + lane * t.box;
-        if (!kPaged || lane >= boxes || key >= it.len) return 0;
-        const int p = list[key >> a.page_shift];
-        if ((unsigned)p < (unsigned)a.pages) return p;
-        bad = true;
-        return 0;
-      };
-      int page = n > 0 ? page_of(it.b0) : 0;
       if (n <= kAskAhead) ask();
 #pragma unroll
       for (int x = 0; x < 2; ++x)
@@ -391,7 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       for (int j = 0; j < n && ok; ++j) {
         const int b = it.b0 + j;
-        const int next = j + 1 < n ? page_of(b + 1) : 0;
+        page = checked(page);
+        const int next = j + 1 < n ? fetch(b + 1) : 0;
         if (j > 0 && n - j == kAskAhead) ask();
         // boxes that hold keys of the sequence; the rest of the tile is not read
         const int nbox = min(boxes, (it.len - b * kKeys + t.box - 1) / t.box);
@@ -858,7 +860,9 @@ int tc_splits(const AttnArgs& a, int num_sms) {
   const long long keys = a.prefix_table ? a.prefix_len : a.page_table ? (long long)a.table_pages << a.page_shift : a.Tk;
   const long long blocks = (keys + kKeys - 1) / kKeys;
   long long s = num_sms / units;
-  if (s > blocks / kBlocksPerSplit) s = blocks / kBlocksPerSplit;
+  // (a prefix's parts are joined with the rows' own keys anyway)
+  const int least = a.prefix_table ? 1 : kBlocksPerSplit;
+  if (s > blocks / least) s = blocks / least;
   return s < 1 ? 1 : (int)s;
 }
 
