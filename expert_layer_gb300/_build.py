@@ -1,4 +1,5 @@
-"""Builds libmoe_gb300.so in-tree with nvcc for sm_103a.
+"""Builds libmoe_gb300.so in-tree with nvcc for sm_103a, and the Python binding
+of the attention functions (_attn_binding.so) with the host compiler.
 
 Each .cu file under csrc/ compiles to its own object (in parallel); the
 objects link into expert_layer_gb300/libmoe_gb300.so.  A file is recompiled
@@ -39,6 +40,40 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def build_binding(verbose: bool = False) -> str:
+    """Compile the extension module of the attention functions (host C++ against
+    this PyTorch's headers); returns its path.  Rebuilt when its source, the
+    C header, PyTorch or Python changed."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "attn_binding.cpp")
+    out = os.path.join(PKG, "_attn_binding.so")
+    made_for = os.path.join(BUILD, "attn_binding.for")
+    this = f"{torch.__version__} {torch.__file__} {sysconfig.get_config_var('EXT_SUFFIX')}"
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "moe.h")))
+    if os.path.exists(out) and os.path.getmtime(out) >= newest and os.path.exists(made_for):
+        with open(made_for) as f:
+            if f.read() == this:
+                return out
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(at, "include"),
+           "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", out,
+           "-L", os.path.join(at, "lib"), "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(made_for, "w") as f:
+        f.write(this)
+    return out
+
+
 def build(verbose: bool = False, extra_flags: list[str] | None = None, build_dir: str | None = None,
           lib_path: str | None = None) -> str:
     """Compile and link the library; returns its path.  ``extra_flags`` go to
@@ -66,7 +101,10 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None, build_dir
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = None if lib_path else ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
+        if binding is not None:
+            binding.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

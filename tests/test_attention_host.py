@@ -2,12 +2,13 @@
 of these calls reaches a GPU), workspace sizes, and the rotary table."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
 
 import expert_layer_gb300 as moe
-from expert_layer_gb300 import _build, attention
+from expert_layer_gb300 import _build
 
 P = ctypes.c_void_p
 INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
@@ -20,11 +21,11 @@ def lib():
 
 
 def H(ptr=1 << 20, tok=512, head=128):
-    return attention._HEADS(ptr, tok, head)
+    return struct.pack("=Qqq", ptr, tok, head)          # moe_heads
 
 
 def C(k=1 << 20, v=1 << 20, pages=8, size=16):
-    return attention._CACHE(k, v, pages, size)
+    return struct.pack("=QQii", k, v, pages, size)      # moe_kv_cache
 
 
 FAKE, MIS = P(1 << 20), P((1 << 20) + 2)      # never dereferenced: every case fails on the host
@@ -150,6 +151,14 @@ def test_binding_rejects_before_the_library(lib):
         moe.attn_decode(q.float(), c, c, i[None], i)
     with pytest.raises(moe.MoEError, match="Tensor"):
         moe.rope_append(None, q, q, q, i, i, c, c)
+    with pytest.raises(TypeError, match="kv_lens"):
+        moe.attn_decode(q, c, c, i[None])
+    with pytest.raises(TypeError, match="unexpected"):
+        moe.attn_decode(q, c, c, i[None], i, softcap=3.0)
+    with pytest.raises(TypeError, match="repeated"):
+        moe.attn_prefill(q, q, q, i, i, q_starts=i)
+    with pytest.raises(TypeError, match="at most"):
+        moe.attn_prefill(*([q] * 12))
 
 
 def test_rope_table_values():
