@@ -92,15 +92,15 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
       float top = m;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) top = fmaxf(top, lse[k]);
-      if (top == -INFINITY) continue;
-      const float f = ex2(m - top);
+      const float zero = top == -INFINITY ? 0.f : top;    // parts that are all NaN have no maximum, and stay NaN
+      const float f = ex2(m - zero);
       sum *= f;
 #pragma unroll
       for (int j = 0; j < N; ++j) acc[j] *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (lse[k] == -INFINITY) continue;
-        const float w = ex2(lse[k] - top);
+        const float w = ex2(lse[k] - zero);
         sum += w;
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[j] = fmaf(w, o[k][j], acc[j]);
@@ -115,14 +115,13 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
       float top = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w].x);
-      if (top != -INFINITY) {
+      if (top == -INFINITY) top = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2(s_ml[w].x - top);
-          l = fmaf(f, s_ml[w].y, l);
-          x = fmaf(f, s_o[w][2 * threadIdx.x], x);
-          y = fmaf(f, s_o[w][2 * threadIdx.x + 1], y);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_ml[w].x - top);
+        l = fmaf(f, s_ml[w].y, l);
+        x = fmaf(f, s_o[w][2 * threadIdx.x], x);
+        y = fmaf(f, s_o[w][2 * threadIdx.x + 1], y);
       }
       const float inv = l > 0.f ? 1.0f / l : l;      // no keys: 0; NaN stays
       reinterpret_cast<uint32_t*>(a.out + row * D)[threadIdx.x] = pack2<kF16>(x * inv, y * inv);

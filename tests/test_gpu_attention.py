@@ -369,6 +369,20 @@ def test_decode(case):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("kv_lens,prefix", [([40], 0), ([9000], 0), ([300, 0, 5000], 512), ([0, 17], 4096)])
+def test_decode_nan_query_stays_in_its_head(kv_lens, prefix):
+    # a NaN that a row does see is in its result, whether the row's keys are in
+    # one piece or joined from parts, and in no other head's
+    q, kc, vc, table, pre = decode_case(kv_lens, prefix, 16, 2, 128, 16, BF)
+    q[:, 5, 3] = float("nan")
+    lse = torch.empty(len(kv_lens), 16, device="cuda")
+    out = moe.attn_decode(q, kc, vc, table, ints(kv_lens), pre, prefix, lse=lse)
+    sees = torch.tensor([n + prefix > 0 for n in kv_lens], device="cuda")
+    assert bool(out[sees, 5].isnan().all()) and bool(lse[sees, 5].isnan().all())
+    others = [h for h in range(16) if h != 5]
+    assert not bool(out[:, others].isnan().any()) and not bool(lse[:, others].isnan().any())
+
+
 def test_decode_strided_rows_and_scale():
     q, kc, vc, table, _ = decode_case([90, 200], 0, 8, 2, 64, 16, BF)
     wide = torch.zeros(2, 8 * 64 + 72, dtype=BF, device="cuda")
