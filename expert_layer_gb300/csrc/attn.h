@@ -137,6 +137,10 @@ inline TcPlan tc_plan(const AttnArgs& a) {
 }
 // Parts that a call splits each row's keys into (1: none, the result is final)
 constexpr int kBlocksPerSplit = 4;
+// A shared prefix leaves this share of the SMs to the rows' own keys, which are
+// read meanwhile (64 sequences with 50 to 700 keys of their own after 16,384
+// shared ones: 41 -> 33.4 us, after 512: 26.5 -> 21.5; after 65,536: 71 -> 73)
+constexpr int kOwnShare = 6;
 int tc_splits(const AttnArgs& a, int num_sms);
 int tc_items(const AttnArgs& a, int splits);      // blocks of the grid; -1: too many
 cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* part_lse, const Report& rep,
@@ -162,26 +166,49 @@ struct DecodeParts {
 // A unit costs its warp about as much as one 16-key slice besides its slices
 // (queries, the end of the softmax): 64 sequences of 1 to 8192 keys
 constexpr int kUnitCost = 1;
-// The line of all units' places, cut into equal ranges for the warps of as many
+// The line of all units' places, cut into ranges for the warps of as many
 // blocks as have a place for each of their eight warps (up to the grid).  Its
 // length is below 2^31 (decode_fits), which keeps the start of the kernel free
 // of 64-bit divisions: code that runs once is fetched from L2 as it runs.
+// With a shared prefix the first `few` blocks run beside its kernel, and their
+// warps take up to `head` places, what they get through meanwhile; the others
+// come after it and share the rest.
 struct Line {
-  int each;            // places per warp; the first `more` warps have one more
+  int few, head;       // leading blocks and their places per warp (0: none)
+  int each;            // places per warp of the others; the first `more` warps have one more
   int blocks, more;
-  __host__ __device__ Line(int total, int grid) {
-    const int n = total / 8 + (total % 8 != 0);
-    blocks = n < 1 ? 1 : n < grid ? n : grid;
-    each = total / (blocks * 8);
-    more = total - each * (blocks * 8);
+  __host__ __device__ Line(int total, int grid, int few_, int head_) : few(few_), head(head_) {
+    if (few > 0 && total / (8 * few) < head) grid = few;       // the leading blocks are enough
+    if (few == 0 || grid == few) few = head = 0;
+    const int rest = total - few * head * 8;
+    const int n = rest / 8 + (rest % 8 != 0), most = grid - few;
+    const int own = n < 1 ? 1 : n < most ? n : most;
+    blocks = few + own;
+    each = rest / (own * 8);
+    more = rest - each * (own * 8);
   }
   // first place of warp g (of all blocks')
-  __host__ __device__ int at(int g) const { return each * g + (g < more ? g : more); }
+  __host__ __device__ int at(int g) const {
+    const int i = g - few * 8;
+    return i < 0 ? g * head : few * 8 * head + each * i + (i < more ? i : more);
+  }
   // block of a place
   __host__ __device__ int block_of(int place) const {
-    const int cut = (each + 1) * more;
-    return (place < cut ? place / (each + 1) : more + (place - cut) / each) / 8;
+    const int p = place - few * 8 * head, cut = (each + 1) * more;
+    if (p < 0) return place / (8 * head);
+    return few + (p < cut ? p / (each + 1) : more + (p - cut) / each) / 8;
   }
+};
+// The decode kernel beside that of a shared prefix: blocks that find room while
+// it runs, and the places that each of their warps gets through: an SM reads
+// ~100 GB/s by itself, and the other kernel takes ~1.6 us per 128 keys of its
+// longest part and 8 us besides.  (With all blocks alike, the second round of
+// them cost more than the first saved: 16,384 shared keys before 1 to 8192 own
+// ones 67 us, now 45, one kernel after the other 53.)
+constexpr int kHeadFixed = 5, kHeadPerBlock = 3;
+struct Beside {
+  bool prefix;
+  int few, head;
 };
 // Units of at most 16 heads per key-value head
 inline int decode_chunks(const AttnArgs& a) { return (a.Hq / a.Hkv + 15) / 16; }
@@ -190,12 +217,12 @@ inline bool decode_fits(const AttnArgs& a) {
   const long long slices = ((((long long)a.table_pages << a.page_shift) + 15) / 16 + kUnitCost) * a.Hkv * decode_chunks(a);
   return slices < (1ll << 31) && slices * a.n_seq < (1ll << 31);
 }
-cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& rep, int num_sms,
-                               cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const DecodeParts& p, const Report& rep,
+                               int num_sms, cudaStream_t stream);
 
 // attn_merge.cu -- joins the parts of every row (decode_grid 0: prefill)
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
-                              cudaStream_t stream);
+                              const Beside& beside, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace moe

@@ -115,17 +115,21 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
   p.base = ws_ptr<int32_t>(ws, L.base);
   Report rep{ws, 0, {sms, 0}};
   int splits = 0;
+  Beside beside{};
   if (a.prefix_len > 0) {
     splits = tc_splits(a, sms);
     rep.set = 1;
     rep.blocks[1] = tc_items(a, splits);
     ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, s)));
+    beside.prefix = true;
+    beside.few = rep.blocks[1] < sms ? sms - rep.blocks[1] : 0;
+    beside.head = kHeadFixed + kHeadPerBlock * (((a.prefix_len + 127) / 128 + splits - 1) / splits);
     p.row_o = p.tc_o + (long long)splits * a.T * a.Hq * a.D;
     p.row_lse = p.tc_lse + (long long)splits * a.T * a.Hq;
   }
   rep.set = 0;
-  ATTN_TRY(cuda_status(launch_attn_decode(a, splits > 0, p, rep, sms, s)));
-  return cuda_status(launch_attn_merge(a, splits, p, sms, s));
+  ATTN_TRY(cuda_status(launch_attn_decode(a, beside, p, rep, sms, s)));
+  return cuda_status(launch_attn_merge(a, splits, p, sms, beside, s));
 }
 
 // The checks shared by the three attention calls, in the order of the others
@@ -154,7 +158,7 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   p.tc_o = ws_ptr<float>(workspace, L.part_o);
   p.tc_lse = ws_ptr<float>(workspace, L.part_lse);
   ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, s)));
-  return cuda_status(launch_attn_merge(a, splits, p, 0, s));
+  return cuda_status(launch_attn_merge(a, splits, p, 0, Beside{}, s));
 }
 
 }  // namespace

@@ -66,6 +66,7 @@ struct DecodeArgs {
   float c;              // |scale| log2 e, > 0
   uint32_t flip;        // sign bits of two elements when the scale is negative
   int chunks;           // units per key-value head
+  int few, head;        // of Line
   DecodeParts p;
 };
 
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == kThreads - 1) t.p.base[a.n_seq] = total;
   }
-  const Line line(total, gridDim.x);
+  const Line line(total, gridDim.x, t.few, t.head);
   const int start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
   const bool work = (int)blockIdx.x < line.blocks && start < end;
   if (work && start >= before && start < before + mine) {
@@ -522,8 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) t.p.tail[blockIdx.x] = tail;
   if (threadIdx.x == 0) report(rep, blockIdx.x, (any_bad ? kStatusBounds : 0) | (any_late ? kStatusTimeout : 0));
   // launched beside the prefix's kernel: this grid ends after it, so that the
-  // merge kernel, which waits for this one, finds the parts of both
-  pdl_wait();
+  // merge kernel, which waits for this one, finds the parts of both (one block
+  // waits; the others leave their SMs to blocks that have not started)
+  if (blockIdx.x == 0) pdl_wait();
 }
 
 template <int D, bool kF16, bool kWide>
@@ -542,8 +544,8 @@ cudaError_t launch(const DecodeArgs& t, const CUtensorMap& k, const CUtensorMap&
 
 // beside: the kernel before this one on the stream is the prefix's, on which
 // nothing here depends
-cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts& p, const Report& shape, int num_sms,
-                               cudaStream_t stream) {
+cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const DecodeParts& p, const Report& shape,
+                               int num_sms, cudaStream_t stream) {
   DecodeArgs t{};
   t.a = a;
   t.c = (a.scale < 0 ? -a.scale : a.scale) * 1.4426950408889634f;
@@ -551,6 +553,8 @@ cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts
   t.flip = a.scale < 0 ? 0x80008000u : 0u;
   const int G = a.Hq / a.Hkv;
   t.chunks = decode_chunks(a);
+  t.few = beside.few;
+  t.head = beside.head;
   t.p = p;
   CUtensorMap k, v;
   if (!pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice)) return cudaErrorInvalidValue;
@@ -558,7 +562,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, bool beside, const DecodeParts
   rep.blocks[rep.set] = num_sms;
   const bool wide = G > 8;
 #define DECODE_CASE(DD, F, W) \
-  if (a.D == DD && (a.f16 != 0) == F && wide == W) return launch<DD, F, W>(t, k, v, rep, beside, num_sms, stream);
+  if (a.D == DD && (a.f16 != 0) == F && wide == W) return launch<DD, F, W>(t, k, v, rep, beside.prefix, num_sms, stream);
   DECODE_CASE(64, false, false)
   DECODE_CASE(64, false, true)
   DECODE_CASE(64, true, false)

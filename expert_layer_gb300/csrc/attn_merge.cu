@@ -14,8 +14,7 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 4;
 constexpr int kBatch = 6;            // 16k shared prefix, 19 parts a row: 4, 6, 8: 41.2, 40.3, 41.3 us a call
 
 struct MergeArgs {
@@ -23,46 +22,54 @@ struct MergeArgs {
   int splits;            // parts in row order: [splits, T * Hq]; 0: decode without a prefix
   DecodeParts p;
   int chunks, grid;      // decode: units per key-value head, blocks of the kernel (0: prefill)
+  int few, head;         // of Line
+  unsigned rows;         // decode without a prefix: rows of a unit, at most 16
+  unsigned todo;         // rows to write
 };
 
-// Work: the rows, or, without parts in row order, the 16 rows of the unit that
-// each of the decode kernel's blocks leaves to the next one.
+// Work: the rows, or, without parts in row order, the rows of the units that
+// cross the decode kernel's blocks, at most one for each block.  (With 16 rows a
+// unit whatever G, the blocks took two rounds: 64 sequences of 1466 keys, G = 8,
+// 40.2 us against 39.0.)
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t) {
+__global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs t) {
   constexpr int N = D / 32;            // elements per lane
   __shared__ float s_o[kWarps][D];
   __shared__ float2 s_ml[kWarps];
-  pdl_wait();   // programmatic dependent launch: the parts are complete
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
-  const long long rows = (long long)a.T * a.Hq, todo = t.splits ? rows : 16ll * t.grid;
+  const long long rows = (long long)a.T * a.Hq;
+  pdl_wait();   // programmatic dependent launch: the parts are complete
 #pragma unroll 1
-  for (long long i = blockIdx.x; i < todo; i += gridDim.x) {
+  for (unsigned i = blockIdx.x; i < t.todo; i += gridDim.x) {
     // blocks c0 .. c0 + own - 1 of the decode kernel hold the row's own keys
-    int c0 = 0, own = 0, r = 0;
+    int c0 = 0, own = 0, r = 0, parts = 0;
     long long row = i;
     if (!t.splits) {
-      c0 = (int)(i >> 4);
-      r = (int)(i & 15);
+      c0 = (int)(i / t.rows);
+      r = (int)(i - c0 * t.rows);
       const int4 u = t.p.tail[c0];
       const int hk = u.y / t.chunks, h = (u.y - hk * t.chunks) * 16 + r;
       if (u.z == 0 || h >= G) continue;
-      own = u.z;
+      parts = own = u.z;
       row = (long long)u.x * a.Hq + hk * G + h;
-    } else if (t.grid > 0) {
-      const int b = (int)(row / a.Hq), h = (int)(row - (long long)b * a.Hq);
-      const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
-      r = (h % G) % 16;
-      const int total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
-      if (n > 0) {
-        const Line line(total, t.grid);
-        const int at = b0 + u * n;
-        c0 = line.block_of(at + kUnitCost);
-        own = line.block_of(at + n - 1) - c0 + 1;
+    } else {
+      parts = t.splits;
+      if (t.grid > 0) {
+        const int b = (int)(i / a.Hq), h = (int)(i - (unsigned)b * a.Hq);
+        const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
+        r = (h % G) % 16;
+        const int total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
+        if (n > 0) {
+          const Line line(total, t.grid, t.few, t.head);
+          const int at = b0 + u * n;
+          c0 = line.block_of(at + kUnitCost);
+          own = line.block_of(at + n - 1) - c0 + 1;
+          parts += own;
+        }
       }
     }
-    const int parts = t.splits + own;
     float m = -INFINITY, sum = 0.f, acc[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.f;
@@ -72,8 +79,6 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k * kWarps;
-        lse[k] = -INFINITY;
-        if (i >= parts) continue;
         const float *po, *pl;
         if (i < t.splits || (t.splits && own == 1)) {      // the row's own part follows the prefix's
           const long long at = (long long)i * rows + row;
@@ -85,9 +90,9 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
           po = t.p.slot_o + at * D;
           pl = t.p.slot_lse + at;
         }
-        lse[k] = *pl;
+        lse[k] = i < parts ? *pl : -INFINITY;
 #pragma unroll
-        for (int j = 0; j < N; ++j) o[k][j] = po[lane * N + j];
+        for (int j = 0; j < N; ++j) o[k][j] = i < parts ? po[lane * N + j] : 0.f;
       }
       float top = m;
 #pragma unroll
@@ -99,11 +104,11 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
       for (int j = 0; j < N; ++j) acc[j] *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (lse[k] == -INFINITY) continue;
+        const bool none = lse[k] == -INFINITY;
         const float w = ex2(lse[k] - zero);
         sum += w;
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = fmaf(w, o[k][j], acc[j]);
+        for (int j = 0; j < N; ++j) acc[j] = fmaf(w, none ? 0.f : o[k][j], acc[j]);
       }
       m = top;
     }
@@ -111,8 +116,9 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
     for (int j = 0; j < N; ++j) s_o[warp][lane * N + j] = acc[j];
     if (lane == 0) s_ml[warp] = make_float2(m, sum);
     __syncthreads();
-    if (threadIdx.x < D / 2) {
-      float top = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
+    const int x = threadIdx.x;
+    if (x < D / 2) {
+      float top = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w].x);
       if (top == -INFINITY) top = 0.f;
@@ -120,12 +126,14 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_ml[w].x - top);
         l = fmaf(f, s_ml[w].y, l);
-        x = fmaf(f, s_o[w][2 * threadIdx.x], x);
-        y = fmaf(f, s_o[w][2 * threadIdx.x + 1], y);
+        o0 = fmaf(f, s_o[w][2 * x], o0);
+        o1 = fmaf(f, s_o[w][2 * x + 1], o1);
       }
       const float inv = l > 0.f ? 1.0f / l : l;      // no keys: 0; NaN stays
-      reinterpret_cast<uint32_t*>(a.out + row * D)[threadIdx.x] = pack2<kF16>(x * inv, y * inv);
-      if (a.lse && threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (top + lg2(l)) * 0.693147180559945f;
+      const uint32_t out = pack2<kF16>(o0 * inv, o1 * inv);
+      const float lse = l == 0.f ? -INFINITY : (top + lg2(l)) * 0.693147180559945f;
+      reinterpret_cast<uint32_t*>(a.out + row * D)[x] = out;
+      if (a.lse && x == 0) a.lse[row] = lse;
     }
     __syncthreads();
   }
@@ -134,18 +142,21 @@ __global__ void __launch_bounds__(kThreads) attn_merge_kernel(const MergeArgs t)
 }  // namespace
 
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
-                              cudaStream_t stream) {
+                              const Beside& beside, cudaStream_t stream) {
   MergeArgs t{};
   t.a = a;
   t.splits = splits;
   t.p = p;
   t.chunks = decode_chunks(a);
   t.grid = decode_grid;
-  const long long todo = splits ? (long long)a.T * a.Hq : 16ll * decode_grid;
-  const unsigned grid = (unsigned)(todo < 2560 ? todo : 2560);
+  t.few = beside.few;
+  t.head = beside.head;
+  const int G = a.Hq / a.Hkv;
+  t.rows = G < 16 ? G : 16;
+  t.todo = splits ? (unsigned)a.T * a.Hq : t.rows * decode_grid;
   auto kern = a.D == 64 ? (a.f16 ? attn_merge_kernel<64, true> : attn_merge_kernel<64, false>)
                         : (a.f16 ? attn_merge_kernel<128, true> : attn_merge_kernel<128, false>);
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, t);
+  return launch_pdl(kern, dim3(t.todo < 2560 ? t.todo : 2560), dim3(kWarps * 32), 0, stream, t);
 }
 
 }  // namespace attn

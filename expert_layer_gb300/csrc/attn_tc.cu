@@ -859,7 +859,8 @@ int tc_splits(const AttnArgs& a, int num_sms) {
   const long long units = (long long)p.slots * a.Hkv;
   const long long keys = a.prefix_table ? a.prefix_len : a.page_table ? (long long)a.table_pages << a.page_shift : a.Tk;
   const long long blocks = (keys + kKeys - 1) / kKeys;
-  long long s = num_sms / units;
+  // (a shared prefix leaves SMs to the rows' own keys)
+  long long s = (a.prefix_table ? num_sms - num_sms / kOwnShare : num_sms) / units;
   // (a prefix's parts are joined with the rows' own keys anyway)
   const int least = a.prefix_table ? 1 : kBlocksPerSplit;
   if (s > blocks / least) s = blocks / least;
