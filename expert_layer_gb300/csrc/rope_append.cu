@@ -15,6 +15,13 @@
 // token, for which cos, sin and the norm's weights are combined once:
 //   a' = r (a (w_a cos) - b (w_b sin)),  b' = r (b (w_b cos) + a (w_a sin)),
 //   r = 1 / sqrt(mean x^2 + eps)
+// The grid is what the GPU holds at once (twice that: 8192 tokens of 32 + 2 x 4
+// heads of 128, 33.0 us instead of 32.4), four heads to a group (eight: 32.0,
+// but 64-wide heads 19.4 instead of 18.0 us), four elements to a load (eight,
+// with half the lanes and twice the registers: 36.9).
+// Measured: 1 token 2.2 us, 256 tokens 3.3, 8192 tokens 32.4 us = 5.3 TB/s, 78%
+// of a copy's rate; 16,384 tokens 60.2 us = 5.7 TB/s (a call of 172 MB starts
+// and ends in 7 us).
 #include "attn.h"
 #include "attn_ptx.cuh"
 
@@ -23,38 +30,45 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMany = 4;            // heads per group of lanes once there are enough of them
+constexpr int kResident = 4;        // blocks of an SM, all that run: 64 registers a thread
 
+// Two elements to fp32 and back
 template <bool kF16>
-__device__ __forceinline__ void unpack4(uint2 v, float* x) {
-  const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (kF16) {
-      asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
-          : "=f"(x[2 * j]), "=f"(x[2 * j + 1])
-          : "r"(w[j]));
-    } else {
-      x[2 * j] = bf16lo(w[j]);
-      x[2 * j + 1] = bf16hi(w[j]);
-    }
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  float x, y;
+  if (kF16) {
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+        : "=f"(x), "=f"(y)
+        : "r"(w));
+  } else {
+    x = bf16lo(w);
+    y = bf16hi(w);
   }
+  return pair(x, y);
 }
-template <bool kF16>
-__device__ __forceinline__ uint2 pack4(const float* x) {
-  return make_uint2(pack2<kF16>(x[0], x[1]), pack2<kF16>(x[2], x[3]));
-}
+
+// Four consecutive elements
+struct Part {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
+};
 
 // Items: (token, kHeads consecutive heads of q, of k or of v).
 template <int D, int kHeads, bool kF16, bool kInter>
-__global__ void __launch_bounds__(kThreads, kHeads > 1 ? 4 : 1) rope_append_kernel(const RopeArgs a, const Report rep) {
-  constexpr int kLanes = D / 8, kGroups = kThreads / kLanes;
-  constexpr int kBatch = kHeads < 4 ? kHeads : 4;       // rows whose loads are in flight together
+__global__ void __launch_bounds__(kThreads, kResident)
+    rope_append_kernel(const RopeArgs a, const Report rep) {
+  constexpr int kPart = 4, kLanes = D / (2 * kPart), kGroups = kThreads / kLanes;
   const int gl = threadIdx.x % kLanes;                  // lane of the group
   const unsigned cq = (a.Hq + kHeads - 1) / kHeads, ck = (a.Hkv + kHeads - 1) / kHeads, chunks = cq + 2 * ck;
   const unsigned long long items = (unsigned long long)a.T * chunks;
   const int half = a.rot / 2;
-  const bool turns = 8 * gl < a.rot;
-  const int o1 = kInter ? 8 * gl : turns ? 4 * gl : 8 * gl, o2 = kInter || !turns ? o1 + 4 : half + 4 * gl;
+  const bool turns = 2 * kPart * gl < a.rot;
+  const int o1 = kInter || !turns ? 2 * kPart * gl : kPart * gl, o2 = kInter || !turns ? o1 + kPart : half + o1;
   const bool norms = a.q_norm || a.k_norm;
   bool bad = false;
   // the trip count is the same for the lanes of a warp: shuffles below
@@ -73,18 +87,15 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 4 : 1) rope_append_kern
     const Heads& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
     const uint16_t* in = src.data + t * src.tok + h0 * src.head;
     const long long in_step = src.head;
-    uint2 raw[kBatch][2];
-    auto load = [&](int i0) {
+    Part raw[kHeads][2];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (i0 + i < n) {
-          raw[i][0] = *reinterpret_cast<const uint2*>(in + (i0 + i) * in_step + o1);
-          raw[i][1] = *reinterpret_cast<const uint2*>(in + (i0 + i) * in_step + o2);
-        } else {
-          raw[i][0] = raw[i][1] = make_uint2(0, 0);
-        }
-    };
-    load(0);
+    for (int i = 0; i < kHeads; ++i)
+      if (i < n) {
+        raw[i][0].load(in + i * in_step + o1);
+        raw[i][1].load(in + i * in_step + o2);
+      } else {
+        raw[i][0] = raw[i][1] = Part{};
+      }
     bool ok = live;
     if ((unsigned)pos >= (unsigned)a.max_pos) {
       bad |= live;
@@ -103,16 +114,16 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 4 : 1) rope_append_kern
     }
     const float* weight = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
     // coefficients: y_j = x_j c_j + partner(x_j) s_j
-    float c[8], s[8];
+    float c[2 * kPart], s[2 * kPart];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = weight ? weight[(j < 4 ? o1 : o2) + (j & 3)] : 1.0f;
+    for (int j = 0; j < 2 * kPart; ++j) c[j] = weight ? weight[(j < kPart ? o1 : o2) + j % kPart] : 1.0f, s[j] = 0.f;
     if (turns) {
-      const float* row = a.table + (long long)pos * a.rot + 4 * gl;
+      const float* row = a.table + (long long)pos * a.rot + kPart * gl;
       const float4 cc = *reinterpret_cast<const float4*>(row), ss = *reinterpret_cast<const float4*>(row + half);
       const float co[4] = {cc.x, cc.y, cc.z, cc.w}, si[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int p = kInter ? 2 * j : j, q = kInter ? 2 * j + 1 : j + 4;   // the pair's two elements
+      for (int j = 0; j < kPart; ++j) {
+        const int p = kInter ? 2 * j : j, q = kInter ? p + 1 : p + kPart;   // the pair's two elements
         s[p] = -si[j] * c[q];
         s[q] = si[j] * c[p];
         c[p] *= co[j];
@@ -120,33 +131,35 @@ __global__ void __launch_bounds__(kThreads, kHeads > 1 ? 4 : 1) rope_append_kern
       }
     }
 #pragma unroll
-    for (int i0 = 0; i0 < kHeads; i0 += kBatch) {
-      if (i0) load(i0);
+    for (int i = 0; i < kHeads; ++i) {
+      uint64_t x[kPart];             // pairs of neighbours
+      float r = 1.0f;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        float x[8], y[8], r = 1.0f;
-        unpack4<kF16>(raw[i][0], x);
-        unpack4<kF16>(raw[i][1], x + 4);
-        if (norms) {
-          float sum = 0.f;
+      for (int j = 0; j < kPart; ++j) x[j] = unpack2<kF16>(raw[i][j / (kPart / 2)].w[j % (kPart / 2)]);
+      if (norms) {
+        uint64_t sum2 = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+        for (int j = 0; j < kPart; ++j) sum2 = fma2(x[j], x[j], sum2);
+        float sum = lo(sum2) + hi(sum2);
 #pragma unroll
-          for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, kLanes);
-          if (weight) r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
-        }
-        if (turns) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = fmaf(x[kInter ? j ^ 1 : j ^ 4], s[j], x[j] * c[j]) * r;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = x[j] * c[j] * r;
-        }
-        if (!ok || i0 + i >= n) continue;
-        uint16_t* dst = out + (i0 + i) * out_step;
-        *reinterpret_cast<uint2*>(dst + o1) = kind == 2 ? raw[i][0] : pack4<kF16>(y);
-        *reinterpret_cast<uint2*>(dst + o2) = kind == 2 ? raw[i][1] : pack4<kF16>(y + 4);
+        for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d, kLanes);
+        if (weight) r = rsqrtf(fmaf(sum, 1.0f / D, a.eps));
       }
+      Part y[2];
+      const uint64_t r2 = pair(r, r);
+#pragma unroll
+      for (int j = 0; j < kPart; ++j) {
+        uint64_t v = mul2(x[j], pair(c[2 * j], c[2 * j + 1]));
+        // (an element that is not rotated has no other whose infinity it would take on)
+        if (turns)
+          v = fma2(kInter ? pair(hi(x[j]), lo(x[j])) : x[(j + kPart / 2) % kPart], pair(s[2 * j], s[2 * j + 1]), v);
+        v = mul2(v, r2);
+        y[j / (kPart / 2)].w[j % (kPart / 2)] = pack2<kF16>(lo(v), hi(v));
+      }
+      if (!ok || i >= n) continue;
+      uint16_t* dst = out + i * out_step;
+      (kind == 2 ? raw[i][0] : y[0]).store(dst + o1);
+      (kind == 2 ? raw[i][1] : y[1]).store(dst + o2);
     }
   }
   const int any = __syncthreads_or(bad);
@@ -158,7 +171,7 @@ cudaError_t launch(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream
   constexpr int kGroups = kThreads / (D / 8);
   const long long chunks = (a.Hq + kHeads - 1) / kHeads + 2 * ((a.Hkv + kHeads - 1) / kHeads);
   const long long blocks = (a.T * chunks + kGroups - 1) / kGroups;
-  const long long most = (long long)num_sms * 8 < kFlagsFirst ? (long long)num_sms * 8 : kFlagsFirst;
+  const long long most = (long long)num_sms * kResident < kFlagsFirst ? (long long)num_sms * kResident : kFlagsFirst;
   const int grid = (int)(blocks < most ? blocks : most);
   const Report rep{ws, 0, {grid, 0}};
   if (a.interleaved) rope_append_kernel<D, kHeads, kF16, true><<<grid, kThreads, 0, stream>>>(a, rep);
@@ -174,10 +187,13 @@ cudaError_t launch_type(const RopeArgs& a, void* ws, int num_sms, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream) {
-  // eight heads to a group once that still gives every SM a full set of threads
-  const bool many = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8) / 8 >= 1024ll * num_sms;
-  if (a.D == 64) return many ? launch_type<64, 8>(a, ws, num_sms, stream) : launch_type<64, 1>(a, ws, num_sms, stream);
-  return many ? launch_type<128, 8>(a, ws, num_sms, stream) : launch_type<128, 1>(a, ws, num_sms, stream);
+  // several heads to a group once that still gives every SM 512 threads (1024
+  // tokens of 32 + 2 x 4 heads 7.5 -> 5.5 us; with one head for 512 tokens
+  // 4.7, several 4.05)
+  const bool many = (long long)a.T * (a.Hq + 2 * a.Hkv) * (a.D / 8) / kMany >= 512ll * num_sms;
+  if (a.D == 64)
+    return many ? launch_type<64, kMany>(a, ws, num_sms, stream) : launch_type<64, 1>(a, ws, num_sms, stream);
+  return many ? launch_type<128, kMany>(a, ws, num_sms, stream) : launch_type<128, 1>(a, ws, num_sms, stream);
 }
 
 }  // namespace attn
