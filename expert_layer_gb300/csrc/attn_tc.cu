@@ -50,7 +50,7 @@ struct Shape {
   static constexpr int kColumn = kPaged ? 1024 : kHalfBytes;   // from a K or V column to the next
   static constexpr int kGroup = kPaged ? kHalves * 1024 : 1024;   // from 8 rows of K or V to the next
   static constexpr int kTileBytes = kHalves * kHalfBytes;      // a Q, K or V tile
-  // ring of K and V tiles: 8192 causal with 3, 4, 5 stages of 32 KB: 440, 354, 358 us
+  // ring of K and V tiles: 8192 causal with 3 and 4 stages of 32 KB 421 and 324 us
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
   static constexpr int kOut = kRing + kStages * kTileBytes;    // 32 rows of 128 bytes per softmax warp
@@ -226,10 +226,10 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // warps 9, 10      issue the MMAs of tile 0 and 1 (warp 11 only completes the
 //                  warpgroup): per key block O += P V, half by half as P
 //                  comes, then S = Q K' of the next block; one tile's softmax
-//                  runs while the other multiplies.  A barrier costs an issuing warp ~200 cycles even
-//                  when it is complete (the MMAs' operands fill the
-//                  shared-memory pipe), which one warp for both tiles spent with
-//                  the tensor core idle.
+//                  runs while the other multiplies.  A barrier costs an
+//                  issuing warp ~200 cycles even when it is complete (the MMAs'
+//                  operands fill the shared-memory pipe), which one warp for
+//                  both tiles spent with the tensor core idle.
 // Tensor memory: S0 | S1 | O0 | O1; P overwrites the first half of its S.
 // One thread issues all MMAs of a tile, in order: a commit after S(j+1) also
 // covers O += P(j) V, so a softmax warp that has S(j+1) may rescale O without
@@ -561,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ni;
       if (it.row0 < 0) break;
       const int n = x ? it.n[1] : it.n[0];
-      const int both = min(it.n[0], it.n[1]);      // blocks that the tiles take in turns
+      // blocks that the tiles take in turns, and after which half
+      const int shared = min(it.n[0], it.n[1]), both = shared > 1 ? shared : 0, turn_half = D == 64 || shared <= 16 ? 0 : 1;
       const uint32_t kv0 = kv;
       kv += 2 * max(it.n[0], it.n[1]);
       // keys that this row sees, and that the tile's first token sees
@@ -574,9 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // Turns: left alone the two tiles fall into step, with the tensor core
         // idle while both compute P and the reverse (8192 x 8192 keys, D = 128:
-        // 913 us).  With D = 128, where the MMAs take longer, a tile hands over
-        // when all its P is formed (702 us; after the first half 743), with
-        // D = 64 after the first half (611 us; after both 678).
+        // 766 us).  A tile hands over when all its P is formed (608 us; after
+        // the first half 641) or, where its MMAs are shorter (D = 64) or its
+        // blocks few (16 prompts of 512 tokens 55.0 us instead of 60.3), after
+        // the first half.
         if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
         const int b = it.b0 + j;
         const uint64_t c2 = pair(t.c, t.c);
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
         };
         auto hand_over = [&](int half) {
-          if (half == (D == 64 ? 0 : 1) && j < both) {
+          if (half == turn_half && j < both) {
             ++nt;
             if (lane == 0) mbar_arrive(&turn[x ^ 1]);
           }
