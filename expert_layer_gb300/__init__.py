@@ -2,7 +2,8 @@
 same decoder layer (``attention.py``).
 
 Thin Python binding (ctypes) over the C ABI of ``libmoe_gb300.so``
-(``include/moe.h``).  The functions here only check and marshal arguments:
+(``include/moe.h``); that of the attention entry points is compiled
+(``csrc/attn_binding.cpp``).  The functions only check and marshal arguments:
 every step of the layer runs in the library's CUDA kernels.  PyTorch supplies
 device memory and the current CUDA stream.  If the library has not been
 built, every call raises ``MoEError``; there is no fallback implementation.

@@ -5,7 +5,9 @@
 keys and values to a paged cache; ``attn_prefill`` / ``attn_prefill_paged``
 attend over whole prompts, ``attn_decode`` over the cache for one new token
 of each sequence, with an optional prefix that the whole batch shares.  As in
-the rest of the package the functions only check and marshal arguments.
+the rest of the package the functions only check and marshal arguments; here
+they do so in compiled code (``_attn_binding.so``, 3 to 7 us a call instead of
+11 to 17 through ctypes), which takes their places at the first call.
 
 A cache is two tensors [pages, Hkv, page_size, D]; a page table row lists a
 sequence's pages, token j sits in row j % page_size of page j // page_size.

@@ -7,6 +7,8 @@
 //
 // Bound: latency (a row's parts are a few KB, just written).  A block takes a
 // row, its four warps every fourth part each, with their loads in batches.
+// Measured: 2048 rows of 17 parts (64 sequences behind a shared prefix) 6 us,
+// 32 rows of 38 parts 5.
 #include "attn.h"
 #include "attn_ptx.cuh"
 
