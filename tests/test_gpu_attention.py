@@ -261,6 +261,77 @@ def test_prefill_paged(case):
     ref.check(lse, le, tl, "lse")
 
 
+# A few sequences of thousands of keys: chunks of long prompts, short sequences
+# among long ones, rows without keys, keys split over blocks or not
+LONG = [
+    # q_lens, kv_lens, Hq, Hkv, D, causal, page, dtype
+    ([300, 17, 1, 512], [4100, 3500, 4000, 512], 32, 4, 128, True, 16, BF),
+    ([1400], [5001], 16, 8, 64, True, 64, HF),
+    ([200, 0, 90, 64], [4000, 100, 0, 64], 16, 16, 64, False, 32, HF),
+    ([150, 400], [60, 3500], 48, 4, 128, True, 128, BF),
+    ([1] * 70 + [40], [5] * 70 + [5000], 8, 2, 128, True, 16, BF),
+    ([129, 1200], [9000, 1200], 8, 4, 128, False, 256, BF),
+]
+
+
+@pytest.mark.parametrize("paged", [True, False], ids=["paged", "packed"])
+@pytest.mark.parametrize("case", LONG, ids=lambda c: f"{c[2]}x{c[3]}x{c[4]}-{sum(c[0])}-{max(c[1])}")
+def test_prefill_long(case, paged):
+    q_lens, kv_lens, Hq, Hkv, D, causal, page, dtype = case
+    q = rand(gen_of(22), sum(q_lens), Hq, D, dtype=dtype, mul=2.5)
+    lse = torch.full((q.shape[0], Hq), 7.0, device="cuda")
+    ws = moe.alloc_attn_workspace(q.shape[0], len(q_lens), Hq, Hkv, D)
+    if paged:
+        kc, vc, table, _ = page_pool(kv_lens, page, Hkv, D, dtype, 21)
+
+        def call(lse):
+            return moe.attn_prefill_paged(q, kc, vc, table, starts(q_lens), ints(kv_lens), causal=causal, lse=lse,
+                                          workspace=ws)
+
+        def keys(s):
+            pages = table[s, :(kv_lens[s] + page - 1) // page]
+            return ref.paged(kc, pages, kv_lens[s]), ref.paged(vc, pages, kv_lens[s])
+    else:
+        _, k, v = packed_case(q_lens, kv_lens, Hq, Hkv, D, dtype, 23, junk=True)
+        at = [int(x) for x in starts(kv_lens)]
+
+        def call(lse):
+            return moe.attn_prefill(q, k, v, starts(q_lens), starts(kv_lens), causal=causal, lse=lse, workspace=ws)
+
+        def keys(s):
+            return k[at[s]:at[s + 1]].transpose(0, 1), v[at[s]:at[s + 1]].transpose(0, 1)
+    out = call(lse)
+    assert moe.read_status(ws) == 0
+    o, le, to, tl = prefill_reference(q, q_lens, keys, causal, D ** -0.5)
+    ref.check(out, o, to, "out")
+    ref.check(lse, le, tl, "lse")
+    assert torch.equal(out, call(lse))
+
+
+def test_prefill_long_reports_bad_lengths_and_pages():
+    q_lens, kv_lens, Hq, Hkv, D, page = [300, 17, 1, 512], [4100, 3500, 4000, 512], 32, 4, 128, 16
+    kc, vc, table, _ = page_pool(kv_lens, page, Hkv, D, BF, 21)
+    q = rand(gen_of(22), sum(q_lens), Hq, D, mul=2.5)
+    ws = moe.alloc_attn_workspace(q.shape[0], 4, Hq, Hkv, D)
+
+    def call(table, kv):
+        out = moe.attn_prefill_paged(q, kc, vc, table, starts(q_lens), ints(kv), workspace=ws)
+        return out, moe.read_status(ws)
+    clean, status = call(table, kv_lens)
+    assert status == 0
+    out, status = call(table, [4100, 1 << 30, 4000, 512])     # the second counts as empty
+    assert status != 0
+    rest = list(range(300)) + list(range(317, sum(q_lens)))
+    # (the other sequences' keys may be split in other places: a rounding of the type, twice on each side)
+    assert bool((out[300:317] == 0).all())
+    assert float((out[rest].float() - clean[rest].float()).abs().max()) <= 4 * 2.0 ** -8 * float(clean[rest].float().abs().max())
+    bad = table.clone()
+    bad[2, 7] = 1 << 29
+    assert call(bad, kv_lens)[1] != 0
+    again, status = call(table, kv_lens)
+    assert status == 0 and torch.equal(again, clean)
+
+
 def test_prefill_scales_and_extreme_logits():
     # scale 0 (every key alike), a negative scale, and logits far apart
     q, k, v = packed_case([200], [200], 4, 2, 128, BF, 31)
