@@ -728,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok) break;
-      if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
-      tc_fence_after();
+      // what needs no O comes before the wait for it (16 sequences of 100 to 1000
+      // keys, D = 64: 40.4 -> 38.6 us)
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;     // l is NaN: so is the row
       // 128 bytes of every row at a time pass through shared memory, swizzled as
       // a copy box is.  A warp whose 32 rows are whole heads of whole tokens, all
@@ -773,6 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
       };
+      stage_free();
+      if (n > 0 && !warp_spin(&o_full[x], no++ & 1)) { ok = false; break; }
+      tc_fence_after();
       if (part) {
         if (n > 0)                                              // a part without keys is not read
 #pragma unroll 1
@@ -780,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[32];
             tmem_ld32(tO + i, *reinterpret_cast<uint32_t(*)[32]>(v));
             tmem_wait_ld();
-            stage_free();
+            if (i) stage_free();
 #pragma unroll
             for (int u = 0; u < 8; ++u)
               put(u, make_uint4(__float_as_uint(v[4 * u] * inv), __float_as_uint(v[4 * u + 1] * inv),
@@ -805,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               pack2<kF16>(v[8 * u + 2] * inv, v[8 * u + 3] * inv),
                               pack2<kF16>(v[8 * u + 4] * inv, v[8 * u + 5] * inv),
                               pack2<kF16>(v[8 * u + 6] * inv, v[8 * u + 7] * inv));
-          stage_free();
+          if (i) stage_free();
 #pragma unroll
           for (int u = 0; u < 8; ++u) put(u, w[u]);
           write(i, D * 2);
