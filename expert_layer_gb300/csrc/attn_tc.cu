@@ -16,9 +16,13 @@
 // f16, and bf16 rounds relative to P whatever its size); only then the row's
 // maximum is taken again and l and O are rescaled, which hardly happens.
 //
-// Bound: the tensor pipe (512 cycles for each of a tile's two products per key
-// block) and, nearly as long, the 128 x 128 exponentials.  Two tiles make one
-// of them run while the other waits for its barriers, and fill tensor memory.
+// Bound: D = 128, the tensor pipe (512 cycles for each of a tile's two products
+// per key block, 2048 for both tiles, of a period of ~2550); D = 64, the chain
+// product - softmax - product of two tiles in turns (~2400, the products half as
+// long).  Two tiles make one of them run while the other waits for its barriers,
+// and fill tensor memory.  Exponentials (32 a cycle and SM: 1024 per period) are
+// not the bound: a quarter of them as a polynomial on the FMA pipe took 375 us
+// for 8192 tokens instead of 324.
 // Measured (32 query and 4 key-value heads of 128, bf16): 8192 tokens causal
 // 322 us = 1.71 PFLOP/s, 89% of the library's matrix product; 8192 x 8192 608 us
 // = 1.81; 16 prompts of 512 tokens 55 us, 64 of 128 39.5 (an item of one block
