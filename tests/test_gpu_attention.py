@@ -440,6 +440,22 @@ def test_decode(case):
     assert torch.equal(out, again)
 
 
+# More keys of the rows' own than fit beside the prefix's kernel (the rest comes
+# after it), more sequences than a block holds lengths of, and both
+DECODE_MANY = [
+    ([1500 + 37 * i for i in range(32)], 256, 8, 4, 64, 16, BF),
+    ([0, 60000, 1, 4000, 40000], 700, 16, 2, 128, 64, HF),
+    ([130 + i % 3 for i in range(400)], 2000, 32, 4, 128, 16, BF),
+    ([90 + i % 50 for i in range(700)], 0, 8, 2, 64, 16, HF),
+    ([0] * 280 + [3] * 20 + [5000], 64, 12, 1, 128, 32, BF),
+]
+
+
+@pytest.mark.parametrize("case", DECODE_MANY, ids=lambda c: f"{c[2]}x{c[3]}x{c[4]}-B{len(c[0])}-{max(c[0])}-pre{c[1]}")
+def test_decode_many_keys(case):
+    test_decode(case)
+
+
 @pytest.mark.parametrize("kv_lens,prefix", [([40], 0), ([9000], 0), ([300, 0, 5000], 512), ([0, 17], 4096)])
 def test_decode_nan_query_stays_in_its_head(kv_lens, prefix):
     # a NaN that a row does see is in its result, whether the row's keys are in
