@@ -81,8 +81,25 @@ struct Item {
   int split;
 };
 
+// Quotients of n in [0, 2^31) by a divisor that the host knows: with
+// 2^(k-1) < d <= 2^k, m = ceil(2^(31+k) / d) < 2^32, n / d = floor(m n / 2^(31+k)):
+// the error of m, less than one part in 2^31 of a quotient's unit, moves no
+// quotient.  (A division is some 20 instructions, and those of a first item
+// come from L2 as they run.)
+struct Divisor {
+  uint32_t m, shift;      // m = 0: d = 1
+  void set(uint32_t d) {
+    shift = 0;
+    while ((1ull << (shift + 1)) < d) ++shift;
+    m = d == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
+  }
+  __device__ __forceinline__ int of(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> shift) : n; }
+};
+
 struct TcAttnArgs {
   AttnArgs a;
+  int G;                         // Hq / Hkv
+  Divisor by_splits, by_Hkv, by_per, by_G;
   int tt, slots, splits;
   int box;                       // rows of a K / V box
   float c;                       // scale log2 e, not 0
@@ -148,13 +165,13 @@ __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_t) {
 // Sequence s owns the tile slots base(s) .. base(s+1) - 1 with base(s) =
 // floor(q_starts[s] / (2 tt)) + s: at least as many as it has tiles, without a
 // prefix sum over the batch.  All lanes of the warp search together.
-__device__ __forceinline__ int find_seq(const AttnArgs& a, int per, int slot) {
+__device__ __forceinline__ int find_seq(const AttnArgs& a, const Divisor& per, int slot) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = a.n_seq;                       // the answer is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int s = lo + lane * step;
-    const bool at = lane * step < n && a.q_starts[s] / per + s <= slot;
+    const bool at = lane * step < n && per.of(max(0, a.q_starts[s])) + s <= slot;
     const int hit = 31 - __clz((int)(__ballot_sync(0xffffffffu, at) | 1u));
     lo += hit * step;
     n = min(step, n - hit * step);
@@ -166,18 +183,18 @@ __device__ __forceinline__ int find_seq(const AttnArgs& a, int per, int slot) {
 // a sequence see more keys: they come first.
 __device__ __forceinline__ bool make_item(const TcAttnArgs& t, int idx, Item& it, int& seq, int& k0) {
   const AttnArgs& a = t.a;
-  it.split = idx % t.splits;
-  idx /= t.splits;
-  it.head = idx % a.Hkv;
-  const int slot = t.slots - 1 - idx / a.Hkv;
+  const int unit = t.by_splits.of(idx), back = t.by_Hkv.of(unit);
+  it.split = idx - unit * t.splits;
+  it.head = unit - back * a.Hkv;
+  const int slot = t.slots - 1 - back;
   const int per = 2 * t.tt;
   int q0 = 0, q1 = a.T, tile = slot;
   seq = 0;
   if (a.q_starts) {
-    seq = find_seq(a, per, slot);
+    seq = find_seq(a, t.by_per, slot);
     q0 = a.q_starts[seq];
     q1 = a.q_starts[seq + 1];
-    tile = slot - (q0 / per + seq);
+    tile = slot - (t.by_per.of(max(0, q0)) + seq);
     if (q0 < 0 || q1 < q0 || q1 > a.T || tile < 0) return false;
   }
   const long long first = (long long)tile * per;
@@ -206,8 +223,10 @@ __device__ __forceinline__ bool make_item(const TcAttnArgs& t, int idx, Item& it
     nb[x] = it.tok[x] > 0 && v > 0 ? (v + kKeys - 1) / kKeys : 0;
   }
   const int all = max(nb[0], nb[1]);
-  it.b0 = (int)((long long)all * it.split / t.splits);
-  const int b1 = (int)((long long)all * (it.split + 1) / t.splits);
+  // floor(all * split / splits), and the same of split + 1
+  const int whole = t.by_splits.of(all), more = all - whole * t.splits;
+  it.b0 = whole * it.split + t.by_splits.of(more * it.split);
+  const int b1 = whole * (it.split + 1) + t.by_splits.of(more * (it.split + 1));
 #pragma unroll
   for (int x = 0; x < 2; ++x) it.n[x] = max(0, min(nb[x], b1) - it.b0);
   return true;
@@ -274,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.Hkv;
+  const int G = t.G;
   if (threadIdx.x == 0) {
     prefetch_map(&tmQ);
     prefetch_map(&tmK);
@@ -559,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax, epilogue
     const int x = warp >> 2;                                   // tile
     const int row = (warp & 3) * 32 + lane;                    // row of the tile
-    const int token = row / G, g = row - token * G;
+    const int token = t.by_G.of(row), g = row - token * G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + x * kKeys, tO = tmem + lanes + 2 * kKeys + x * D;
     uint32_t ni = 0, ns = 0, no = 0, nt = 0, kv = 0;
@@ -897,6 +916,11 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.tt = p.tt;
   t.slots = p.slots;
   t.splits = splits;
+  t.G = a.Hq / a.Hkv;
+  t.by_splits.set(splits);
+  t.by_Hkv.set(a.Hkv);
+  t.by_per.set(2 * p.tt);
+  t.by_G.set(t.G);
   const int items = tc_items(a, splits);
   if (items < 0) return cudaErrorInvalidValue;
   t.box = a.page_table && (1 << a.page_shift) < kKeys ? 1 << a.page_shift : kKeys;
