@@ -34,7 +34,7 @@ constexpr long long kMaxBlocks = 160;
 constexpr long long kTileRows = 256;
 
 struct Layout {
-  size_t hdr, flags, part_o, part_lse, slot_o, slot_lse, tail, base, total;
+  size_t hdr, flags, part_o, part_lse, slot_o, slot_lse, tail, held, total;
 };
 
 inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long long Hkv, long long D) {
@@ -54,7 +54,7 @@ inline Layout make_attn_layout(long long T, long long n_seq, long long Hq, long 
   L.slot_o = take(sizeof(float) * 2 * kMaxBlocks * 16 * D);
   L.slot_lse = take(sizeof(float) * 2 * kMaxBlocks * 16);
   L.tail = take(sizeof(int4) * kMaxBlocks);
-  L.base = take(sizeof(int) * (size_t)(n_seq + 1));
+  L.held = take(sizeof(int2) * (size_t)n_seq * Hkv * ((Hq / Hkv + 15) / 16));
   L.total = o;
   return L;
 }
@@ -126,6 +126,23 @@ struct AttnArgs {
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);
 
+// Quotients of n in [0, 2^31) by a divisor that the host knows: with
+// 2^(k-1) < d <= 2^k, m = ceil(2^(31+k) / d) < 2^32, n / d = floor(m n / 2^(31+k)):
+// the error of m, less than one part in 2^31 of a quotient's unit, moves no
+// quotient.  (A division is some 20 instructions, and those of a first item
+// come from L2 as they run.)
+struct Divisor {
+  uint32_t m, shift;      // m = 0: d = 1
+  void set(uint32_t d) {
+    shift = 0;
+    while ((1ull << (shift + 1)) < d) ++shift;
+    m = d == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int of(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> shift) : n; }
+#endif
+};
+
 // attn_tc.cu -- tiles of 128 rows (tt tokens x G heads), two per block; slots:
 // tile slots of the batch (see find_seq)
 struct TcPlan {
@@ -151,8 +168,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
 // own keys, row_*, null without a prefix), per block (two slots of 16 rows: a
 // unit that began in an earlier block, and one that goes on in the next), the
 // unit that each block's range ends in, {sequence, unit, blocks from this one
-// on, 0} (0 blocks: none), and each sequence's first place on the line (only
-// with a prefix).
+// on, 0} (0 blocks: none); with a prefix instead, for every unit, {blocks that
+// hold its keys (one: the parts are in row order), the first of them}.
 struct DecodeParts {
   float* tc_o;
   float* tc_lse;
@@ -161,7 +178,7 @@ struct DecodeParts {
   float* slot_o;
   float* slot_lse;
   int4* tail;
-  int32_t* base;
+  int2* held;
 };
 // A unit costs its warp about as much as one 16-key slice besides its slices
 // (queries, the end of the softmax): 64 sequences of 1 to 8192 keys
@@ -222,7 +239,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const De
 
 // attn_merge.cu -- joins the parts of every row (decode_grid 0: prefill)
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
-                              const Beside& beside, cudaStream_t stream);
+                              cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace moe

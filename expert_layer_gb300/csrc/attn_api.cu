@@ -112,7 +112,7 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
   p.slot_o = ws_ptr<float>(ws, L.slot_o);
   p.slot_lse = ws_ptr<float>(ws, L.slot_lse);
   p.tail = ws_ptr<int4>(ws, L.tail);
-  p.base = ws_ptr<int32_t>(ws, L.base);
+  p.held = ws_ptr<int2>(ws, L.held);
   Report rep{ws, 0, {sms, 0}};
   int splits = 0;
   Beside beside{};
@@ -129,7 +129,7 @@ int run_decode(const AttnArgs& a, const Layout& L, void* ws, int sms, cudaStream
   }
   rep.set = 0;
   ATTN_TRY(cuda_status(launch_attn_decode(a, beside, p, rep, sms, s)));
-  return cuda_status(launch_attn_merge(a, splits, p, sms, beside, s));
+  return cuda_status(launch_attn_merge(a, splits, p, sms, s));
 }
 
 // The checks shared by the three attention calls, in the order of the others
@@ -158,7 +158,7 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   p.tc_o = ws_ptr<float>(workspace, L.part_o);
   p.tc_lse = ws_ptr<float>(workspace, L.part_lse);
   ATTN_TRY(cuda_status(launch_attn_tc(a, splits, p.tc_o, p.tc_lse, rep, s)));
-  return cuda_status(launch_attn_merge(a, splits, p, 0, Beside{}, s));
+  return cuda_status(launch_attn_merge(a, splits, p, 0, s));
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ struct DecodeArgs {
   AttnArgs a;
   float c;              // |scale| log2 e, > 0
   uint32_t flip;        // sign bits of two elements when the scale is negative
+  int G;                // Hq / Hkv
   int chunks;           // units per key-value head
   int few, head;        // of Line
   DecodeParts p;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* scan = reinterpret_cast<int*>(smem + S::kScan);     // [8] warp sums, then the start
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.Hkv, units = a.Hkv * t.chunks;
+  const int G = t.G, units = a.Hkv * t.chunks;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * kStages;
   unsigned char* ring = smem + warp * S::kRing;
   bool bad = false, late = false;
@@ -184,14 +185,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += scan[w];
   }
   before += incl - mine;
-  if (blockIdx.x == 0 && t.p.row_o) {        // with a prefix the merge kernel reads where each sequence lies
-    int at = before;
-    for (int s = s0; s < s1; ++s) {
-      t.p.base[s] = at;
-      at += unit_weight(run == 1 ? window[s] : seq_len(a, s)) * units;
-    }
-    if (threadIdx.x == kThreads - 1) t.p.base[a.n_seq] = total;
-  }
   const Line line(total, gridDim.x, t.few, t.head);
   const int start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
   const bool work = (int)blockIdx.x < line.blocks && start < end;
@@ -407,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long row = (long long)cur.b * a.Hq + h0 + r;
           const float inv = 1.0f / l[rs], lse = m[rs] + lg2(l[rs]);
           if (t.p.row_o) {
+            if (lane == 0 && rs == 0) t.p.held[cur.b * units + cur.u] = make_int2(1, 0);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
               *reinterpret_cast<float2*>(t.p.row_o + row * D + 8 * i + 2 * quad) =
@@ -453,14 +447,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   // --- rows without keys (with a prefix the merge kernel writes every row)
-  if (!t.p.row_o)
-    for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x)
-      if ((run == 1 ? window[s] : seq_len(a, s)) == 0) {
+  for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x)
+    if ((run == 1 ? window[s] : seq_len(a, s)) == 0) {
+      if (t.p.row_o) {
+        for (int i = threadIdx.x; i < units; i += kThreads) t.p.held[s * units + i] = make_int2(0, 0);
+      } else {
         for (int i = threadIdx.x; i < a.Hq * (D / 8); i += kThreads)
           reinterpret_cast<uint4*>(a.out + (long long)s * a.Hq * D)[i] = make_uint4(0, 0, 0, 0);
         if (a.lse)
           for (int i = threadIdx.x; i < a.Hq; i += kThreads) a.lse[(long long)s * a.Hq + i] = -INFINITY;
       }
+    }
 
   // --- join the warps' parts of units that cross their ranges: row r is
   // out = sum_w 2^{m_w - M} O_w / sum_w 2^{m_w - M} l_w.  The parts of a unit
@@ -479,6 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = 2 * blockIdx.x + (begin < start ? 0 : 1);
     if (begin >= start && !whole)
       tail = make_int4(op.b, op.u, line.block_of(begin + op.slices - 1) - (int)blockIdx.x + 1, 0);
+    if (t.p.row_o && threadIdx.x == 0 && begin >= start)
+      t.p.held[op.b * units + op.u] = whole ? make_int2(1, 0) : make_int2(tail.z, (int)blockIdx.x);
     const int hk = t.chunks == 1 ? op.u : op.u / t.chunks;
     const int h0 = hk * G + (op.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
@@ -559,6 +558,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const De
   if (t.c < 1.2e-38f) t.c = 1.2e-38f;      // a masked logit of -inf stays one
   t.flip = a.scale < 0 ? 0x80008000u : 0u;
   const int G = a.Hq / a.Hkv;
+  t.G = G;
   t.chunks = decode_chunks(a);
   t.few = beside.few;
   t.head = beside.head;

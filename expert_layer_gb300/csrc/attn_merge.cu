@@ -24,8 +24,8 @@ struct MergeArgs {
   int splits;            // parts in row order: [splits, T * Hq]; 0: decode without a prefix
   DecodeParts p;
   int chunks, grid;      // decode: units per key-value head, blocks of the kernel (0: prefill)
-  int few, head;         // of Line
-  unsigned rows;         // decode without a prefix: rows of a unit, at most 16
+  int G, rows;           // heads of a key-value head; of a unit, at most 16
+  Divisor by_rows, by_chunks, by_Hq, by_G;
   unsigned todo;         // rows to write
 };
 
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
   __shared__ float2 s_ml[kWarps];
   const AttnArgs& a = t.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.Hq / a.Hkv;
+  const int G = t.G;
   const long long rows = (long long)a.T * a.Hq;
   pdl_wait();   // programmatic dependent launch: the parts are complete
 #pragma unroll 1
@@ -49,27 +49,22 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
     int c0 = 0, own = 0, r = 0, parts = 0;
     long long row = i;
     if (!t.splits) {
-      c0 = (int)(i / t.rows);
-      r = (int)(i - c0 * t.rows);
+      c0 = t.by_rows.of((int)i);
+      r = (int)i - c0 * t.rows;
       const int4 u = t.p.tail[c0];
-      const int hk = u.y / t.chunks, h = (u.y - hk * t.chunks) * 16 + r;
+      const int hk = t.by_chunks.of(u.y), h = (u.y - hk * t.chunks) * 16 + r;
       if (u.z == 0 || h >= G) continue;
       parts = own = u.z;
       row = (long long)u.x * a.Hq + hk * G + h;
     } else {
       parts = t.splits;
       if (t.grid > 0) {
-        const int b = (int)(i / a.Hq), h = (int)(i - (unsigned)b * a.Hq);
-        const int units = a.Hkv * t.chunks, u = (h / G) * t.chunks + (h % G) / 16;
-        r = (h % G) % 16;
-        const int total = t.p.base[a.n_seq], b0 = t.p.base[b], n = (t.p.base[b + 1] - b0) / units;
-        if (n > 0) {
-          const Line line(total, t.grid, t.few, t.head);
-          const int at = b0 + u * n;
-          c0 = line.block_of(at + kUnitCost);
-          own = line.block_of(at + n - 1) - c0 + 1;
-          parts += own;
-        }
+        const int b = t.by_Hq.of((int)i), h = (int)i - b * a.Hq, hk = t.by_G.of(h), g = h - hk * G;
+        const int2 u = t.p.held[(b * a.Hkv + hk) * t.chunks + g / 16];
+        own = u.x;
+        c0 = u.y;
+        r = g % 16;
+        parts += own;
       }
     }
     float m = -INFINITY, sum = 0.f, acc[N];
@@ -144,17 +139,19 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
 }  // namespace
 
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
-                              const Beside& beside, cudaStream_t stream) {
+                              cudaStream_t stream) {
   MergeArgs t{};
   t.a = a;
   t.splits = splits;
   t.p = p;
   t.chunks = decode_chunks(a);
   t.grid = decode_grid;
-  t.few = beside.few;
-  t.head = beside.head;
-  const int G = a.Hq / a.Hkv;
-  t.rows = G < 16 ? G : 16;
+  t.G = a.Hq / a.Hkv;
+  t.rows = t.G < 16 ? t.G : 16;
+  t.by_rows.set(t.rows);
+  t.by_chunks.set(t.chunks);
+  t.by_Hq.set(a.Hq);
+  t.by_G.set(t.G);
   t.todo = splits ? (unsigned)a.T * a.Hq : t.rows * decode_grid;
   auto kern = a.D == 64 ? (a.f16 ? attn_merge_kernel<64, true> : attn_merge_kernel<64, false>)
                         : (a.f16 ? attn_merge_kernel<128, true> : attn_merge_kernel<128, false>);

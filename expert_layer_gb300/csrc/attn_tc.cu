@@ -81,21 +81,6 @@ struct Item {
   int split;
 };
 
-// Quotients of n in [0, 2^31) by a divisor that the host knows: with
-// 2^(k-1) < d <= 2^k, m = ceil(2^(31+k) / d) < 2^32, n / d = floor(m n / 2^(31+k)):
-// the error of m, less than one part in 2^31 of a quotient's unit, moves no
-// quotient.  (A division is some 20 instructions, and those of a first item
-// come from L2 as they run.)
-struct Divisor {
-  uint32_t m, shift;      // m = 0: d = 1
-  void set(uint32_t d) {
-    shift = 0;
-    while ((1ull << (shift + 1)) < d) ++shift;
-    m = d == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
-  }
-  __device__ __forceinline__ int of(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> shift) : n; }
-};
-
 struct TcAttnArgs {
   AttnArgs a;
   int G;                         // Hq / Hkv
