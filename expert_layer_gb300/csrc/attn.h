@@ -88,6 +88,23 @@ struct Heads {                // [tokens, heads, D], strides in elements
   long long tok, head;
 };
 
+// Quotients of n in [0, 2^31) by a divisor that the host knows: with
+// 2^(k-1) < d <= 2^k, m = ceil(2^(31+k) / d) < 2^32, n / d = floor(m n / 2^(31+k)):
+// the error of m, less than one part in 2^31 of a quotient's unit, moves no
+// quotient.  (A division is some 20 instructions, and those of a first item
+// come from L2 as they run.)
+struct Divisor {
+  uint32_t m, shift;      // m = 0: d = 1
+  void set(uint32_t d) {
+    shift = 0;
+    while ((1ull << (shift + 1)) < d) ++shift;
+    m = d == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int of(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> shift) : n; }
+#endif
+};
+
 struct RopeArgs {
   Heads q, k, v;
   const float* q_norm;        // [D] or null
@@ -102,6 +119,8 @@ struct RopeArgs {
   uint16_t* k_cache;          // [pages, Hkv, page_size, D]
   uint16_t* v_cache;
   int pages, page_shift;      // page_size = 1 << page_shift
+  unsigned chunks;            // groups of heads of a token (the kernel's)
+  Divisor by_chunks;
 };
 
 // One attention call.  Packed keys: k, v, kv_starts.  Paged: k_cache,
@@ -125,23 +144,6 @@ struct AttnArgs {
 };
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);
-
-// Quotients of n in [0, 2^31) by a divisor that the host knows: with
-// 2^(k-1) < d <= 2^k, m = ceil(2^(31+k) / d) < 2^32, n / d = floor(m n / 2^(31+k)):
-// the error of m, less than one part in 2^31 of a quotient's unit, moves no
-// quotient.  (A division is some 20 instructions, and those of a first item
-// come from L2 as they run.)
-struct Divisor {
-  uint32_t m, shift;      // m = 0: d = 1
-  void set(uint32_t d) {
-    shift = 0;
-    while ((1ull << (shift + 1)) < d) ++shift;
-    m = d == 1 ? 0 : (uint32_t)(((1ull << (32 + shift)) + d - 1) / d);
-  }
-#ifdef __CUDACC__
-  __device__ __forceinline__ int of(int n) const { return m ? (int)(__umulhi((uint32_t)n, m) >> shift) : n; }
-#endif
-};
 
 // attn_tc.cu -- tiles of 128 rows (tt tokens x G heads), two per block; slots:
 // tile slots of the batch (see find_seq)

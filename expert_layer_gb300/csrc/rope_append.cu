@@ -19,8 +19,8 @@
 // heads of 128, 33.0 us instead of 32.4), four heads to a group (eight: 32.0,
 // but 64-wide heads 19.4 instead of 18.0 us), four elements to a load (eight,
 // with half the lanes and twice the registers: 36.9).
-// Measured: 1 token 2.2 us, 256 tokens 3.3, 8192 tokens 32.4 us = 5.3 TB/s, 78%
-// of a copy's rate; 16,384 tokens 60.2 us = 5.7 TB/s (a call of 172 MB starts
+// Measured: 1 token 2.2 us, 256 tokens 3.3, 8192 tokens 32.3 us = 5.3 TB/s, 79%
+// of a copy's rate; 16,384 tokens 60.0 us = 5.7 TB/s (a call of 172 MB starts
 // and ends in 7 us).
 #include "attn.h"
 #include "attn_ptx.cuh"
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     rope_append_kernel(const RopeArgs a, const Report rep) {
   constexpr int kPart = 4, kLanes = D / (2 * kPart), kGroups = kThreads / kLanes;
   const int gl = threadIdx.x % kLanes;                  // lane of the group
-  const unsigned cq = (a.Hq + kHeads - 1) / kHeads, ck = (a.Hkv + kHeads - 1) / kHeads, chunks = cq + 2 * ck;
+  const unsigned cq = (a.Hq + kHeads - 1) / kHeads, ck = (a.Hkv + kHeads - 1) / kHeads, chunks = a.chunks;
   const unsigned long long items = (unsigned long long)a.T * chunks;
   const int half = a.rot / 2;
   const bool turns = 2 * kPart * gl < a.rot;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     const unsigned long long item = base + threadIdx.x / kLanes;
     const bool live = item < items;
     const unsigned long long it = live ? item : 0;
-    const unsigned t = items >> 32 ? (unsigned)(it / chunks) : (unsigned)it / chunks;
+    const unsigned t = items >> 31 ? (unsigned)(it / chunks) : (unsigned)a.by_chunks.of((int)it);
     const unsigned chunk = (unsigned)(it - (unsigned long long)t * chunks);
     int pos = a.positions[t];
     const int slot = a.slots[t];
@@ -167,10 +167,11 @@ __global__ void __launch_bounds__(kThreads, kResident)
 }
 
 template <int D, int kHeads, bool kF16>
-cudaError_t launch(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream) {
+cudaError_t launch(RopeArgs a, void* ws, int num_sms, cudaStream_t stream) {
   constexpr int kGroups = kThreads / (D / 8);
-  const long long chunks = (a.Hq + kHeads - 1) / kHeads + 2 * ((a.Hkv + kHeads - 1) / kHeads);
-  const long long blocks = (a.T * chunks + kGroups - 1) / kGroups;
+  a.chunks = (a.Hq + kHeads - 1) / kHeads + 2 * ((a.Hkv + kHeads - 1) / kHeads);
+  a.by_chunks.set(a.chunks);
+  const long long blocks = ((long long)a.T * a.chunks + kGroups - 1) / kGroups;
   const long long most = (long long)num_sms * kResident < kFlagsFirst ? (long long)num_sms * kResident : kFlagsFirst;
   const int grid = (int)(blocks < most ? blocks : most);
   const Report rep{ws, 0, {grid, 0}};
