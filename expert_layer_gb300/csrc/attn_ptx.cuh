@@ -92,14 +92,18 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 // A bounded wait that does not sleep between polls: for warps that the tensor
-// cores or the softmax depend on.
+// cores or the softmax depend on.  One poll, then a rolled loop that reads the
+// clock between polls: sixteen polls in a row were a quarter of the kernels'
+// code (8192 causal 317 us, 37 ragged prompts 27.9, 16 sequences D = 64 37.1;
+// now 306, 26.1, 34.9).
 __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = now_ns();
-  while (!mbar_try_wait(bar, parity))
+#pragma unroll 1
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
     if (now_ns() - t0 > kWaitNs) return false;
-  return true;
+  }
 }
 // The same for a converged warp: every lane polls, the verdict is uniform.
 __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity) {
