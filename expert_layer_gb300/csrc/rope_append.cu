@@ -19,8 +19,8 @@
 // heads of 128, 33.0 us instead of 32.4), four heads to a group (eight: 32.0,
 // but 64-wide heads 19.4 instead of 18.0 us), four elements to a load (eight,
 // with half the lanes and twice the registers: 36.9).
-// Measured: 1 token 2.2 us, 256 tokens 3.3, 8192 tokens 32.3 us = 5.3 TB/s, 79%
-// of a copy's rate; 16,384 tokens 60.0 us = 5.7 TB/s (a call of 172 MB starts
+// Measured: 1 token 2.2 us, 256 tokens 3.3, 8192 tokens 32.1 us = 5.4 TB/s, 79%
+// of a copy's rate; 16,384 tokens 59.4 us = 5.8 TB/s (a call of 172 MB starts
 // and ends in 7 us).
 #include "attn.h"
 #include "attn_ptx.cuh"
