@@ -20,9 +20,9 @@
 // latter multiplies, and the kernel waits for HBM in any case (issue slots 20%
 // used, mma pipe 14%).
 // Measured (32 query and 4 key-value heads of 128, bf16): 128 sequences of 4096
-// keys 167 us = 6.4 TB/s, 95% of a copy's rate; one of 131,001 keys 50.6 us, of
-// which it streams 38 at 6.9 TB/s; 64 of 1 to 8192 keys 26.9; 1024 of 90 keys
-// 47.7; 8 of 400 keys 9.5 (start 2.5, keys 1, join and merge 4).
+// keys 168 us = 6.4 TB/s, 95% of a copy's rate; one of 131,001 keys 50.4 us, of
+// which it streams 38 at 6.9 TB/s; 64 of 1 to 8192 keys 26.7; 1024 of 90 keys
+// 47.7; 8 of 400 keys 9.1 (start 2.5, keys 1, join and merge 4).
 #include "attn.h"
 #include "attn_ptx.cuh"
 

@@ -24,9 +24,10 @@
 // not the bound: a quarter of them as a polynomial on the FMA pipe took 375 us
 // for 8192 tokens instead of 324.
 // Measured (32 query and 4 key-value heads of 128, bf16): 8192 tokens causal
-// 322 us = 1.71 PFLOP/s, 89% of the library's matrix product; 8192 x 8192 608 us
-// = 1.81; 16 prompts of 512 tokens 55 us, 64 of 128 39.5 (an item of one block
-// is a chain of 4.6 us: product 0.2, softmax 1.3, product 0.7, epilogue 1.7).
+// 310 us = 1.77 PFLOP/s, 92% of the library's matrix product (340 after seconds,
+// at 1725 MHz under the power cap, 94% of its rate then); 8192 x 8192 594 us =
+// 1.85; 16 prompts of 512 tokens 50.4 us, 64 of 128 35 (an item of one block is a
+// chain of ~4.2 us: product 0.2, softmax 1.3, product 0.7, epilogue 1.6).
 #include <cuda.h>
 
 #include "attn.h"
@@ -578,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.row0 < 0) break;
       const int n = x ? it.n[1] : it.n[0];
       // blocks that the tiles take in turns, and after which half
-      const int shared = min(it.n[0], it.n[1]), both = shared > 1 ? shared : 0, turn_half = D == 64 || shared <= 16 ? 0 : 1;
+      const int shared = min(it.n[0], it.n[1]), both = shared > 1 ? shared : 0;
+      const int turn_half = D == 64 || shared <= 16 ? 0 : 1;
       const uint32_t kv0 = kv;
       kv += 2 * max(it.n[0], it.n[1]);
       // keys that this row sees, and that the tile's first token sees
@@ -591,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // Turns: left alone the two tiles fall into step, with the tensor core
         // idle while both compute P and the reverse (8192 x 8192 keys, D = 128:
-        // 766 us).  A tile hands over when all its P is formed (608 us; after
-        // the first half 641) or, where its MMAs are shorter (D = 64) or its
+        // 668 us).  A tile hands over when all its P is formed (594 us; after
+        // the first half 622) or, where its MMAs are shorter (D = 64) or its
         // blocks few (16 prompts of 512 tokens 55.0 us instead of 60.3), after
         // the first half.
         if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
