@@ -614,8 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const int lim = vis - b * kKeys;    // keys of the block that the row sees: more in later rows
         const int lim0 = __shfl_sync(0xffffffffu, lim, 0), lim1 = __shfl_sync(0xffffffffu, lim, 31);
-        if (__any_sync(0xffffffffu, live && m == -INFINITY && lim > 0)) {
-          // a first scale: the maximum of the first few logits
+        bool unset = __any_sync(0xffffffffu, live && m == -INFINITY && lim > 0);
+        if (unset) {
+          // a first scale: the maximum of the first few logits (all of them
+          // -inf, as a product past fp32 or an infinity in a key makes them: the
+          // loop below, which looks at every logit)
           float u[16];
           tmem_ld16(tS, *reinterpret_cast<uint32_t(*)[16]>(u));
           tmem_wait_ld();
@@ -623,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * t.c : -INFINITY);
           if (m == -INFINITY) m = top;
+          unset = __any_sync(0xffffffffu, live && m == -INFINITY);
         }
         // 64 logits to P with the scale in use; the sum
         auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32]) {
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // without a look at the logits first and without branches (those of a
         // mask cost 10% over 8192 keys).
         int slow = 0;                       // first half that is left to the loop below
-        if (lim0 >= kKeys) {
+        if (lim0 >= kKeys && !unset) {
           float s0[kHalf], s1[kHalf];
           uint32_t p[32];
           tmem_ld64(tS, s0);
@@ -667,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // Blocks with masked keys, and rows that outgrew their scale: a loop
+        // Blocks with masked keys, and rows that outgrew their scale or have none: a loop
         // over the halves, one piece of code.  (Code that does not stay in the
         // instruction cache costs ~100 cycles per eight instructions: with the
         // rare cases written out twice a first block took 3500 cycles.)
