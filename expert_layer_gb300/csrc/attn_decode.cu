@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = gq + 8 * rs;
           if (r >= rows) continue;
           const long long row = (long long)cur.b * a.Hq + h0 + r;
-          const float inv = 1.0f / l[rs], lse = m[rs] + lg2(l[rs]);
+          // (every logit -inf: a weight of 0 and a log-sum of -inf, as without keys)
+          const float inv = l[rs] > 0.f ? 1.0f / l[rs] : l[rs], lse = m[rs] + lg2(l[rs]);
           if (t.p.row_o) {
             if (lane == 0 && rs == 0) t.p.held[cur.b * units + cur.u] = make_int2(1, 0);
 #pragma unroll
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         v.z = fmaf(w, x[k].z, v.z);
         v.w = fmaf(w, x[k].w, v.w);
       }
-      const float inv = 1.0f / sum;
+      const float inv = sum > 0.f ? 1.0f / sum : sum;        // 0 stays 0, NaN stays NaN
       v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
       const float lse = M + lg2(sum);
       const long long row = (long long)op.b * a.Hq + h0 + r;

@@ -422,7 +422,7 @@ int moe_rope_append(const moe_heads *q, const moe_heads *k, const moe_heads *v, 
  *   out[t, h] = sum_j p_j v[j, h/G],  p = softmax_j(scale * q[t, h] . k[j, h/G])
  * over the keys j of row t's own sequence; with causal != 0 row i of a
  * sequence of n rows and m keys sees the keys j <= i + (m - n).  A row that
- * sees no key gets out = 0 and lse = -inf.
+ * sees no key, or none whose logit is above -inf, gets out = 0 and lse = -inf.
  *   q_starts, kv_starts [n_seq + 1] int32, ascending from 0 to T and Tk: the
  *            rows / keys of sequence s are [starts[s], starts[s+1])
  *   out      [T, Hq, D] dense;  lse [T, Hq] fp32 or NULL: the natural log of
@@ -453,7 +453,8 @@ int moe_attn_prefill_paged(const moe_heads *q, const moe_kv_cache *cache, const 
  * prefix_table[0 ..], the same for every row; prefix_table may be NULL when
  * prefix_len is 0) followed by its own kv_lens[b] tokens on
  * page_table[b, 0 ..].  The prefix is read and multiplied once for the whole
- * batch.  A row without any key gets out = 0, lse = -inf.
+ * batch.  A row without any key, or with none whose logit is above -inf, gets
+ * out = 0, lse = -inf.
  * B * (table_pages * page_size / 16 + 1) * Hkv * ceil(G / 16) must stay below 2^31.
  */
 int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t *page_table,

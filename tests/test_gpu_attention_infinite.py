@@ -115,7 +115,7 @@ DECODE = [
 ]
 
 
-@pytest.mark.parametrize("gone", ["first16", "every third"])
+@pytest.mark.parametrize("gone", ["first16", "first block", "every third", "all"])
 @pytest.mark.parametrize("case,where", [(c, w) for c in DECODE for w in (["prefix", "own", "both"] if c[1] else ["own"])],
                          ids=lambda c: c if isinstance(c, str) else f"{c[2]}x{c[3]}x{c[4]}-B{len(c[0])}-{max(c[0])}-pre{c[1]}")
 def test_decode(case, where, gone):
