@@ -11,6 +11,11 @@ they do so in compiled code (``_attn_binding.so``, 3 to 7 us a call instead of
 
 A cache is two tensors [pages, Hkv, page_size, D]; a page table row lists a
 sequence's pages, token j sits in row j % page_size of page j // page_size.
+
+``stream``: the stream to launch on (default: the current one).  Outputs and
+workspaces that a call makes come from its memory; that the tensors passed in
+are ready there, and kept until it is past them, is the caller's business, as
+with any use of a tensor on another stream.
 """
 from __future__ import annotations
 

@@ -7,12 +7,14 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -128,46 +130,50 @@ Cache cache(PyObject* k, PyObject* v, const Query& q) {
                whole(kt.size(1), "k_cache")};
 }
 
-// Tensors that a call allocates: on another stream than the current one they
-// stay reserved until the work there is done.
-struct Made {
-  std::vector<at::Tensor> all;
-  at::Tensor add(at::IntArrayRef shape, at::ScalarType type, int device) {
-    all.push_back(at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, device))));
-    return all.back();
+// Where a call runs.  What it allocates comes from that stream's memory: a
+// block of the caller's stream that was just freed may still be in use by work
+// queued there, for which another stream does not wait.
+struct Run {
+  int device;
+  void* stream;
+  c10::cuda::CUDAStream callers;
+  std::optional<c10::cuda::CUDAStreamGuard> guard;        // of a launch stream that is not the caller's
+  std::vector<at::Tensor> made;
+
+  Run(PyObject* given_stream, int dev) : device(dev), callers(c10::cuda::getCurrentCUDAStream(dev)) {
+    stream = callers.stream();
+    if (!given(given_stream)) return;
+    PyObject* attr = PyObject_GetAttrString(given_stream, "cuda_stream");
+    if (!attr) throw PythonError{};
+    stream = PyLong_AsVoidPtr(attr);
+    Py_DECREF(attr);
+    if (PyErr_Occurred()) throw PythonError{};
+    if (stream != callers.stream())
+      guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), dev));
+  }
+  at::Tensor make(at::IntArrayRef shape, at::ScalarType type) {
+    made.push_back(at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, device))));
+    return made.back();
+  }
+  // a tensor that the caller gets: freed, it is kept until the caller's stream is past it
+  at::Tensor returned(const at::Tensor& t) {
+    if (guard) t.record_stream(callers.unwrap());
+    return t;
   }
 };
-void* launch_stream(PyObject* stream, int device, const Made& made) {
-  void* current = c10::cuda::getCurrentCUDAStream(device).stream();
-  if (!given(stream)) return current;
-  PyObject* attr = PyObject_GetAttrString(stream, "cuda_stream");
-  if (!attr) throw PythonError{};
-  void* s = PyLong_AsVoidPtr(attr);
-  Py_DECREF(attr);
-  if (PyErr_Occurred()) throw PythonError{};
-  if (s != current)
-    for (const at::Tensor& t : made.all) {
-      PyObject* w = THPVariable_Wrap(t);
-      PyObject* r = w ? PyObject_CallMethod(w, "record_stream", "O", stream) : nullptr;
-      Py_XDECREF(w);
-      if (!r) throw PythonError{};
-      Py_DECREF(r);
-    }
-  return s;
-}
 
 struct Space {
   void* data;
   size_t bytes;
 };
-Space workspace(PyObject* o, int T, int n_seq, int Hq, int Hkv, int D, int device, Made& made) {
+Space workspace(PyObject* o, int T, int n_seq, int Hq, int Hkv, int D, Run& run) {
   if (given(o)) {
-    const at::Tensor& t = dense(o, "workspace", at::kByte, {-1}, device);
+    const at::Tensor& t = dense(o, "workspace", at::kByte, {-1}, run.device);
     return Space{t.data_ptr(), (size_t)t.numel()};
   }
   const size_t n = lib.workspace_size(T > 0 ? T : 1, n_seq, Hq, Hkv, D);
   if (n == 0) throw Refusal{"unsupported shape"};
-  return Space{made.add({(int64_t)n}, at::kByte, device).data_ptr(), n};
+  return Space{run.make({(int64_t)n}, at::kByte).data_ptr(), n};
 }
 
 // An output of this shape: the caller's, or a new one (then `wrapped` owns it)
@@ -175,13 +181,13 @@ struct Output {
   PyObject* object;
   void* data;
 };
-Output output(PyObject* o, const char* name, const Query& q, Made& made) {
+Output output(PyObject* o, const char* name, const Query& q, Run& run) {
   if (given(o)) {
     void* data = dense(o, name, q.type, {q.T, q.Hq, q.D}, q.device).data_ptr();
     Py_INCREF(o);
     return Output{o, data};
   }
-  at::Tensor t = made.add({q.T, q.Hq, q.D}, q.type, q.device);
+  at::Tensor t = run.returned(run.make({q.T, q.Hq, q.D}, q.type));
   return Output{THPVariable_Wrap(t), t.data_ptr()};
 }
 struct Owned {      // gives the reference back unless it is returned
@@ -291,13 +297,13 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const float* kn = given(a.v[9]) ? ptr<float>(dense(a.v[9], "k_norm", at::kFloat, {q.D}, q.device)) : nullptr;
     const float eps = (float)number(a.v[10], 1e-6);
     const bool interleaved = truth(a.v[11], false);
-    Made made;
-    const Output out = output(a.v[12], "q_out", q, made);
+    Run run(a.v[14], q.device);
+    const Output out = output(a.v[12], "q_out", q, run);
     Owned owned{out.object};
-    const Space ws = workspace(a.v[13], q.T, 0, q.Hq, c.Hkv, q.D, q.device, made);
+    const Space ws = workspace(a.v[13], q.T, 0, q.Hq, c.Hkv, q.D, run);
     check(lib.rope_append(&q.view, &k, &v, qn, kn, eps, ptr<float>(table), whole(table.size(0), "table"),
                           whole(table.size(1), "table"), interleaved, pos, slots, q.T, q.Hq, c.Hkv, q.D, q.code,
-                          out.data, &c.c, ws.data, ws.bytes, launch_stream(a.v[14], q.device, made)),
+                          out.data, &c.c, ws.data, ws.bytes, run.stream),
           "moe_rope_append");
     return owned.release();
   });
@@ -321,14 +327,13 @@ PyObject* attn_prefill(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
     if (seqs < 0) throw Refusal{"q_starts must have n_seq + 1 entries"};
     const at::Tensor& ks = dense(a.v[4], "kv_starts", at::kInt, {seqs + 1}, q.device);
     const int Tk = whole(kt.size(0), "k"), Hkv = whole(kt.size(1), "k");
-    Made made;
-    const Output out = output(a.v[7], "out", q, made);
+    Run run(a.v[10], q.device);
+    const Output out = output(a.v[7], "out", q, run);
     Owned owned{out.object};
     float* lse = lse_of(a.v[8], q);
-    const Space ws = workspace(a.v[9], q.T, seqs, q.Hq, Hkv, q.D, q.device, made);
+    const Space ws = workspace(a.v[9], q.T, seqs, q.Hq, Hkv, q.D, run);
     check(lib.prefill(&q.view, &k, &v, ptr<int32_t>(qs), ptr<int32_t>(ks), seqs, q.T, Tk, q.Hq, Hkv, q.D, q.code,
-                      truth(a.v[5], true), scale_of(a.v[6], q.D), out.data, lse, ws.data, ws.bytes,
-                      launch_stream(a.v[10], q.device, made)),
+                      truth(a.v[5], true), scale_of(a.v[6], q.D), out.data, lse, ws.data, ws.bytes, run.stream),
           "moe_attn_prefill");
     return owned.release();
   });
@@ -346,15 +351,15 @@ PyObject* attn_prefill_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
     const int seqs = whole(lens.size(0), "kv_lens");
     const at::Tensor& qs = dense(a.v[4], "q_starts", at::kInt, {seqs + 1}, q.device);
     const at::Tensor& table = dense(a.v[3], "page_table", at::kInt, {seqs, -1}, q.device);
-    Made made;
-    const Output out = output(a.v[8], "out", q, made);
+    Run run(a.v[11], q.device);
+    const Output out = output(a.v[8], "out", q, run);
     Owned owned{out.object};
     float* lse = lse_of(a.v[9], q);
-    const Space ws = workspace(a.v[10], q.T, seqs, q.Hq, c.Hkv, q.D, q.device, made);
+    const Space ws = workspace(a.v[10], q.T, seqs, q.Hq, c.Hkv, q.D, run);
     check(lib.prefill_paged(&q.view, &c.c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(qs),
                             ptr<int32_t>(lens), seqs, q.T, q.Hq, c.Hkv, q.D, q.code, truth(a.v[6], true),
                             scale_of(a.v[7], q.D), out.data, lse, ws.data, ws.bytes,
-                            launch_stream(a.v[11], q.device, made)),
+                            run.stream),
           "moe_attn_prefill_paged");
     return owned.release();
   });
@@ -380,14 +385,14 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
                       std::to_string(prefix_len) + " tokens"};
       prefix = ptr<int32_t>(pt);
     }
-    Made made;
-    const Output out = output(a.v[8], "out", q, made);
+    Run run(a.v[11], q.device);
+    const Output out = output(a.v[8], "out", q, run);
     Owned owned{out.object};
     float* lse = lse_of(a.v[9], q);
-    const Space ws = workspace(a.v[10], q.T, q.T, q.Hq, c.Hkv, q.D, q.device, made);
+    const Space ws = workspace(a.v[10], q.T, q.T, q.Hq, c.Hkv, q.D, run);
     check(lib.decode(&q.view, &c.c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(lens), prefix,
                      prefix_len, q.T, q.Hq, c.Hkv, q.D, q.code, scale_of(a.v[7], q.D), out.data, lse, ws.data, ws.bytes,
-                     launch_stream(a.v[11], q.device, made)),
+                     run.stream),
           "moe_attn_decode");
     return owned.release();
   });
