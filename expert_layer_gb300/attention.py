@@ -134,8 +134,11 @@ def attn_prefill(q, k, v, q_starts, kv_starts, causal=True, scale=None, out=None
                  stream=None):
     """Attention of packed sequences: q [T, Hq, D], k and v [Tk, Hkv, D];
     sequence s has the rows q_starts[s] .. q_starts[s+1] and the keys
-    kv_starts[s] .. kv_starts[s+1] (int32 [n_seq + 1]).  With ``causal`` the
-    last row of a sequence sees its last key.  Returns out [T, Hq, D];
+    kv_starts[s] .. kv_starts[s+1] (int32 [n_seq + 1]).  q_starts go from 0 to
+    T: rows outside are left as they were and reported (``read_status``);
+    padding rows can be a last sequence without keys.  With ``causal`` the
+    last row of a sequence sees its last key, and the values that a row does
+    not see must be finite (a weight of 0 does not silence them).  Returns out [T, Hq, D];
     ``lse`` (fp32 [T, Hq]) optionally receives the log of the softmax
     denominators.  ``scale`` defaults to 1 / sqrt(D)."""
     return _load().attn_prefill(q, k, v, q_starts, kv_starts, causal, scale, out, lse, workspace, stream)

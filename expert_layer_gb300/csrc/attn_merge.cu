@@ -42,12 +42,29 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = t.G;
   const long long rows = (long long)a.T * a.Hq;
+  // Rows of no sequence (reported by the kernel before) have no parts and stay
+  // as they are.  Whether there are any is seen while that kernel runs; a call
+  // with parts has few sequences (tc_splits).
+  bool tidy = true;
+  if (t.grid == 0) {
+    for (int s = lane; s < a.n_seq; s += 32) tidy &= a.q_starts[s] <= a.q_starts[s + 1];
+    tidy = __all_sync(0xffffffffu, tidy) && a.q_starts[0] == 0 && a.q_starts[a.n_seq] == a.T;
+  }
   pdl_wait();   // programmatic dependent launch: the parts are complete
 #pragma unroll 1
   for (unsigned i = blockIdx.x; i < t.todo; i += gridDim.x) {
     // blocks c0 .. c0 + own - 1 of the decode kernel hold the row's own keys
     int c0 = 0, own = 0, r = 0, parts = 0;
     long long row = i;
+    bool ours = tidy;
+    if (!tidy) {
+      const int token = t.by_Hq.of((int)i);
+      for (int s = lane; s < a.n_seq; s += 32) {
+        const int q0 = a.q_starts[s], q1 = a.q_starts[s + 1];
+        ours |= q0 >= 0 && q0 <= token && token < q1 && q1 <= a.T;
+      }
+      ours = __any_sync(0xffffffffu, ours);
+    }
     if (!t.splits) {
       c0 = t.by_rows.of((int)i);
       r = (int)i - c0 * t.rows;
@@ -114,7 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
     if (lane == 0) s_ml[warp] = make_float2(m, sum);
     __syncthreads();
     const int x = threadIdx.x;
-    if (x < D / 2) {
+    if (x < D / 2 && ours) {
       float top = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w].x);

@@ -221,7 +221,7 @@ __device__ __forceinline__ bool make_item(const TcAttnArgs& t, int idx, Item& it
 // Index arrays of the call, checked once (by the warp that has item 0): what is
 // out of order is reported here and skipped or clamped where it is used.
 __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
-  bool bad = false;
+  bool bad = a.q_starts && (a.q_starts[0] != 0 || a.q_starts[a.n_seq] != a.T);      // rows of no sequence
   if (a.q_starts)
     for (int s = threadIdx.x & 31; s < a.n_seq; s += 32) {
       const int q0 = a.q_starts[s], q1 = a.q_starts[s + 1];

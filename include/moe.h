@@ -423,8 +423,11 @@ int moe_rope_append(const moe_heads *q, const moe_heads *k, const moe_heads *v, 
  * over the keys j of row t's own sequence; with causal != 0 row i of a
  * sequence of n rows and m keys sees the keys j <= i + (m - n).  A row that
  * sees no key, or none whose logit is above -inf, gets out = 0 and lse = -inf.
- *   q_starts, kv_starts [n_seq + 1] int32, ascending from 0 to T and Tk: the
- *            rows / keys of sequence s are [starts[s], starts[s+1])
+ *   q_starts, kv_starts [n_seq + 1] int32, ascending: the rows / keys of
+ *            sequence s are [starts[s], starts[s+1]).  q_starts go from 0 to T
+ *            (rows that no sequence has are reported as MOE_ERR_DEVICE and
+ *            left as they were; padding rows can be a last sequence without
+ *            keys), kv_starts lie within [0, Tk].
  *   out      [T, Hq, D] dense;  lse [T, Hq] fp32 or NULL: the natural log of
  *            the softmax denominator, log sum_j exp(scale * q . k_j)
  * Keys and values that a row does not see through the causal mask must be
