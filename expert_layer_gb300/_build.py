@@ -1,5 +1,7 @@
 """Builds libmoe_gb300.so in-tree with nvcc for sm_103a, and the Python binding
-of the attention functions (_attn_binding.so) with the host compiler.
+of the attention functions (_attn_binding.so) with the host compiler.  The
+library needs nvcc alone: where the binding cannot be built (no g++, or no
+headers of PyTorch or Python), the build warns and those functions raise.
 
 Each .cu file under csrc/ compiles to its own object (in parallel); the
 objects link into expert_layer_gb300/libmoe_gb300.so.  A file is recompiled
@@ -11,12 +13,15 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BINDING = os.path.join(PKG, "_attn_binding.so")
+CXX = "g++"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -43,13 +48,14 @@ def sources():
 def build_binding(verbose: bool = False) -> str:
     """Compile the extension module of the attention functions (host C++ against
     this PyTorch's headers); returns its path.  Rebuilt when its source, the
-    C header, PyTorch or Python changed."""
+    C header, PyTorch or Python changed; put in place whole, so that a process
+    that has the old one mapped keeps it."""
     import sysconfig
 
     import torch
 
     src = os.path.join(CSRC, "attn_binding.cpp")
-    out = os.path.join(PKG, "_attn_binding.so")
+    out, part = BINDING, f"{BINDING}.{os.getpid()}.so"
     made_for = os.path.join(BUILD, "attn_binding.for")
     this = f"{torch.__version__} {torch.__file__} {sysconfig.get_config_var('EXT_SUFFIX')}"
     newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "moe.h")))
@@ -59,16 +65,24 @@ def build_binding(verbose: bool = False) -> str:
                 return out
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(at, "include"),
            "-I", os.path.join(at, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", out,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o", part,
            "-L", os.path.join(at, "lib"), "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{CXX} failed for {src}:\n{r.stdout}\n{r.stderr}")
+        os.replace(part, out)
+    except (RuntimeError, OSError):
+        for f in (part, out):             # one for other sources or another PyTorch is not left behind
+            if os.path.exists(f):
+                os.remove(f)
+        raise
     with open(made_for, "w") as f:
         f.write(this)
     return out
@@ -103,13 +117,16 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None, build_dir
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         binding = None if lib_path else ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources()))
-        if binding is not None:
-            binding.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc, *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if binding is not None:
+        try:
+            binding.result()
+        except (RuntimeError, OSError, ImportError) as e:
+            warnings.warn(f"the attention functions are not available, their binding was not built: {e}", stacklevel=2)
     return LIB
 
 
