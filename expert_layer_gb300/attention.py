@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib
+import inspect
 import math
 import sys
 
@@ -48,8 +49,10 @@ _native = None
 def _load():
     """The compiled binding (csrc/attn_binding.cpp), connected to the library.
 
-    Its functions take the place of the ones below, in this module and in the
-    package, on the first call."""
+    Its functions take their parameters, defaults and documentation from the
+    ones below and their place, in this module and in the package, on the first
+    call; a name imported from here before that goes on through the one below
+    (0.15 us more a call)."""
     global _native
     if _native is None:
         handle = lib()
@@ -60,8 +63,10 @@ def _load():
                            f"`python -m expert_layer_gb300._build` ({e})") from e
         native.bind(MoEError, *(ctypes.cast(getattr(handle, n), _P).value for n in (
             "moe_attn_workspace_size", "moe_rope_append", "moe_attn_prefill", "moe_attn_prefill_paged",
-            "moe_attn_decode", "moe_error_string")))
-        for name in ("rope_append", "attn_prefill", "attn_prefill_paged", "attn_decode"):
+            "moe_attn_decode", "moe_error_string")), *(
+                (tuple(inspect.signature(f).parameters), f.__defaults__ or (),
+                 f"{f.__name__}{inspect.signature(f)}\n--\n\n{inspect.getdoc(f)}") for f in _FUNCTIONS))
+        for name in (f.__name__ for f in _FUNCTIONS):
             for module in (sys.modules[__name__], sys.modules[__package__]):
                 setattr(module, name, getattr(native, name))
         _native = native
@@ -161,3 +166,6 @@ def attn_decode(q, k_cache, v_cache, page_table, kv_lens, prefix_table=None, pre
     page_table[b]; the prefix is read once for the whole batch."""
     return _load().attn_decode(q, k_cache, v_cache, page_table, kv_lens, prefix_table, prefix_len, scale, out, lse,
                                workspace, stream)
+
+
+_FUNCTIONS = (rope_append, attn_prefill, attn_prefill_paged, attn_decode)

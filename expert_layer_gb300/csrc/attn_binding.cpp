@@ -206,17 +206,22 @@ void check(int rc, const char* what) {
 }
 
 // ------------------------------------------------------------- arguments
+// A function's parameters, defaults and documentation are those of its Python
+// definition (attention.py), handed over by bind(); the functions below take
+// them in that order.
 constexpr int kMost = 17;
 struct Spec {
   const char* function;
-  int required, total;
-  const char* names[kMost];
-  PyObject* interned[kMost];
+  int total;
+  int required;
+  PyObject* names[kMost];         // interned
+  PyObject* defaults[kMost];      // null where required
+  std::string doc;
 };
 struct Args {
   PyObject* v[kMost] = {};
 };
-Args parse(Spec& s, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
+Args parse(const Spec& s, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
   Args a;
   if (!lib.rope_append) throw Refusal{"the attention functions are not bound to the library"};
   const std::string f = std::string(s.function) + "() ";
@@ -230,18 +235,18 @@ Args parse(Spec& s, PyObject* const* args, Py_ssize_t n, PyObject* kwnames) {
     PyObject* name = PyTuple_GET_ITEM(kwnames, i);
     int at = -1;
     for (int j = 0; j < s.total && at < 0; ++j)
-      if (s.interned[j] == name) at = j;
+      if (s.names[j] == name) at = j;
     for (int j = 0; j < s.total && at < 0; ++j)
-      if (PyUnicode_Compare(s.interned[j], name) == 0) at = j;
+      if (PyUnicode_Compare(s.names[j], name) == 0) at = j;
     if (at < 0 || a.v[at]) {
       PyErr_Format(PyExc_TypeError, "%s() got an unexpected or repeated argument '%U'", s.function, name);
       throw PythonError{};
     }
     a.v[at] = args[n + i];
   }
-  for (int j = 0; j < s.required; ++j)
-    if (!a.v[j]) {
-      PyErr_SetString(PyExc_TypeError, (f + "misses the argument '" + s.names[j] + "'").c_str());
+  for (int j = 0; j < s.total; ++j)
+    if (!a.v[j] && !(a.v[j] = s.defaults[j])) {
+      PyErr_Format(PyExc_TypeError, "%s() misses the argument '%U'", s.function, s.names[j]);
       throw PythonError{};
     }
   return a;
@@ -258,8 +263,7 @@ long integer(PyObject* o, long otherwise, const char* name) {
   if (v == -1 && PyErr_Occurred()) throw PythonError{};
   return whole(v, name);
 }
-bool truth(PyObject* o, bool otherwise) {
-  if (!o) return otherwise;
+bool truth(PyObject* o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw PythonError{};
   return v != 0;
@@ -280,9 +284,7 @@ PyObject* guarded(F f) {
 }
 
 // ------------------------------------------------------------- functions
-Spec rope_spec = {"rope_append", 8, 15,
-                  {"q", "k", "v", "table", "positions", "slots", "k_cache", "v_cache", "q_norm", "k_norm", "eps",
-                   "interleaved", "q_out", "workspace", "stream"}, {}};
+Spec rope_spec = {"rope_append", 15};
 PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     const Args a = parse(rope_spec, args, n, kw);
@@ -296,7 +298,7 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const float* qn = given(a.v[8]) ? ptr<float>(dense(a.v[8], "q_norm", at::kFloat, {q.D}, q.device)) : nullptr;
     const float* kn = given(a.v[9]) ? ptr<float>(dense(a.v[9], "k_norm", at::kFloat, {q.D}, q.device)) : nullptr;
     const float eps = (float)number(a.v[10], 1e-6);
-    const bool interleaved = truth(a.v[11], false);
+    const bool interleaved = truth(a.v[11]);
     Run run(a.v[14], q.device);
     const Output out = output(a.v[12], "q_out", q, run);
     Owned owned{out.object};
@@ -313,9 +315,7 @@ float* lse_of(PyObject* o, const Query& q) {
   return given(o) ? ptr<float>(dense(o, "lse", at::kFloat, {q.T, q.Hq}, q.device)) : nullptr;
 }
 
-Spec prefill_spec = {"attn_prefill", 5, 11,
-                     {"q", "k", "v", "q_starts", "kv_starts", "causal", "scale", "out", "lse", "workspace", "stream"},
-                     {}};
+Spec prefill_spec = {"attn_prefill", 11};
 PyObject* attn_prefill(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     const Args a = parse(prefill_spec, args, n, kw);
@@ -333,15 +333,13 @@ PyObject* attn_prefill(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject*
     float* lse = lse_of(a.v[8], q);
     const Space ws = workspace(a.v[9], q.T, seqs, q.Hq, Hkv, q.D, run);
     check(lib.prefill(&q.view, &k, &v, ptr<int32_t>(qs), ptr<int32_t>(ks), seqs, q.T, Tk, q.Hq, Hkv, q.D, q.code,
-                      truth(a.v[5], true), scale_of(a.v[6], q.D), out.data, lse, ws.data, ws.bytes, run.stream),
+                      truth(a.v[5]), scale_of(a.v[6], q.D), out.data, lse, ws.data, ws.bytes, run.stream),
           "moe_attn_prefill");
     return owned.release();
   });
 }
 
-Spec paged_spec = {"attn_prefill_paged", 6, 12,
-                   {"q", "k_cache", "v_cache", "page_table", "q_starts", "kv_lens", "causal", "scale", "out", "lse",
-                    "workspace", "stream"}, {}};
+Spec paged_spec = {"attn_prefill_paged", 12};
 PyObject* attn_prefill_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     const Args a = parse(paged_spec, args, n, kw);
@@ -357,7 +355,7 @@ PyObject* attn_prefill_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
     float* lse = lse_of(a.v[9], q);
     const Space ws = workspace(a.v[10], q.T, seqs, q.Hq, c.Hkv, q.D, run);
     check(lib.prefill_paged(&q.view, &c.c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(qs),
-                            ptr<int32_t>(lens), seqs, q.T, q.Hq, c.Hkv, q.D, q.code, truth(a.v[6], true),
+                            ptr<int32_t>(lens), seqs, q.T, q.Hq, c.Hkv, q.D, q.code, truth(a.v[6]),
                             scale_of(a.v[7], q.D), out.data, lse, ws.data, ws.bytes,
                             run.stream),
           "moe_attn_prefill_paged");
@@ -365,9 +363,7 @@ PyObject* attn_prefill_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
   });
 }
 
-Spec decode_spec = {"attn_decode", 5, 12,
-                    {"q", "k_cache", "v_cache", "page_table", "kv_lens", "prefix_table", "prefix_len", "scale", "out",
-                     "lse", "workspace", "stream"}, {}};
+Spec decode_spec = {"attn_decode", 12};
 PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     const Args a = parse(decode_spec, args, n, kw);
@@ -398,14 +394,57 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   });
 }
 
-// bind(error type, addresses of the library's functions in the order of Library)
+PyObject* bind(PyObject*, PyObject* args);
+
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL | METH_KEYWORDS
+PyMethodDef methods[] = {
+    {"rope_append", FAST(rope_append), nullptr},
+    {"attn_prefill", FAST(attn_prefill), nullptr},
+    {"attn_prefill_paged", FAST(attn_prefill_paged), nullptr},
+    {"attn_decode", FAST(attn_decode), nullptr},
+    {"bind", bind, METH_VARARGS, "Connect the functions to a loaded library and to their Python definitions."},
+    {nullptr, nullptr, 0, nullptr}};
+
+// bind(error type, addresses of the library's functions in the order of
+// Library, then for each of the first four methods (parameter names, defaults
+// of the last of them, documentation))
 PyObject* bind(PyObject*, PyObject* args) {
   PyObject* err;
   unsigned long long p[6];
-  if (!PyArg_ParseTuple(args, "OKKKKKK", &err, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5])) return nullptr;
+  PyObject *names[4], *defaults[4];
+  const char* doc[4];
+  if (!PyArg_ParseTuple(args, "OKKKKKK(O!O!s)(O!O!s)(O!O!s)(O!O!s)", &err, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5],
+                        &PyTuple_Type, &names[0], &PyTuple_Type, &defaults[0], &doc[0],
+                        &PyTuple_Type, &names[1], &PyTuple_Type, &defaults[1], &doc[1],
+                        &PyTuple_Type, &names[2], &PyTuple_Type, &defaults[2], &doc[2],
+                        &PyTuple_Type, &names[3], &PyTuple_Type, &defaults[3], &doc[3]))
+    return nullptr;
+  Spec* specs[4] = {&rope_spec, &prefill_spec, &paged_spec, &decode_spec};
+  for (int f = 0; f < 4; ++f) {
+    Spec& s = *specs[f];
+    if (PyTuple_GET_SIZE(names[f]) != s.total || PyTuple_GET_SIZE(defaults[f]) > s.total) {
+      PyErr_Format(PyExc_TypeError, "%s: %d parameters expected", s.function, s.total);
+      return nullptr;
+    }
+    s.required = s.total - (int)PyTuple_GET_SIZE(defaults[f]);
+    for (int i = 0; i < s.total; ++i) {
+      PyObject* name = PyTuple_GET_ITEM(names[f], i);
+      if (!PyUnicode_Check(name)) {
+        PyErr_SetString(PyExc_TypeError, "parameter names must be strings");
+        return nullptr;
+      }
+      Py_INCREF(name);
+      PyUnicode_InternInPlace(&name);
+      Py_XSETREF(s.names[i], name);
+      PyObject* value = i < s.required ? nullptr : PyTuple_GET_ITEM(defaults[f], i - s.required);
+      Py_XINCREF(value);
+      Py_XSETREF(s.defaults[i], value);
+    }
+    s.doc = doc[f];
+    methods[f].ml_doc = s.doc.c_str();
+  }
   Py_INCREF(err);
-  Py_XDECREF(error_type);
-  error_type = err;
+  Py_XSETREF(error_type, err);
   lib.workspace_size = reinterpret_cast<decltype(lib.workspace_size)>(p[0]);
   lib.rope_append = reinterpret_cast<decltype(lib.rope_append)>(p[1]);
   lib.prefill = reinterpret_cast<decltype(lib.prefill)>(p[2]);
@@ -415,21 +454,8 @@ PyObject* bind(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
-#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL | METH_KEYWORDS
-PyMethodDef methods[] = {
-    {"rope_append", FAST(rope_append), "See expert_layer_gb300.attention.rope_append."},
-    {"attn_prefill", FAST(attn_prefill), "See expert_layer_gb300.attention.attn_prefill."},
-    {"attn_prefill_paged", FAST(attn_prefill_paged), "See expert_layer_gb300.attention.attn_prefill_paged."},
-    {"attn_decode", FAST(attn_decode), "See expert_layer_gb300.attention.attn_decode."},
-    {"bind", bind, METH_VARARGS, "Connect the functions to a loaded library."},
-    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_binding", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__attn_binding() {
-  for (Spec* s : {&rope_spec, &prefill_spec, &paged_spec, &decode_spec})
-    for (int i = 0; i < s->total; ++i)
-      if (!(s->interned[i] = PyUnicode_InternFromString(s->names[i]))) return nullptr;
-  return PyModule_Create(&module);
-}
+PyMODINIT_FUNC PyInit__attn_binding() { return PyModule_Create(&module); }
