@@ -36,6 +36,7 @@ _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
 SIGNATURES = {
     "moe_attn_workspace_size": (_SZ, [_I] * 5),
+    "moe_debug_attn_wait_timeout": (_I, [_I]),
     "moe_rope_append": (_I, [_P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ,
                              _P]),
     "moe_attn_prefill": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),

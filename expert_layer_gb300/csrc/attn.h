@@ -123,6 +123,11 @@ struct RopeArgs {
   Divisor by_chunks;
 };
 
+// Barriers that are made to wait for an arrival that never comes, in tests only
+// (moe_debug_attn_wait_timeout): their arrival count, a kernel argument, is one
+// too many
+enum Hold { kHoldNone, kHoldDecode, kHolds };
+
 // One attention call.  Packed keys: k, v, kv_starts.  Paged: k_cache,
 // v_cache, page_table, kv_lens.  Decode is n_seq rows of one token each
 // (q_starts null) with an optional shared prefix.
@@ -141,6 +146,7 @@ struct AttnArgs {
   float scale;
   uint16_t* out;              // [T, Hq, D]
   float* lse;                 // [T, Hq] or null
+  int hold;                   // Hold
 };
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);

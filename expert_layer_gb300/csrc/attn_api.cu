@@ -1,7 +1,10 @@
 // C ABI of the attention operators: argument checks and launches.  Nothing
-// here allocates, synchronises or keeps state between calls.
+// here allocates, synchronises or keeps state between calls (but for the
+// test-only setting of the waits).
 #include <limits.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "moe.h"
 #include "attn.h"
@@ -35,6 +38,9 @@ int read_flags(const void* workspace) {
 }  // namespace moe
 
 namespace {
+
+// Test-only (moe_debug_attn_wait_timeout)
+std::atomic<int> g_hold{kHoldNone};
 
 #define ATTN_TRY(expr)             \
   do {                             \
@@ -148,6 +154,7 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   a.f16 = dtype == MOE_F16;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  a.hold = g_hold.load(std::memory_order_relaxed);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sms > kMaxBlocks) sms = kMaxBlocks;
   const Report rep{workspace, 1, {0, 0}};
@@ -168,6 +175,12 @@ extern "C" {
 size_t moe_attn_workspace_size(int T, int n_seq, int Hq, int Hkv, int D) {
   if (check_shape(T, n_seq, Hq, Hkv, D) != MOE_OK) return 0;
   return make_attn_layout(T, n_seq, Hq, Hkv, D).total;
+}
+
+int moe_debug_attn_wait_timeout(int wait) {
+  if (wait < 0 || wait >= kHolds) return MOE_ERR_INVALID_ARG;
+  g_hold.store(wait);
+  return MOE_OK;
 }
 
 int moe_rope_append(const moe_heads* q, const moe_heads* k, const moe_heads* v, const float* q_norm,

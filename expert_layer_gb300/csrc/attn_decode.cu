@@ -75,6 +75,7 @@ struct DecodeArgs {
   int G;                // Hq / Hkv
   int chunks;           // units per key-value head
   int few, head;        // of Line
+  int arrivals;         // that a stage's barrier waits for: 1, or one too many
   DecodeParts p;
 };
 
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], t.arrivals);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     open[2 * warp].b = open[2 * warp + 1].b = -1;
@@ -306,7 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int s = first; s < last; ++s) {
         const int st = used % kStages;
-        if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true;
+        // after a timeout nothing more is loaded: a stage whose load has not
+        // landed must not be loaded again, nor its barrier be armed again
+        if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true, more = false;
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -563,6 +566,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const De
   t.chunks = decode_chunks(a);
   t.few = beside.few;
   t.head = beside.head;
+  t.arrivals = a.hold == kHoldDecode ? 2 : 1;
   t.p = p;
   CUtensorMap k, v;
   if (!pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice)) return cudaErrorInvalidValue;

@@ -465,6 +465,18 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
                     int prefix_len, int B, int Hq, int Hkv, int D, int dtype, float scale, void *out,
                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * TEST ONLY.  With wait > 0, every moe_attn_* launched afterwards in this
+ * process has some barriers of its kernels wait for an arrival that never
+ * comes, until the waits give up as every one does after half a second: the
+ * call completes, its results are unspecified, and moe_read_status reports
+ * MOE_ERR_DEVICE_TIMEOUT.  (wait 1: keys and values of moe_attn_decode.)
+ * wait == 0 restores normal operation (the default).  Process-wide, not
+ * thread-safe with concurrent calls; it exists so that tests can run what
+ * follows a wait that gives up, without a hung or faulted GPU.
+ */
+int moe_debug_attn_wait_timeout(int wait);
+
 /* Static, human-readable name of a moe_status value. */
 const char *moe_error_string(int status);
 
