@@ -126,7 +126,11 @@ struct RopeArgs {
 // Barriers that are made to wait for an arrival that never comes, in tests only
 // (moe_debug_attn_wait_timeout): their arrival count, a kernel argument, is one
 // too many
-enum Hold { kHoldNone, kHoldDecode, kHolds };
+enum Hold {
+  kHoldNone, kHoldDecode,
+  kHoldKeys, kHoldStage, kHoldQuery, kHoldS, kHoldP, kHoldO, kHoldHalf, kHoldTurn, kHoldItem, kHoldNext,    // attn_tc.cu
+  kHolds
+};
 
 // One attention call.  Packed keys: k, v, kv_starts.  Paged: k_cache,
 // v_cache, page_table, kv_lens.  Decode is n_seq rows of one token each

@@ -82,6 +82,15 @@ struct Item {
   int split;
 };
 
+// Arrivals that the barriers wait for, one too many where a test holds one
+struct Arrivals {
+  int keys, stage, query, s, p, o, half, turn, item, next;
+  Arrivals(int hold = kHoldNone)
+      : keys(1 + (hold == kHoldKeys)), stage(2 + (hold == kHoldStage)), query(1 + (hold == kHoldQuery)),
+        s(1 + (hold == kHoldS)), p(4 + (hold == kHoldP)), o(1 + (hold == kHoldO)), half(1 + (hold == kHoldHalf)),
+        turn(4 + (hold == kHoldTurn)), item(1 + (hold == kHoldItem)), next(1 + (hold == kHoldNext)) {}
+};
+
 struct TcAttnArgs {
   AttnArgs a;
   int G;                         // Hq / Hkv
@@ -93,6 +102,7 @@ struct TcAttnArgs {
   int out_box;                   // 32 rows of a tile are whole heads of whole tokens
   float* part_o;                 // [splits, T, Hq, D], null when the result is final
   float* part_lse;               // [splits, T, Hq], log2
+  Arrivals arrivals;
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -289,21 +299,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();   // a merge kernel, or the decode kernel beside it, may become resident
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], 1); mbar_init(&kv_empty[s], 2); }
+    const Arrivals& n = t.arrivals;
+    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], s ? 1 : n.keys); mbar_init(&kv_empty[s], n.stage); }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&q_full[x], 1);
+      mbar_init(&q_full[x], n.query);
       mbar_init(&q_empty[x], 1);
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[2 * x], 4);
-      mbar_init(&p_full[2 * x + 1], 4);
-      mbar_init(&o_full[x], 1);
-      mbar_init(&h_done[x], 1);
-      mbar_init(&turn[x], 4);
+      mbar_init(&s_full[x], n.s);
+      mbar_init(&p_full[2 * x], n.p);
+      mbar_init(&p_full[2 * x + 1], n.p);
+      mbar_init(&o_full[x], n.o);
+      mbar_init(&h_done[x], n.half);
+      mbar_init(&turn[x], n.turn);
     }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], 1); mbar_init(&it_empty[i], kSoftWarps + 2); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], n.item); mbar_init(&it_empty[i], kSoftWarps + 2); }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
-    mbar_init(clc, 1);
+    mbar_init(clc, n.next);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -342,8 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++asked;
     };
-    auto taken = [&]() {                          // the block asked for, -1: none is left
-      ok = warp_spin(clc, (asked - 1) & 1);
+    auto answered = [&]() {                       // the block asked for, -1: none is left
       int next = -1;
       asm volatile(
           "{\n .reg .b128 r;\n .reg .pred p;\n .reg .b32 y, z, w;\n ld.shared.b128 r, [%1];\n"
@@ -352,6 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           : "+r"(next)
           : "r"(smem_u32(answer))
           : "memory");
+      return next;
+    };
+    auto taken = [&]() {
+      ok = warp_spin(clc, (asked - 1) & 1);
+      const int next = answered();
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       return ok ? next : -1;
@@ -439,17 +454,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*(volatile int*)abort_flag) ok = false;
       if (ok) idx = taken();
     }
-    if (!ok) {
-      // after a timeout: the loads already issued land before the block exits
-      if (lane == 0) {
+    if (lane == 0) {
+      if (!ok) {
         atomicOr(abort_flag, 1);
-        if (asked) spin_wait(clc, (asked - 1) & 1);
-        for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) spin_wait(&kv_full[i % NS], (i / NS) & 1);
-        for (int x = 0; x < 2; ++x)
-          if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
+        // the block asked for last is run by nobody: its word is written here
+        if (asked && spin_wait(clc, (asked - 1) & 1)) {
+          const int next = answered();
+          if (next >= 0) report(rep, next, kStatusTimeout);
+        }
       }
-      __syncwarp();
+      // The loads issued land before the block exits, also where another warp
+      // gives up after this one's last item (in normal use they are all used).
+      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) spin_wait(&kv_full[i % NS], (i / NS) & 1);
+      for (int x = 0; x < 2; ++x)
+        if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
     }
+    __syncwarp();
     } else if (warp <= kSoftWarps + 2) {
     // ------------------------------------------------------------ MMA issuers
     // The whole warp runs the loop on values that are uniform to the compiler
@@ -551,13 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*(volatile int*)abort_flag) ok = false;
     }
-    if (!ok) {
-      // after a timeout: the MMAs already issued finish before their memory is freed
-      if (lane == 0) atomicOr(abort_flag, 1);
-      commit(&drain[x]);
-      if (lane == 0) spin_wait(&drain[x], 0);
-      __syncwarp();
-    }
+    // the MMAs issued finish before their memory is freed, whoever gives up
+    if (!ok && lane == 0) atomicOr(abort_flag, 1);
+    commit(&drain[x]);
+    if (lane == 0) spin_wait(&drain[x], 0);
+    __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -922,6 +940,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.hidden = t.c > 0 ? -INFINITY : INFINITY;
   t.part_o = part_o;
   t.part_lse = part_lse;
+  t.arrivals = Arrivals(a.hold);
   const bool paged = a.page_table != nullptr;
   CUtensorMap q, k, v, o = {};
   if (!q_map(&q, a, t.tt)) return cudaErrorInvalidValue;

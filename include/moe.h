@@ -470,7 +470,9 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
  * process has some barriers of its kernels wait for an arrival that never
  * comes, until the waits give up as every one does after half a second: the
  * call completes, its results are unspecified, and moe_read_status reports
- * MOE_ERR_DEVICE_TIMEOUT.  (wait 1: keys and values of moe_attn_decode.)
+ * MOE_ERR_DEVICE_TIMEOUT.  (wait 1: keys and values of moe_attn_decode; 2 to 11
+ * the prefill kernel's, which also reads a shared prefix: keys and values, a
+ * stage given back, queries, S, P, O, half a block, a turn, an item, the next.)
  * wait == 0 restores normal operation (the default).  Process-wide, not
  * thread-safe with concurrent calls; it exists so that tests can run what
  * follows a wait that gives up, without a hung or faulted GPU.
