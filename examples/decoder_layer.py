@@ -44,6 +44,8 @@ class DecoderLayer:
 
     def take_pages(self, tokens):
         n = (tokens + self.page - 1) // self.page
+        if n > len(self.free):
+            raise RuntimeError(f"the cache has {len(self.free)} free pages, {n} are needed")
         got, self.free = self.free[:n], self.free[n:]
         return got
 
@@ -64,10 +66,14 @@ class DecoderLayer:
         return moe.rope_append(qkv[:, :Hq * D].view(T, Hq, D), self.k, self.v, self.table, ints(positions), ints(slots),
                                self.k_cache, self.v_cache, q_norm=self.q_norm, k_norm=self.k_norm)
 
+    def experts(self, x):
+        """The MoE layer on normed rows."""
+        return moe.forward(x, self.gate_w, None, self.w_gate_up, self.w_down, self.top_k)
+
     def finish(self, x, attended):
         """Output projection and MoE layer, each added to its input."""
         x = x + attended.flatten(1) @ self.w_o.T
-        return x + moe.forward(self.norm(x), self.gate_w, None, self.w_gate_up, self.w_down, self.top_k)
+        return x + self.experts(self.norm(x))
 
 
 def ints(v):
