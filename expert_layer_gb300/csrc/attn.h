@@ -168,8 +168,8 @@ inline TcPlan tc_plan(const AttnArgs& a) {
 constexpr int kBlocksPerSplit = 4;
 // A shared prefix leaves this share of the SMs to the rows' own keys, which are
 // read meanwhile (64 sequences with 50 to 700 keys of their own after 16,384
-// shared ones: 41 -> 33.4 us when it was done, now 29.3; after 512 26.5 -> 21.5,
-// now 19.3; after 65,536 71 -> 73, now 67.6)
+// shared ones: 41 -> 33.4 us when it was done, now 29.7; after 512 26.5 -> 21.5,
+// now 20.1; after 65,536 71 -> 73, now 68.0)
 constexpr int kOwnShare = 6;
 int tc_splits(const AttnArgs& a, int num_sms);
 int tc_items(const AttnArgs& a, int splits);      // blocks of the grid; -1: too many
@@ -234,7 +234,7 @@ struct Line {
 // ~100 GB/s by itself, and the other kernel takes ~1.6 us per 128 keys of its
 // longest part and 8 us besides.  (With all blocks alike, the second round of
 // them cost more than the first saved: 16,384 shared keys before 1 to 8192 own
-// ones 67 us, this way 45, one kernel after the other 53; now 43.4.)
+// ones 67 us, this way 45, one kernel after the other 53; now 42.8.)
 constexpr int kHeadFixed = 5, kHeadPerBlock = 3;
 struct Beside {
   bool prefix;

@@ -1,7 +1,7 @@
 // The Python functions of the attention entry points (attention.py): argument
 // checks and marshalling on tensors directly.  A decode step calls them once a
 // layer; done through Python attributes and ctypes the checks cost 8 us a call,
-// several times the kernels of a small batch (now about 1 us).
+// several times the kernels of a small batch (here about 1 us).
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

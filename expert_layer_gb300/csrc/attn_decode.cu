@@ -19,10 +19,14 @@
 // mma.sync rather than tcgen05: a unit has 8 or 16 rows of the 128 that the
 // latter multiplies, and the kernel waits for HBM in any case (issue slots 20%
 // used, mma pipe 14%).
+// P is rounded to the element type for the second product, l sums it before
+// that: error against 64 bits 1.7e-3 where weights in 32 bits leave 1.5e-3 (64
+// sequences of 1 to 8192 keys, bf16; attn_tc.cu says more).
 // Measured (32 query and 4 key-value heads of 128, bf16): 128 sequences of 4096
-// keys 168 us = 6.4 TB/s, 95% of a copy's rate; one of 131,001 keys 50.4 us, of
-// which it streams 38 at 6.9 TB/s; 64 of 1 to 8192 keys 26.7; 1024 of 90 keys
-// 47.7; 8 of 400 keys 9.1 (start 2.5, keys 1, join and merge 4).
+// keys 167 us = 6.4 TB/s, 95% of a copy's rate; one of 131,001 keys 49.9 us, of
+// which it streams 38 at 6.9 TB/s; 64 of 1 to 8192 keys 26.8; 1024 of 90 keys
+// 46.9; 8 of 400 keys 9.5, the keys themselves 1 (the rest is start, join and
+// merge).
 #include "attn.h"
 #include "attn_ptx.cuh"
 

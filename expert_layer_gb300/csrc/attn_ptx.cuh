@@ -27,7 +27,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 // Two fp32 values in one 64-bit register and the paired operations on them
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;
@@ -94,8 +93,8 @@ __device__ __forceinline__ uint64_t now_ns() {
 // A bounded wait that does not sleep between polls: for warps that the tensor
 // cores or the softmax depend on.  One poll, then a rolled loop that reads the
 // clock between polls: sixteen polls in a row were a quarter of the kernels'
-// code (8192 causal 317 us, 37 ragged prompts 27.9, 16 sequences D = 64 37.1;
-// now 306, 26.1, 34.9).
+// code (8192 causal 317 -> 306 us, 37 ragged prompts 27.9 -> 26.1, 16 sequences
+// of D = 64 37.1 -> 34.9 when it was done).
 __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = now_ns();
@@ -169,7 +168,7 @@ inline bool rows_map(CUtensorMap* m, const Heads& v, const AttnArgs& a, long lon
 // rows whole, as groups of 8 rows, each group D / 64 swizzled atoms of 1 KB.
 // (With a box per 64 columns a 16-row page takes two boxes of 2 KB, and the
 // copy engine spends ~95 cycles on a box: causal 8192 from 16-row pages then took
-// 22% longer than from pages of 128; now 336 us against 326.)
+// 22% longer than from pages of 128; now 322 us against 316.)
 inline bool pages_map(CUtensorMap* m, const uint16_t* cache, const AttnArgs& a, int rows) {
   const cuuint64_t page = (cuuint64_t)a.D << a.page_shift;
   const cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, 1ull << (a.page_shift - 3), (cuuint64_t)a.pages * a.Hkv};

@@ -14,7 +14,17 @@
 // formed with it from then on, without looking at the logits first.  The sum of
 // P, needed anyway, says when a row has outgrown its scale (2^15: P stays within
 // f16, and bf16 rounds relative to P whatever its size); only then the row's
-// maximum is taken again and l and O are rescaled, which hardly happens.
+// maximum is taken again and l and O are rescaled, which hardly happens.  A row
+// whose logits are all -inf so far has no scale (m = -inf) and takes the path
+// that looks at every logit.
+//
+// Rounding P to the element type is the price of the second product on the
+// tensor cores: the outputs' error against 64 bits (relative, over all outputs)
+// is 2.3e-3 where weights in 32 bits leave 1.7e-3, the rounding of the output
+// (bf16; f16 2.9e-4 and 2.1e-4).  l sums P before that, for the log-sums and the
+// joins of parts; dividing by a second sum, of the rounded P, so that the
+// rounding of a dominant key cancels, gave 2.1e-3 (2.5e-4) and took 3 to 11%
+// more time (8192 causal 313 -> 344 us, 16 prompts of 512 tokens 50.8 -> 56.4).
 //
 // Bound: D = 128, the tensor pipe (512 cycles for each of a tile's two products
 // per key block, 2048 for both tiles, of a period of ~2550); D = 64, the chain
@@ -22,12 +32,13 @@
 // long).  Two tiles make one of them run while the other waits for its barriers,
 // and fill tensor memory.  Exponentials (32 a cycle and SM: 1024 per period) are
 // not the bound: a quarter of them as a polynomial on the FMA pipe took 375 us
-// for 8192 tokens instead of 324.
+// for 8192 tokens where the kernel of that time took 324.
 // Measured (32 query and 4 key-value heads of 128, bf16): 8192 tokens causal
-// 310 us = 1.77 PFLOP/s, 92% of the library's matrix product (340 after seconds,
-// at 1725 MHz under the power cap, 94% of its rate then); 8192 x 8192 594 us =
-// 1.85; 16 prompts of 512 tokens 50.4 us, 64 of 128 35 (an item of one block is a
-// chain of ~4.2 us: product 0.2, softmax 1.3, product 0.7, epilogue 1.6).
+// 313 us in bursts of a few calls = 1.75 PFLOP/s, 91% of the library's matrix
+// product (345 after seconds, under the power cap, 93% of its rate then); 8192 x
+// 8192 598 us = 1.84; 16 prompts of 512 tokens 51 us, 64 of 128 35.5 (an item of
+// one block is a chain of ~4.2 us: product 0.2, softmax 1.3, product 0.7,
+// epilogue 1.6).
 #include <cuda.h>
 
 #include "attn.h"
@@ -601,9 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int turn_half = D == 64 || shared <= 16 ? 0 : 1;
       const uint32_t kv0 = kv;
       kv += 2 * max(it.n[0], it.n[1]);
-      // keys that this row sees, and that the tile's first token sees
+      // keys that this row sees
       const int vis = a.causal ? min(it.seen + x * t.tt + token, it.len) : it.len;
-      const int vis0 = a.causal ? min(it.seen + x * t.tt, it.len) : it.len;
       const bool live = token < (x ? it.tok[1] : it.tok[0]);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++ns) {

@@ -356,8 +356,9 @@ int moe_debug_force_wait_timeout(int polls);
  * G = Hq / Hkv (query head h reads key-value head h / G), D head size.
  * Element types: bf16 or f16 (`dtype`), the same for q, k, v, the cache and
  * the outputs; every sum, softmax statistic and norm is fp32.
- * Supported: D 64 or 128, Hq a multiple of Hkv with G <= 128, page sizes 16,
- * 32, 64, 128 and 256, T * Hq < 2^31.
+ * Supported: D 64 or 128, Hq <= 65536 a multiple of Hkv with G <= 128, T * Hq <
+ * 2^31, strides below 2^38 elements; page sizes 16, 32, 64, 128 and 256 with
+ * pages * page_size < 2^31; prefixes of at most 2^30 tokens.
  *
  * Conventions as above, except that int32 index arrays (positions, slots,
  * starts, lengths, page tables) need only 4-byte alignment and heads may be
@@ -443,6 +444,12 @@ int moe_attn_prefill(const moe_heads *q, const moe_heads *k, const moe_heads *v,
  * long prompt, whose new tokens are in the cache already and read the ones
  * before them): sequence s has kv_lens[s] keys on the pages
  * page_table[s, 0 ..]; page_table is [n_seq, table_pages] int32.
+ *
+ * How the keys of a call with few rows are split over the GPU follows the
+ * sizes that the host knows, not the lengths: here table_pages * page_size, Tk
+ * of moe_attn_prefill.  A table much wider than its sequences gives right
+ * results with empty parts to join (64 rows of 200 keys: 10.7 us, with room for
+ * 131,072 keys 14.9), and another split can change their last bits.
  */
 int moe_attn_prefill_paged(const moe_heads *q, const moe_kv_cache *cache, const int32_t *page_table,
                            int table_pages, const int32_t *q_starts, const int32_t *kv_lens,
