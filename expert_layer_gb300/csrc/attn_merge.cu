@@ -23,7 +23,7 @@ struct MergeArgs {
   AttnArgs a;
   int splits;            // parts in row order: [splits, T * Hq]; 0: decode without a prefix
   DecodeParts p;
-  int chunks, grid;      // decode: units per key-value head, blocks of the kernel (0: prefill)
+  int chunks;            // decode: units per key-value head
   int G, rows;           // heads of a key-value head; of a unit, at most 16
   Divisor by_rows, by_chunks, by_Hq, by_G;
   unsigned todo;         // rows to write
@@ -33,7 +33,7 @@ struct MergeArgs {
 // cross the decode kernel's blocks, at most one for each block.  (With 16 rows a
 // unit whatever G, the blocks took two rounds: 64 sequences of 1466 keys, G = 8,
 // 40.2 us against 39.0.)
-template <int D, bool kF16>
+template <int D, bool kF16, bool kPrefill>
 __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs t) {
   constexpr int N = D / 32;            // elements per lane
   __shared__ float s_o[kWarps][D];
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
   // as they are.  Whether there are any is seen while that kernel runs; a call
   // with parts has few sequences (tc_splits).
   bool tidy = true;
-  if (t.grid == 0) {
+  if (kPrefill) {
     for (int s = lane; s < a.n_seq; s += 32) tidy &= a.q_starts[s] <= a.q_starts[s + 1];
     tidy = __all_sync(0xffffffffu, tidy) && a.q_starts[0] == 0 && a.q_starts[a.n_seq] == a.T;
   }
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
     int c0 = 0, own = 0, r = 0, parts = 0;
     long long row = i;
     bool ours = tidy;
-    if (!tidy) {
+    if (kPrefill && !tidy) {
       const int token = t.by_Hq.of((int)i);
       for (int s = lane; s < a.n_seq; s += 32) {
         const int q0 = a.q_starts[s], q1 = a.q_starts[s + 1];
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
       }
       ours = __any_sync(0xffffffffu, ours);
     }
-    if (!t.splits) {
+    if (!kPrefill && !t.splits) {
       c0 = t.by_rows.of((int)i);
       r = (int)i - c0 * t.rows;
       const int4 u = t.p.tail[c0];
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
       row = (long long)u.x * a.Hq + hk * G + h;
     } else {
       parts = t.splits;
-      if (t.grid > 0) {
+      if (!kPrefill) {
         const int b = t.by_Hq.of((int)i), h = (int)i - b * a.Hq, hk = t.by_G.of(h), g = h - hk * G;
         const int2 u = t.p.held[(b * a.Hkv + hk) * t.chunks + g / 16];
         own = u.x;
@@ -153,6 +153,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_merge_kernel(const MergeArgs
   }
 }
 
+template <int D, bool kF16>
+auto kernel_of(bool prefill) {
+  return prefill ? attn_merge_kernel<D, kF16, true> : attn_merge_kernel<D, kF16, false>;
+}
+
 }  // namespace
 
 cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& p, int decode_grid,
@@ -162,7 +167,6 @@ cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& 
   t.splits = splits;
   t.p = p;
   t.chunks = decode_chunks(a);
-  t.grid = decode_grid;
   t.G = a.Hq / a.Hkv;
   t.rows = t.G < 16 ? t.G : 16;
   t.by_rows.set(t.rows);
@@ -170,8 +174,9 @@ cudaError_t launch_attn_merge(const AttnArgs& a, int splits, const DecodeParts& 
   t.by_Hq.set(a.Hq);
   t.by_G.set(t.G);
   t.todo = splits ? (unsigned)a.T * a.Hq : t.rows * decode_grid;
-  auto kern = a.D == 64 ? (a.f16 ? attn_merge_kernel<64, true> : attn_merge_kernel<64, false>)
-                        : (a.f16 ? attn_merge_kernel<128, true> : attn_merge_kernel<128, false>);
+  const bool rows = decode_grid == 0;
+  auto kern = a.D == 64 ? (a.f16 ? kernel_of<64, true>(rows) : kernel_of<64, false>(rows))
+                        : (a.f16 ? kernel_of<128, true>(rows) : kernel_of<128, false>(rows));
   return launch_pdl(kern, dim3(t.todo < 2560 ? t.todo : 2560), dim3(kWarps * 32), 0, stream, t);
 }
 
