@@ -18,8 +18,9 @@ import torch
 __all__ = ["MoEError", "lib", "workspace_size", "alloc_workspace", "route", "permute", "forward",
            "read_status", "read_diagnostics", "LIB_PATH", "nvfp4_tc_scales", "nvfp4_quantize",
            "W4A4Weights", "w4a4_weights", "forward_w4a4", "forward_int8", "int8_struct",
-           "attn_workspace_size", "alloc_attn_workspace", "rope_table", "rope_append", "attn_prefill",
-           "attn_prefill_paged", "attn_decode"]
+           "attn_workspace_size", "alloc_attn_workspace", "rope_table", "rope_axes", "rope_append", "attn_prefill",
+           "attn_prefill_paged", "attn_decode", "alloc_fp8_cache", "rope_append_fp8", "attn_prefill_paged_fp8",
+           "attn_decode_fp8", "attn_key_weights", "kv_evict"]
 
 # MOE_GB300_LIB selects another build of the library (e.g. the index-checking
 # MOE_DEBUG_BOUNDS build); the default is the in-tree libmoe_gb300.so.
@@ -350,7 +351,8 @@ def read_diagnostics(workspace, stream=None) -> dict:
 
 
 from . import attention as _attention  # noqa: E402  (uses the helpers above)
-from .attention import (alloc_attn_workspace, attn_decode, attn_prefill, attn_prefill_paged,  # noqa: E402,F401
-                        attn_workspace_size, rope_append, rope_table)
+from .attention import (alloc_attn_workspace, alloc_fp8_cache, attn_decode, attn_decode_fp8,  # noqa: E402,F401
+                        attn_key_weights, attn_prefill, attn_prefill_paged, attn_prefill_paged_fp8,
+                        attn_workspace_size, kv_evict, rope_append, rope_append_fp8, rope_axes, rope_table)
 
 _SIGNATURES.update(_attention.SIGNATURES)

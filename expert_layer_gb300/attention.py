@@ -29,8 +29,9 @@ import torch
 
 from . import MoEError, lib
 
-__all__ = ["attn_workspace_size", "alloc_attn_workspace", "rope_table", "rope_append", "attn_prefill",
-           "attn_prefill_paged", "attn_decode"]
+__all__ = ["attn_workspace_size", "alloc_attn_workspace", "rope_table", "rope_axes", "rope_append", "attn_prefill",
+           "attn_prefill_paged", "attn_decode", "alloc_fp8_cache", "rope_append_fp8", "attn_prefill_paged_fp8",
+           "attn_decode_fp8", "attn_key_weights", "kv_evict"]
 
 _P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -42,6 +43,15 @@ SIGNATURES = {
     "moe_attn_prefill": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
     "moe_attn_prefill_paged": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
     "moe_attn_decode": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "moe_rope_append_axes": (_I, [_P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P,
+                                  _P, _SZ, _P]),
+    "moe_rope_append_fp8": (_I, [_P, _P, _P, _P, _P, _F, _P, _I, _I, _I, _P, _P, _I, _P, _I, _P, _P, _I, _I, _I, _I,
+                                 _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_attn_prefill_paged_fp8": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "moe_attn_decode_fp8": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "moe_attn_key_weights": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _I, _P, _SZ,
+                                  _P]),
+    "moe_kv_evict": (_I, [_P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
 }
 
 _native = None
@@ -63,8 +73,9 @@ def _load():
             raise MoEError("the attention binding is missing or does not load: build it with "
                            f"`python -m expert_layer_gb300._build` ({e})") from e
         native.bind(MoEError, *(ctypes.cast(getattr(handle, n), _P).value for n in (
-            "moe_attn_workspace_size", "moe_rope_append", "moe_attn_prefill", "moe_attn_prefill_paged",
-            "moe_attn_decode", "moe_error_string")), *(
+            "moe_attn_workspace_size", "moe_rope_append_axes", "moe_attn_prefill", "moe_attn_prefill_paged",
+            "moe_attn_decode", "moe_rope_append_fp8", "moe_attn_prefill_paged_fp8", "moe_attn_decode_fp8",
+            "moe_attn_key_weights", "moe_kv_evict", "moe_error_string")), *(
                 (tuple(inspect.signature(f).parameters), f.__defaults__ or (),
                  f"{f.__name__}{inspect.signature(f)}\n--\n\n{inspect.getdoc(f)}") for f in _FUNCTIONS))
         for name in (f.__name__ for f in _FUNCTIONS):
@@ -123,17 +134,66 @@ def rope_table(max_pos: int, rot: int, base: float = 10000.0, scaling: str | Non
     return torch.cat([angle.cos() * mul, angle.sin() * mul], dim=1).float().contiguous()
 
 
+def rope_axes(rot: int, sections, interleaved: bool = False, device="cuda") -> torch.Tensor:
+    """The axis of each of a head's rot / 2 rotated pairs (uint8), for the
+    ``axes`` of ``rope_append``: ``sections[x]`` pairs for axis x, one axis
+    after the other, or with ``interleaved`` in turns (0, 1, 2, 0, 1, ...)
+    while they have pairs left."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or rot < 0 or 2 * sum(left) != rot:
+        raise MoEError("rope_axes: one to four sections that add up to rot / 2 pairs")
+    if interleaved:
+        order = []
+        while sum(left):
+            order += [x for x in range(len(left)) if left[x] > 0]
+            left = [max(0, n - 1) for n in left]
+    else:
+        order = [x for x, n in enumerate(left) for _ in range(n)]
+    return torch.tensor(order, dtype=torch.uint8, device=device)
+
+
+def alloc_fp8_cache(pages: int, Hkv: int, page_size: int, D: int, device="cuda"):
+    """An empty cache in 8 bits: (k_cache, v_cache) float8_e4m3fn [pages, Hkv,
+    page_size, D] and their scales, fp32 [pages, Hkv, page_size / 16, 2] (of
+    the keys, of the values), for ``rope_append_fp8`` and the attention over
+    it.  A value is its code times its scale."""
+    if min(pages, Hkv, D) <= 0 or page_size not in (16, 32, 64, 128, 256):
+        raise MoEError("unsupported shape")
+    k, v = (torch.zeros(pages, Hkv, page_size, D, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    return k, v, torch.ones(pages, Hkv, page_size // 16, 2, dtype=torch.float32, device=device)
+
+
 def rope_append(q, k, v, table, positions, slots, k_cache, v_cache, q_norm=None, k_norm=None, eps=1e-6,
-                interleaved=False, q_out=None, workspace=None, stream=None):
+                interleaved=False, q_out=None, workspace=None, stream=None, axes=None):
     """Norm (per head, optional) and rotate q [T, Hq, D] and k [T, Hkv, D],
     and write k and v [T, Hkv, D] to the paged cache; returns q_out.
 
     q, k, v may be strided views of one projection's rows.  ``table``
     [max_pos, rot] fp32 from ``rope_table``; ``positions`` and ``slots`` int32
     [T]; a slot is page * page_size + row, negative to leave the cache alone.
-    ``q_norm`` / ``k_norm``: fp32 [D] weights or None."""
+    ``q_norm`` / ``k_norm``: fp32 [D] weights or None.
+
+    ``axes`` (uint8 [rot / 2], from ``rope_axes``): ``positions`` is then
+    [n_axes, T], up to four positions of a token (time, height and width of an
+    image's or video's), and pair i turns by positions[axes[i]]."""
     return _load().rope_append(q, k, v, table, positions, slots, k_cache, v_cache, q_norm, k_norm, eps, interleaved,
-                               q_out, workspace, stream)
+                               q_out, workspace, stream, axes)
+
+
+def rope_append_fp8(q, k, v, table, positions, page_table, q_starts, kv_lens, k_cache, v_cache, scales, q_norm=None,
+                    k_norm=None, eps=1e-6, interleaved=False, axes=None, q_out=None, workspace=None, stream=None):
+    """``rope_append`` to a cache in 8 bits (``alloc_fp8_cache``); returns q_out.
+
+    Sequence s has the rows q_starts[s] .. q_starts[s+1] (int32 [n_seq + 1])
+    and kv_lens[s] tokens with them (int32 [n_seq]): its rows go behind what
+    its pages page_table[s] (int32 [n_seq, table_pages]) hold, as the attention
+    calls then read them.  Every 16 tokens of a page share a scale per head, a
+    power of two between 2^-24 and 2^7: the smallest with which their largest
+    value is at most 448.  Where a later token needs a larger one, the codes
+    that were there are rounded again."""
+    return _load().rope_append_fp8(q, k, v, table, positions, page_table, q_starts, kv_lens, k_cache, v_cache, scales,
+                                   q_norm, k_norm, eps, interleaved, axes, q_out, workspace, stream)
 
 
 def attn_prefill(q, k, v, q_starts, kv_starts, causal=True, scale=None, out=None, lse=None, workspace=None,
@@ -169,4 +229,54 @@ def attn_decode(q, k_cache, v_cache, page_table, kv_lens, prefix_table=None, pre
                                workspace, stream)
 
 
-_FUNCTIONS = (rope_append, attn_prefill, attn_prefill_paged, attn_decode)
+def attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal=True, scale=None,
+                           out=None, lse=None, workspace=None, stream=None):
+    """``attn_prefill_paged`` over a cache in 8 bits (``alloc_fp8_cache``):
+    codes are multiplied exactly, sums and softmax statistics are fp32."""
+    return _load().attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal, scale,
+                                          out, lse, workspace, stream)
+
+
+def attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table=None, prefix_len=0, scale=None,
+                    out=None, lse=None, workspace=None, stream=None):
+    """``attn_decode`` over a cache in 8 bits (``alloc_fp8_cache``), its shared
+    prefix there too: codes are multiplied exactly, sums and softmax
+    statistics are fp32."""
+    return _load().attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table, prefix_len, scale,
+                                   out, lse, workspace, stream)
+
+
+def attn_key_weights(q, k_cache, page_table, q_starts, kv_lens, lse, weights, causal=True, scale=None, workspace=None,
+                     stream=None):
+    """Add the attention that the rows q [T, Hq, D] give to each key of their
+    sequences to ``weights`` (fp32 [n_seq, Hkv, capacity], at least as many
+    entries as a sequence has keys), summed over a sequence's rows and the
+    query heads of a key-value head; returns ``weights``.
+
+    ``lse`` (fp32 [T, Hq]) is what the attention call over the same rows left:
+    weight j of a row is exp(scale q . k_j - lse).  ``q_starts``, ``kv_lens``,
+    ``page_table`` and ``causal`` as in ``attn_prefill_paged``; for a decode
+    batch q_starts is 0, 1, .. B.  Rows without keys (lse -inf) add nothing."""
+    return _load().attn_key_weights(q, k_cache, page_table, q_starts, kv_lens, lse, weights, causal, scale, workspace,
+                                    stream)
+
+
+def kv_evict(k_cache, v_cache, page_table, kv_lens, weights, out_table, budget, keep_first=0, keep_last=0,
+             new_lens=None, new_weights=None, kept=None, workspace=None, stream=None):
+    """Cut every sequence's keys to at most ``budget`` per head: the first
+    ``keep_first``, the last ``keep_last`` and those of largest ``weights``
+    between (ties: the first; NaN counts as the smallest), copied in their order to the
+    pages out_table[s] (int32 [n_seq, out_pages], none of them read by the
+    call).  The pages page_table[s] stay as they were.
+
+    Returns (new_lens int32 [n_seq], new_weights fp32 [n_seq, Hkv, budget],
+    kept int32 [n_seq, Hkv, budget]): min(kv_lens, budget), the weights of the
+    kept keys (0 behind them) and their places before (-1 behind them).  Keys
+    keep the positions they were rotated by; a sequence's next token goes on
+    counting from its own position, and its slot from new_lens."""
+    return _load().kv_evict(k_cache, v_cache, page_table, kv_lens, weights, out_table, budget, keep_first, keep_last,
+                            new_lens, new_weights, kept, workspace, stream)
+
+
+_FUNCTIONS = (rope_append, attn_prefill, attn_prefill_paged, attn_decode, rope_append_fp8, attn_prefill_paged_fp8,
+              attn_decode_fp8, attn_key_weights, kv_evict)

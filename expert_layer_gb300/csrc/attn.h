@@ -105,6 +105,8 @@ struct Divisor {
 #endif
 };
 
+constexpr int kMaxAxes = 4;
+
 struct RopeArgs {
   Heads q, k, v;
   const float* q_norm;        // [D] or null
@@ -112,7 +114,9 @@ struct RopeArgs {
   float eps;
   const float* table;         // [max_pos, rot]: cos | sin
   int max_pos, rot, interleaved;
-  const int32_t* positions;
+  const uint8_t* axes;        // [rot / 2]: the row of `positions` that turns each pair; null: one row
+  int n_axes;                 // at most kMaxAxes
+  const int32_t* positions;   // [n_axes, T]
   const int32_t* slots;
   int T, Hq, Hkv, D, f16;
   uint16_t* q_out;            // [T, Hq, D]
@@ -122,6 +126,39 @@ struct RopeArgs {
   unsigned chunks;            // groups of heads of a token (the kernel's)
   Divisor by_chunks;
 };
+
+// ------------------------------------------------------------- the cache in 8 bits
+// e4m3 codes and one scale 2^e per kScaleBlock tokens of a page and key-value
+// head, of the keys and of the values: scales [pages, Hkv, page_size / 16, 2].
+// A power of two costs a floating code nothing, and leaves every product with
+// it, and every change of it, exact (but for codes that become subnormal).
+// 57344 = 448 * 2^7 is the largest value, below f16's; 2^-24 * 2^-9 the
+// smallest step.
+constexpr int kScaleBlock = 16;
+constexpr int kScaleMin = -24, kScaleMax = 7;
+
+struct RopeFp8Args {
+  RopeArgs r;                 // without slots and cache
+  uint8_t* k_codes;           // [pages, Hkv, page_size, D]
+  uint8_t* v_codes;
+  float* scales;
+  const int32_t* page_table;  // [n_seq, table_pages]
+  const int32_t* q_starts;    // [n_seq + 1]
+  const int32_t* kv_lens;     // [n_seq], with the call's tokens
+  int table_pages, n_seq;
+  int q_blocks;               // the kernel's: blocks of the grid that take q rows
+  int by_token;               // slots of sequences by their tokens (else by 16 of them)
+  Divisor by_Hkv2;
+};
+
+#ifdef __CUDACC__
+// Exponent of a scale; whatever else a damaged cache holds becomes one of the range
+__device__ __forceinline__ int scale_exp(float s) {
+  const int e = (int)((__float_as_uint(s) >> 23) & 255) - 127;
+  return e < kScaleMin ? kScaleMin : e > kScaleMax ? kScaleMax : e;
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+#endif
 
 // Barriers that are made to wait for an arrival that never comes, in tests only
 // (moe_debug_attn_wait_timeout): their arrival count, a kernel argument, is one
@@ -137,8 +174,9 @@ enum Hold {
 // (q_starts null) with an optional shared prefix.
 struct AttnArgs {
   Heads q, k, v;
-  const uint16_t* k_cache;
+  const uint16_t* k_cache;    // (the cache in 8 bits: codes, with `scales`)
   const uint16_t* v_cache;
+  const float* scales;        // null: k_cache and v_cache hold elements of the call's type
   const int32_t* page_table;  // [n_seq, table_pages], null when packed
   const int32_t* prefix_table;
   const int32_t* q_starts;
@@ -154,6 +192,42 @@ struct AttnArgs {
 };
 
 cudaError_t launch_rope_append(const RopeArgs& a, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_append_fp8(const RopeFp8Args& a, void* ws, int num_sms, cudaStream_t stream);
+
+// attn_weights.cu -- attention weight of every key
+struct WeightArgs {
+  Heads q;
+  const uint16_t* k_cache;    // [pages, Hkv, page_size, D]
+  const int32_t* page_table;  // [n_seq, table_pages]
+  const int32_t* q_starts;
+  const int32_t* kv_lens;
+  int table_pages, pages, page_shift;
+  int n_seq, T, Hq, Hkv, D, f16, causal;
+  float c;                    // scale log2 e
+  const float* lse;           // [T, Hq]
+  float* weights;             // [n_seq, Hkv, capacity]
+  int capacity;
+  Divisor by_G;
+};
+cudaError_t launch_attn_weights(const WeightArgs& a, void* ws, int num_sms, cudaStream_t stream);
+
+// kv_evict.cu
+struct EvictArgs {
+  uint16_t* k_cache;          // [pages, Hkv, page_size, D]
+  uint16_t* v_cache;
+  const int32_t* page_table;  // [n_seq, table_pages]
+  const int32_t* out_table;   // [n_seq, out_pages]
+  const int32_t* kv_lens;
+  const float* weights;       // [n_seq, Hkv, capacity]
+  int table_pages, out_pages, pages, page_shift, capacity;
+  int n_seq, Hkv, D;
+  int budget, first, last;
+  int32_t* new_lens;          // [n_seq]
+  float* new_weights;         // [n_seq, Hkv, budget]
+  int32_t* kept;              // [n_seq, Hkv, budget]
+  Divisor by_Hkv, by_budget;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, void* ws, int num_sms, cudaStream_t stream);
 
 // attn_tc.cu -- tiles of 128 rows (tt tokens x G heads), two per block; slots:
 // tile slots of the batch (see find_seq)

@@ -13,6 +13,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 #include <optional>
 #include <string>
@@ -24,12 +25,18 @@ namespace {
 
 struct Library {
   decltype(&moe_attn_workspace_size) workspace_size;
-  decltype(&moe_rope_append) rope_append;
+  decltype(&moe_rope_append_axes) rope_append;
   decltype(&moe_attn_prefill) prefill;
   decltype(&moe_attn_prefill_paged) prefill_paged;
   decltype(&moe_attn_decode) decode;
+  decltype(&moe_rope_append_fp8) rope_append_fp8;
+  decltype(&moe_attn_prefill_paged_fp8) prefill_paged_fp8;
+  decltype(&moe_attn_decode_fp8) decode_fp8;
+  decltype(&moe_attn_key_weights) key_weights;
+  decltype(&moe_kv_evict) evict;
   decltype(&moe_error_string) error_string;
 } lib = {};
+constexpr int kAddresses = sizeof(Library) / sizeof(void*);
 PyObject* error_type = nullptr;       // MoEError
 
 struct Refusal {
@@ -50,6 +57,7 @@ const char* type_text(at::ScalarType t) {
     case at::kFloat: return "torch.float32";
     case at::kInt: return "torch.int32";
     case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return at::toString(t);
   }
 }
@@ -128,6 +136,19 @@ Cache cache(PyObject* k, PyObject* v, const Query& q) {
   const at::Tensor& vt = dense(v, "v_cache", q.type, kt.sizes(), q.device);
   return Cache{moe_kv_cache{kt.data_ptr(), vt.data_ptr(), whole(kt.size(0), "k_cache"), whole(kt.size(2), "k_cache")},
                whole(kt.size(1), "k_cache")};
+}
+
+struct CacheFp8 {
+  moe_kv_cache_fp8 c;
+  int Hkv;
+};
+CacheFp8 cache_fp8(PyObject* k, PyObject* v, PyObject* scales, const Query& q) {
+  const at::Tensor& kt = dense(k, "k_cache", at::kFloat8_e4m3fn, {-1, -1, -1, q.D}, q.device);
+  const at::Tensor& vt = dense(v, "v_cache", at::kFloat8_e4m3fn, kt.sizes(), q.device);
+  const at::Tensor& st = dense(scales, "scales", at::kFloat, {kt.size(0), kt.size(1), kt.size(2) / 16, 2}, q.device);
+  return CacheFp8{moe_kv_cache_fp8{kt.data_ptr(), vt.data_ptr(), ptr<float>(st), whole(kt.size(0), "k_cache"),
+                                   whole(kt.size(2), "k_cache")},
+                  whole(kt.size(1), "k_cache")};
 }
 
 // Where a call runs.  What it allocates comes from that stream's memory: a
@@ -209,7 +230,7 @@ void check(int rc, const char* what) {
 // A function's parameters, defaults and documentation are those of its Python
 // definition (attention.py), handed over by bind(); the functions below take
 // them in that order.
-constexpr int kMost = 17;
+constexpr int kMost = 19;
 struct Spec {
   const char* function;
   int total;
@@ -284,7 +305,21 @@ PyObject* guarded(F f) {
 }
 
 // ------------------------------------------------------------- functions
-Spec rope_spec = {"rope_append", 15};
+// Positions [T], or with axes (uint8 [rot / 2]) [n_axes, T]
+struct Turn {
+  const int32_t* positions;
+  const uint8_t* axes;
+  int n_axes;
+};
+Turn turn(PyObject* positions, PyObject* axes, const at::Tensor& table, const Query& q) {
+  if (!given(axes)) return Turn{ptr<int32_t>(dense(positions, "positions", at::kInt, {q.T}, q.device)), nullptr, 0};
+  const at::Tensor& a = dense(axes, "axes", at::kByte, {table.size(1) / 2}, q.device);
+  const at::Tensor& p = dense(positions, "positions", at::kInt, {-1, q.T}, q.device);
+  // (no pair is turned: no axes, and a pointer that may be null)
+  return Turn{ptr<int32_t>(p), a.numel() ? ptr<uint8_t>(a) : nullptr, whole(p.size(0), "positions")};
+}
+
+Spec rope_spec = {"rope_append", 16};
 PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     const Args a = parse(rope_spec, args, n, kw);
@@ -293,7 +328,7 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const moe_heads k = heads(checked(a.v[1], "k", q.type, {q.T, c.Hkv, q.D}, q.device), "k");
     const moe_heads v = heads(checked(a.v[2], "v", q.type, {q.T, c.Hkv, q.D}, q.device), "v");
     const at::Tensor& table = dense(a.v[3], "table", at::kFloat, {-1, -1}, q.device);
-    const int32_t* pos = ptr<int32_t>(dense(a.v[4], "positions", at::kInt, {q.T}, q.device));
+    const Turn by = turn(a.v[4], a.v[15], table, q);
     const int32_t* slots = ptr<int32_t>(dense(a.v[5], "slots", at::kInt, {q.T}, q.device));
     const float* qn = given(a.v[8]) ? ptr<float>(dense(a.v[8], "q_norm", at::kFloat, {q.D}, q.device)) : nullptr;
     const float* kn = given(a.v[9]) ? ptr<float>(dense(a.v[9], "k_norm", at::kFloat, {q.D}, q.device)) : nullptr;
@@ -304,9 +339,56 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     Owned owned{out.object};
     const Space ws = workspace(a.v[13], q.T, 0, q.Hq, c.Hkv, q.D, run);
     check(lib.rope_append(&q.view, &k, &v, qn, kn, eps, ptr<float>(table), whole(table.size(0), "table"),
-                          whole(table.size(1), "table"), interleaved, pos, slots, q.T, q.Hq, c.Hkv, q.D, q.code,
-                          out.data, &c.c, ws.data, ws.bytes, run.stream),
+                          whole(table.size(1), "table"), interleaved, by.positions, by.axes, by.n_axes, slots, q.T,
+                          q.Hq, c.Hkv, q.D, q.code, out.data, &c.c, ws.data, ws.bytes, run.stream),
           "moe_rope_append");
+    return owned.release();
+  });
+}
+
+// The page table, starts and lengths of a ragged call
+struct Ragged {
+  const int32_t* table;
+  const int32_t* q_starts;
+  const int32_t* lens;
+  int pages, seqs;
+};
+Ragged ragged(PyObject* page_table, PyObject* q_starts, PyObject* kv_lens, int device) {
+  Ragged r;
+  const at::Tensor& lens = dense(kv_lens, "kv_lens", at::kInt, {-1}, device);
+  r.seqs = whole(lens.size(0), "kv_lens");
+  r.lens = ptr<int32_t>(lens);
+  r.q_starts = ptr<int32_t>(dense(q_starts, "q_starts", at::kInt, {r.seqs + 1}, device));
+  const at::Tensor& table = dense(page_table, "page_table", at::kInt, {r.seqs, -1}, device);
+  r.table = ptr<int32_t>(table);
+  r.pages = whole(table.size(1), "page_table");
+  return r;
+}
+
+Spec rope_fp8_spec = {"rope_append_fp8", 19};
+PyObject* rope_append_fp8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    const Args a = parse(rope_fp8_spec, args, n, kw);
+    const Query q = query(a.v[0]);
+    const CacheFp8 c = cache_fp8(a.v[8], a.v[9], a.v[10], q);
+    const moe_heads k = heads(checked(a.v[1], "k", q.type, {q.T, c.Hkv, q.D}, q.device), "k");
+    const moe_heads v = heads(checked(a.v[2], "v", q.type, {q.T, c.Hkv, q.D}, q.device), "v");
+    const at::Tensor& table = dense(a.v[3], "table", at::kFloat, {-1, -1}, q.device);
+    const Turn by = turn(a.v[4], a.v[15], table, q);
+    const Ragged r = ragged(a.v[5], a.v[6], a.v[7], q.device);
+    const float* qn = given(a.v[11]) ? ptr<float>(dense(a.v[11], "q_norm", at::kFloat, {q.D}, q.device)) : nullptr;
+    const float* kn = given(a.v[12]) ? ptr<float>(dense(a.v[12], "k_norm", at::kFloat, {q.D}, q.device)) : nullptr;
+    const float eps = (float)number(a.v[13], 1e-6);
+    const bool interleaved = truth(a.v[14]);
+    Run run(a.v[18], q.device);
+    const Output out = output(a.v[16], "q_out", q, run);
+    Owned owned{out.object};
+    const Space ws = workspace(a.v[17], q.T, r.seqs, q.Hq, c.Hkv, q.D, run);
+    check(lib.rope_append_fp8(&q.view, &k, &v, qn, kn, eps, ptr<float>(table), whole(table.size(0), "table"),
+                              whole(table.size(1), "table"), interleaved, by.positions, by.axes, by.n_axes, r.table,
+                              r.pages, r.q_starts, r.lens, r.seqs, q.T, q.Hq, c.Hkv, q.D, q.code, out.data, &c.c,
+                              ws.data, ws.bytes, run.stream),
+          "moe_rope_append_fp8");
     return owned.release();
   });
 }
@@ -345,22 +427,28 @@ PyObject* attn_prefill_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyO
     const Args a = parse(paged_spec, args, n, kw);
     const Query q = query(a.v[0]);
     const Cache c = cache(a.v[1], a.v[2], q);
-    const at::Tensor& lens = dense(a.v[5], "kv_lens", at::kInt, {-1}, q.device);
-    const int seqs = whole(lens.size(0), "kv_lens");
-    const at::Tensor& qs = dense(a.v[4], "q_starts", at::kInt, {seqs + 1}, q.device);
-    const at::Tensor& table = dense(a.v[3], "page_table", at::kInt, {seqs, -1}, q.device);
+    const Ragged r = ragged(a.v[3], a.v[4], a.v[5], q.device);
     Run run(a.v[11], q.device);
     const Output out = output(a.v[8], "out", q, run);
     Owned owned{out.object};
     float* lse = lse_of(a.v[9], q);
-    const Space ws = workspace(a.v[10], q.T, seqs, q.Hq, c.Hkv, q.D, run);
-    check(lib.prefill_paged(&q.view, &c.c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(qs),
-                            ptr<int32_t>(lens), seqs, q.T, q.Hq, c.Hkv, q.D, q.code, truth(a.v[6]),
-                            scale_of(a.v[7], q.D), out.data, lse, ws.data, ws.bytes,
-                            run.stream),
+    const Space ws = workspace(a.v[10], q.T, r.seqs, q.Hq, c.Hkv, q.D, run);
+    check(lib.prefill_paged(&q.view, &c.c, r.table, r.pages, r.q_starts, r.lens, r.seqs, q.T, q.Hq, c.Hkv, q.D, q.code,
+                            truth(a.v[6]), scale_of(a.v[7], q.D), out.data, lse, ws.data, ws.bytes, run.stream),
           "moe_attn_prefill_paged");
     return owned.release();
   });
+}
+
+// The pages of a shared prefix (null without one)
+const int32_t* prefix_of(PyObject* table, int prefix_len, int page_size, int device) {
+  if (prefix_len <= 0) return nullptr;
+  if (!given(table)) throw Refusal{"prefix_len > 0 needs a prefix_table"};
+  const at::Tensor& pt = dense(table, "prefix_table", at::kInt, {-1}, device);
+  if (pt.size(0) * page_size < prefix_len)
+    throw Refusal{"prefix_table holds " + std::to_string(pt.size(0)) + " pages, too few for " +
+                  std::to_string(prefix_len) + " tokens"};
+  return ptr<int32_t>(pt);
 }
 
 Spec decode_spec = {"attn_decode", 12};
@@ -372,15 +460,7 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
     const at::Tensor& lens = dense(a.v[4], "kv_lens", at::kInt, {q.T}, q.device);
     const at::Tensor& table = dense(a.v[3], "page_table", at::kInt, {q.T, -1}, q.device);
     const int prefix_len = (int)integer(a.v[6], 0, "prefix_len");
-    const int32_t* prefix = nullptr;
-    if (prefix_len > 0) {
-      if (!given(a.v[5])) throw Refusal{"prefix_len > 0 needs a prefix_table"};
-      const at::Tensor& pt = dense(a.v[5], "prefix_table", at::kInt, {-1}, q.device);
-      if (pt.size(0) * c.c.page_size < prefix_len)
-        throw Refusal{"prefix_table holds " + std::to_string(pt.size(0)) + " pages, too few for " +
-                      std::to_string(prefix_len) + " tokens"};
-      prefix = ptr<int32_t>(pt);
-    }
+    const int32_t* prefix = prefix_of(a.v[5], prefix_len, c.c.page_size, q.device);
     Run run(a.v[11], q.device);
     const Output out = output(a.v[8], "out", q, run);
     Owned owned{out.object};
@@ -394,6 +474,119 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* 
   });
 }
 
+Spec paged_fp8_spec = {"attn_prefill_paged_fp8", 13};
+PyObject* attn_prefill_paged_fp8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    const Args a = parse(paged_fp8_spec, args, n, kw);
+    const Query q = query(a.v[0]);
+    const CacheFp8 c = cache_fp8(a.v[1], a.v[2], a.v[3], q);
+    const Ragged r = ragged(a.v[4], a.v[5], a.v[6], q.device);
+    Run run(a.v[12], q.device);
+    const Output out = output(a.v[9], "out", q, run);
+    Owned owned{out.object};
+    float* lse = lse_of(a.v[10], q);
+    const Space ws = workspace(a.v[11], q.T, r.seqs, q.Hq, c.Hkv, q.D, run);
+    check(lib.prefill_paged_fp8(&q.view, &c.c, r.table, r.pages, r.q_starts, r.lens, r.seqs, q.T, q.Hq, c.Hkv, q.D,
+                                q.code, truth(a.v[7]), scale_of(a.v[8], q.D), out.data, lse, ws.data, ws.bytes,
+                                run.stream),
+          "moe_attn_prefill_paged_fp8");
+    return owned.release();
+  });
+}
+
+Spec decode_fp8_spec = {"attn_decode_fp8", 13};
+PyObject* attn_decode_fp8(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    const Args a = parse(decode_fp8_spec, args, n, kw);
+    const Query q = query(a.v[0]);
+    const CacheFp8 c = cache_fp8(a.v[1], a.v[2], a.v[3], q);
+    const at::Tensor& lens = dense(a.v[5], "kv_lens", at::kInt, {q.T}, q.device);
+    const at::Tensor& table = dense(a.v[4], "page_table", at::kInt, {q.T, -1}, q.device);
+    const int prefix_len = (int)integer(a.v[7], 0, "prefix_len");
+    const int32_t* prefix = prefix_of(a.v[6], prefix_len, c.c.page_size, q.device);
+    Run run(a.v[12], q.device);
+    const Output out = output(a.v[9], "out", q, run);
+    Owned owned{out.object};
+    float* lse = lse_of(a.v[10], q);
+    const Space ws = workspace(a.v[11], q.T, q.T, q.Hq, c.Hkv, q.D, run);
+    check(lib.decode_fp8(&q.view, &c.c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(lens),
+                         prefix, prefix_len, q.T, q.Hq, c.Hkv, q.D, q.code, scale_of(a.v[8], q.D), out.data, lse,
+                         ws.data, ws.bytes, run.stream),
+          "moe_attn_decode_fp8");
+    return owned.release();
+  });
+}
+
+Spec weights_spec = {"attn_key_weights", 11};
+PyObject* attn_key_weights(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    const Args a = parse(weights_spec, args, n, kw);
+    const Query q = query(a.v[0]);
+    const at::Tensor& kt = dense(a.v[1], "k_cache", q.type, {-1, -1, -1, q.D}, q.device);
+    const int Hkv = whole(kt.size(1), "k_cache");
+    const Ragged r = ragged(a.v[2], a.v[3], a.v[4], q.device);
+    const float* lse = ptr<float>(dense(a.v[5], "lse", at::kFloat, {q.T, q.Hq}, q.device));
+    const at::Tensor& wt = dense(a.v[6], "weights", at::kFloat, {r.seqs, Hkv, -1}, q.device);
+    Run run(a.v[10], q.device);
+    const Space ws = workspace(a.v[9], q.T, r.seqs, q.Hq, Hkv, q.D, run);
+    check(lib.key_weights(&q.view, kt.data_ptr(), whole(kt.size(0), "k_cache"), whole(kt.size(2), "k_cache"), r.table,
+                          r.pages, r.q_starts, r.lens, r.seqs, q.T, q.Hq, Hkv, q.D, q.code, truth(a.v[7]),
+                          scale_of(a.v[8], q.D), lse, ptr<float>(wt), whole(wt.size(2), "weights"), ws.data, ws.bytes,
+                          run.stream),
+          "moe_attn_key_weights");
+    Py_INCREF(a.v[6]);
+    return a.v[6];
+  });
+}
+
+// The caller's tensor, or a new one
+Owned made(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, Run& run, void** data) {
+  if (given(o)) {
+    *data = dense(o, name, type, shape, run.device).data_ptr();
+    Py_INCREF(o);
+    return Owned{o};
+  }
+  const at::Tensor t = run.returned(run.make(shape, type));
+  *data = t.data_ptr();
+  return Owned{THPVariable_Wrap(t)};
+}
+
+Spec evict_spec = {"kv_evict", 14};
+PyObject* kv_evict(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded([&]() -> PyObject* {
+    const Args a = parse(evict_spec, args, n, kw);
+    const at::Tensor& kt = as_tensor(a.v[0], "k_cache");
+    const at::ScalarType type = kt.scalar_type();
+    if (type != at::kBFloat16 && type != at::kHalf) throw Refusal{"k_cache must be a bfloat16 or float16 torch.Tensor"};
+    if (!kt.is_cuda()) throw Refusal{"k_cache must be a CUDA tensor"};
+    const int device = c10::cuda::current_device();
+    dense(a.v[0], "k_cache", type, {-1, -1, -1, -1}, device);
+    const at::Tensor& vt = dense(a.v[1], "v_cache", type, kt.sizes(), device);
+    const moe_kv_cache c{kt.data_ptr(), vt.data_ptr(), whole(kt.size(0), "k_cache"), whole(kt.size(2), "k_cache")};
+    const int Hkv = whole(kt.size(1), "k_cache"), D = whole(kt.size(3), "k_cache");
+    const at::Tensor& lens = dense(a.v[3], "kv_lens", at::kInt, {-1}, device);
+    const int seqs = whole(lens.size(0), "kv_lens");
+    const at::Tensor& table = dense(a.v[2], "page_table", at::kInt, {seqs, -1}, device);
+    const at::Tensor& wt = dense(a.v[4], "weights", at::kFloat, {seqs, Hkv, -1}, device);
+    const at::Tensor& to = dense(a.v[5], "out_table", at::kInt, {seqs, -1}, device);
+    const int budget = (int)integer(a.v[6], 0, "budget"), first = (int)integer(a.v[7], 0, "keep_first"),
+              last = (int)integer(a.v[8], 0, "keep_last");
+    if (budget <= 0) throw Refusal{"budget must be positive"};
+    Run run(a.v[13], device);
+    void *new_lens, *new_weights, *kept;
+    Owned o0 = made(a.v[9], "new_lens", at::kInt, {seqs}, run, &new_lens);
+    Owned o1 = made(a.v[10], "new_weights", at::kFloat, {seqs, Hkv, budget}, run, &new_weights);
+    Owned o2 = made(a.v[11], "kept", at::kInt, {seqs, Hkv, budget}, run, &kept);
+    const Space ws = workspace(a.v[12], 0, seqs, Hkv, Hkv, D, run);
+    check(lib.evict(&c, ptr<int32_t>(table), whole(table.size(1), "page_table"), ptr<int32_t>(lens), ptr<float>(wt),
+                    whole(wt.size(2), "weights"), ptr<int32_t>(to), whole(to.size(1), "out_table"), budget, first, last,
+                    seqs, Hkv, D, static_cast<int32_t*>(new_lens), static_cast<float*>(new_weights),
+                    static_cast<int32_t*>(kept), ws.data, ws.bytes, run.stream),
+          "moe_kv_evict");
+    return PyTuple_Pack(3, o0.o, o1.o, o2.o);
+  });
+}
+
 PyObject* bind(PyObject*, PyObject* args);
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL | METH_KEYWORDS
@@ -402,33 +595,49 @@ PyMethodDef methods[] = {
     {"attn_prefill", FAST(attn_prefill), nullptr},
     {"attn_prefill_paged", FAST(attn_prefill_paged), nullptr},
     {"attn_decode", FAST(attn_decode), nullptr},
+    {"rope_append_fp8", FAST(rope_append_fp8), nullptr},
+    {"attn_prefill_paged_fp8", FAST(attn_prefill_paged_fp8), nullptr},
+    {"attn_decode_fp8", FAST(attn_decode_fp8), nullptr},
+    {"attn_key_weights", FAST(attn_key_weights), nullptr},
+    {"kv_evict", FAST(kv_evict), nullptr},
     {"bind", bind, METH_VARARGS, "Connect the functions to a loaded library and to their Python definitions."},
     {nullptr, nullptr, 0, nullptr}};
 
+Spec* const specs[] = {&rope_spec,     &prefill_spec,   &paged_spec,      &decode_spec, &rope_fp8_spec,
+                       &paged_fp8_spec, &decode_fp8_spec, &weights_spec, &evict_spec};
+constexpr int kFunctions = sizeof(specs) / sizeof(specs[0]);
+static_assert(sizeof(methods) / sizeof(methods[0]) == kFunctions + 2, "a method per function, bind and the end");
+
 // bind(error type, addresses of the library's functions in the order of
-// Library, then for each of the first four methods (parameter names, defaults
-// of the last of them, documentation))
+// Library, then for each of the functions above (parameter names, defaults of
+// the last of them, documentation))
 PyObject* bind(PyObject*, PyObject* args) {
-  PyObject* err;
-  unsigned long long p[6];
-  PyObject *names[4], *defaults[4];
-  const char* doc[4];
-  if (!PyArg_ParseTuple(args, "OKKKKKK(O!O!s)(O!O!s)(O!O!s)(O!O!s)", &err, &p[0], &p[1], &p[2], &p[3], &p[4], &p[5],
-                        &PyTuple_Type, &names[0], &PyTuple_Type, &defaults[0], &doc[0],
-                        &PyTuple_Type, &names[1], &PyTuple_Type, &defaults[1], &doc[1],
-                        &PyTuple_Type, &names[2], &PyTuple_Type, &defaults[2], &doc[2],
-                        &PyTuple_Type, &names[3], &PyTuple_Type, &defaults[3], &doc[3]))
+  if (PyTuple_GET_SIZE(args) != 1 + kAddresses + kFunctions) {
+    PyErr_Format(PyExc_TypeError, "bind: %d arguments expected", 1 + kAddresses + kFunctions);
     return nullptr;
-  Spec* specs[4] = {&rope_spec, &prefill_spec, &paged_spec, &decode_spec};
-  for (int f = 0; f < 4; ++f) {
+  }
+  void* address[kAddresses];
+  for (int i = 0; i < kAddresses; ++i) {
+    address[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(args, 1 + i));
+    if (PyErr_Occurred()) return nullptr;
+  }
+  for (int f = 0; f < kFunctions; ++f) {
     Spec& s = *specs[f];
-    if (PyTuple_GET_SIZE(names[f]) != s.total || PyTuple_GET_SIZE(defaults[f]) > s.total) {
+    PyObject *names, *defaults;
+    const char* doc;
+    PyObject* given_spec = PyTuple_GET_ITEM(args, 1 + kAddresses + f);
+    if (!PyTuple_Check(given_spec)) {
+      PyErr_SetString(PyExc_TypeError, "bind: a tuple per function expected");
+      return nullptr;
+    }
+    if (!PyArg_ParseTuple(given_spec, "O!O!s", &PyTuple_Type, &names, &PyTuple_Type, &defaults, &doc)) return nullptr;
+    if (PyTuple_GET_SIZE(names) != s.total || PyTuple_GET_SIZE(defaults) > s.total) {
       PyErr_Format(PyExc_TypeError, "%s: %d parameters expected", s.function, s.total);
       return nullptr;
     }
-    s.required = s.total - (int)PyTuple_GET_SIZE(defaults[f]);
+    s.required = s.total - (int)PyTuple_GET_SIZE(defaults);
     for (int i = 0; i < s.total; ++i) {
-      PyObject* name = PyTuple_GET_ITEM(names[f], i);
+      PyObject* name = PyTuple_GET_ITEM(names, i);
       if (!PyUnicode_Check(name)) {
         PyErr_SetString(PyExc_TypeError, "parameter names must be strings");
         return nullptr;
@@ -436,21 +645,17 @@ PyObject* bind(PyObject*, PyObject* args) {
       Py_INCREF(name);
       PyUnicode_InternInPlace(&name);
       Py_XSETREF(s.names[i], name);
-      PyObject* value = i < s.required ? nullptr : PyTuple_GET_ITEM(defaults[f], i - s.required);
+      PyObject* value = i < s.required ? nullptr : PyTuple_GET_ITEM(defaults, i - s.required);
       Py_XINCREF(value);
       Py_XSETREF(s.defaults[i], value);
     }
-    s.doc = doc[f];
+    s.doc = doc;
     methods[f].ml_doc = s.doc.c_str();
   }
+  PyObject* err = PyTuple_GET_ITEM(args, 0);
   Py_INCREF(err);
   Py_XSETREF(error_type, err);
-  lib.workspace_size = reinterpret_cast<decltype(lib.workspace_size)>(p[0]);
-  lib.rope_append = reinterpret_cast<decltype(lib.rope_append)>(p[1]);
-  lib.prefill = reinterpret_cast<decltype(lib.prefill)>(p[2]);
-  lib.prefill_paged = reinterpret_cast<decltype(lib.prefill_paged)>(p[3]);
-  lib.decode = reinterpret_cast<decltype(lib.decode)>(p[4]);
-  lib.error_string = reinterpret_cast<decltype(lib.error_string)>(p[5]);
+  std::memcpy(&lib, address, sizeof(lib));
   Py_RETURN_NONE;
 }
 

@@ -388,7 +388,7 @@ typedef struct {
   int32_t page_size;
 } moe_kv_cache;
 
-/* Bytes of workspace for any moe_rope_append / moe_attn_* call with up to T
+/* Bytes of workspace for any moe_rope_append* / moe_attn_* call with up to T
  * query rows and n_seq sequences.  Returns 0 for an invalid shape. */
 size_t moe_attn_workspace_size(int T, int n_seq, int Hq, int Hkv, int D);
 
@@ -417,6 +417,62 @@ int moe_rope_append(const moe_heads *q, const moe_heads *k, const moe_heads *v, 
                     int interleaved, const int32_t *positions, const int32_t *slots, int T, int Hq,
                     int Hkv, int D, int dtype, void *q_out, const moe_kv_cache *cache,
                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * moe_rope_append with positions of several axes (time, height and width of
+ * images and video): `positions` is [n_axes, T], and the angle of pair i of
+ * token t is that of position positions[axes[i], t].
+ *   axes       [rot / 2] uint8, each below n_axes (4-byte aligned)
+ *   1 <= n_axes <= 4; axes NULL: one position per token, as moe_rope_append.
+ */
+int moe_rope_append_axes(const moe_heads *q, const moe_heads *k, const moe_heads *v,
+                         const float *q_norm, const float *k_norm, float eps, const float *table,
+                         int max_pos, int rot, int interleaved, const int32_t *positions,
+                         const uint8_t *axes, int n_axes, const int32_t *slots, int T, int Hq,
+                         int Hkv, int D, int dtype, void *q_out, const moe_kv_cache *cache,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A paged cache in 8 bits (host struct): k and v hold e4m3 codes [pages, Hkv,
+ * page_size, D], and each 16 tokens of a page share one scale per head for
+ * their keys and one for their values:
+ *   key = code * scales[page, h, row / 16, 0],  value: [.., 1]
+ *   scales [pages, Hkv, page_size / 16, 2] fp32, powers of two 2^e with
+ *          -24 <= e <= 7 (another value counts as the power of two below it,
+ *          within that range)
+ * A value beyond 448 * 2^7 = 57344 is stored as that, an infinity too; NaN
+ * stays NaN. */
+typedef struct {
+  void *k;
+  void *v;
+  float *scales;
+  int32_t pages;
+  int32_t page_size;
+} moe_kv_cache_fp8;
+
+/*
+ * moe_rope_append to a cache in 8 bits.  Where the tokens go follows from the
+ * page table: sequence s has the rows q_starts[s] .. q_starts[s + 1] and, with
+ * them, kv_lens[s] tokens, so that its last row is token kv_lens[s] - 1.  The
+ * new rows of a scale block take the smallest e with which their largest
+ * magnitude (fp32, before rounding) is at most 448 * 2^e; rows that the block
+ * held before keep its scale or, where it has to grow, are rounded once more
+ * with the new one (exactly, unless a code becomes subnormal).  Each code is
+ * rounded once, to nearest even.  Rows behind a sequence's end stay as they
+ * were; no other sequence may have its own tokens in the same 16 rows.
+ *   positions  [T], or [n_axes, T] with axes as in moe_rope_append_axes
+ *   page_table [n_seq, table_pages], q_starts [n_seq + 1], kv_lens [n_seq];
+ *              q_starts go from 0 to T (the tokens of no sequence are reported
+ *              as MOE_ERR_DEVICE: only their queries are written), and
+ *              kv_lens[s] >= q_starts[s + 1] - q_starts[s]
+ */
+int moe_rope_append_fp8(const moe_heads *q, const moe_heads *k, const moe_heads *v,
+                        const float *q_norm, const float *k_norm, float eps, const float *table,
+                        int max_pos, int rot, int interleaved, const int32_t *positions,
+                        const uint8_t *axes, int n_axes, const int32_t *page_table, int table_pages,
+                        const int32_t *q_starts, const int32_t *kv_lens, int n_seq, int T, int Hq,
+                        int Hkv, int D, int dtype, void *q_out, const moe_kv_cache_fp8 *cache,
+                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Attention over packed sequences (whole prompts):
@@ -471,6 +527,63 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
                     int table_pages, const int32_t *kv_lens, const int32_t *prefix_table,
                     int prefix_len, int B, int Hq, int Hkv, int D, int dtype, float scale, void *out,
                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * moe_attn_prefill_paged and moe_attn_decode over a cache in 8 bits; queries
+ * and outputs are bf16 or f16, codes are multiplied exactly, every sum and
+ * softmax statistic is fp32.
+ */
+int moe_attn_prefill_paged_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,
+                               const int32_t *page_table, int table_pages, const int32_t *q_starts,
+                               const int32_t *kv_lens, int n_seq, int T, int Hq, int Hkv, int D,
+                               int dtype, int causal, float scale, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream);
+int moe_attn_decode_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,
+                        const int32_t *page_table, int table_pages, const int32_t *kv_lens,
+                        const int32_t *prefix_table, int prefix_len, int B, int Hq, int Hkv, int D,
+                        int dtype, float scale, void *out, float *lse, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * Attention weight of every key, for eviction: what the rows of a call give to
+ * the keys of their sequences, added to what `weights` holds,
+ *   weights[s, h, j] += sum_{t, g} exp(scale * q[t, hG + g] . k[j, h] - lse[t, hG + g])
+ * over the rows t of sequence s that see key j (`causal` as in
+ * moe_attn_prefill) and the heads g of a group.  Rows whose lse is -inf add
+ * nothing.  Each entry is one fp32 sum in a fixed order, added once; entries
+ * behind a sequence's keys stay as they were.
+ *   k_cache [pages, Hkv, page_size, D] of the type of q (the keys alone)
+ *   lse     [T, Hq] fp32, as the attention call over the same rows gave it
+ *   weights [n_seq, Hkv, capacity] fp32, kv_lens[s] <= capacity (4-byte aligned)
+ * A decode batch is one row per sequence: q_starts 0, 1, .. B.
+ */
+int moe_attn_key_weights(const moe_heads *q, const void *k_cache, int pages, int page_size,
+                         const int32_t *page_table, int table_pages, const int32_t *q_starts,
+                         const int32_t *kv_lens, int n_seq, int T, int Hq, int Hkv, int D, int dtype,
+                         int causal, float scale, const float *lse, float *weights, int capacity,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction by weight: each head of a sequence of n = kv_lens[s] keys keeps
+ * m = min(n, budget) of them: all, or the first keep_first, the last keep_last
+ * and, of those between, the ones of largest weight (of equal weights the
+ * first; NaN counts as the smallest).  The kept keys and values are copied, in
+ * their order, to rows 0 .. m - 1 of the pages out_table[s]; the pages they
+ * come from stay as they were.
+ *   weights     [n_seq, Hkv, capacity] fp32
+ *   out_table   [n_seq, out_pages] int32, budget <= out_pages * page_size; none
+ *               of these pages may be one that a sequence of the call reads
+ *   new_lens    [n_seq] int32 (out): m
+ *   new_weights [n_seq, Hkv, budget] fp32 (out): weights of the kept keys, 0 from m on
+ *   kept        [n_seq, Hkv, budget] int32 (out): their places before, -1 from m on
+ * The cache is bf16 or f16 (its bits are copied).  Workspace of
+ * moe_attn_workspace_size(0, n_seq, Hkv, Hkv, D) bytes.
+ */
+int moe_kv_evict(const moe_kv_cache *cache, const int32_t *page_table, int table_pages,
+                 const int32_t *kv_lens, const float *weights, int capacity,
+                 const int32_t *out_table, int out_pages, int budget, int keep_first, int keep_last,
+                 int n_seq, int Hkv, int D, int32_t *new_lens, float *new_weights, int32_t *kept,
+                 void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * TEST ONLY.  With wait > 0, every moe_attn_* launched afterwards in this
