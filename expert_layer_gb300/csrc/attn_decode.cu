@@ -40,14 +40,15 @@ constexpr int kSlice = 16;          // keys
 constexpr int kWindow = kThreads;   // sequences whose lengths a block keeps in shared memory
 constexpr float kLag = 8.0f;        // log2 of how far the maximum in use may lag
 
-template <int D, bool kWide>
+template <int D, bool kWide, bool kCodes>
 struct Shape {
   static constexpr int kRows = kWide ? 16 : 8;                     // heads of a unit
   static constexpr int kHalves = D / 64;
   static constexpr int kGroup = kHalves * 1024;                    // 8 keys: kHalves swizzle atoms
-  static constexpr int kTileBytes = 2 * kGroup;                    // K or V of a slice
+  static constexpr int kTileBytes = kCodes ? kSlice * D : 2 * kGroup;   // K or V of a slice
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 64 ? 5 : kWide ? 2 : 3;      // slices in flight per warp
+  // slices in flight per warp
+  static constexpr int kStages = kCodes ? (D == 64 ? 8 : kWide ? 4 : 5) : D == 64 ? 5 : kWide ? 2 : 3;
   static constexpr int kRing = kStages * kStageBytes;              // of one warp
   static constexpr int kPart = kRows * D * 4;                      // O of one unit
   static_assert(kPart <= kRing, "a warp's last part takes the place of its ring");
@@ -55,11 +56,14 @@ struct Shape {
   static constexpr int kStats = kFirst + kWarps * kPart;           // m and l of the rows, two parts per warp
   static constexpr int kOpen = kStats + kWarps * 2 * kRows * 8;       // the units that the parts belong to
   static constexpr int kBars = kOpen + kWarps * 2 * 16;
-  static constexpr int kLens = kBars + kWarps * kStages * 8;
+  static constexpr int kScales = kBars + kWarps * kStages * 8;     // of the slices of the rings (K, V)
+  static constexpr int kLens = kScales + (kCodes ? kWarps * kStages * 8 : 0);
   static constexpr int kScan = kLens + kWindow * 4;
   static constexpr size_t kSmem = kScan + 128;
 };
-static_assert(Shape<128, false>::kSmem <= 232448 && Shape<128, true>::kSmem <= 232448, "227 KB a block");
+static_assert(Shape<128, false, false>::kSmem <= 232448 && Shape<128, true, false>::kSmem <= 232448 &&
+                  Shape<128, false, true>::kSmem <= 232448 && Shape<128, true, true>::kSmem <= 232448,
+              "227 KB a block");
 
 // The units of a range: a cursor over (sequence, unit of the sequence),
 // empty sequences left out.  `pos` is the unit's place on the line; its slices
@@ -102,6 +106,32 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// Two e4m3 codes (the low or the high half of w) as f16
+template <int kHalf>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  uint32_t r;
+  if (kHalf) asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(w));
+  else asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+// The bytes of a row of codes in a tile as TMA leaves it: 16-byte pieces
+// swizzled by the row (128-byte rows by 128 bytes, 64-byte rows by 64)
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t tile, int row, int byte) {
+  const int piece = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
+  return tile + row * D + piece * 16 + (byte & 15);
+}
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
   const int n = a.kv_lens[b];
   return n < 0 || n > ((long long)a.table_pages << a.page_shift) ? 0 : n;
@@ -133,11 +163,13 @@ __device__ __forceinline__ void advance(const Lens& lens, Cursor& c, int units) 
   }
 }
 
-template <int D, bool kF16, bool kWide>
+template <int D, bool kF16, bool kWide, bool kCodes>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const DecodeArgs t, const Report rep) {
-  using S = Shape<D, kWide>;
+  using S = Shape<D, kWide, kCodes>;
+  constexpr bool kP16 = kF16 || kCodes;              // operands of the products: f16 (else bf16)
+  constexpr int kCols = D / 8;                       // codes: elements of a column of a fragment
   constexpr int kRowSets = kWide ? 2 : 1;            // rows g and (wide) g + 8 of a thread
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
@@ -150,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = t.G, units = a.Hkv * t.chunks;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars) + warp * kStages;
   unsigned char* ring = smem + warp * S::kRing;
+  float2* scales = reinterpret_cast<float2*>(smem + S::kScales) + warp * kStages;
   bool bad = false, late = false;
   pdl_trigger();     // the merge kernel may become resident; it waits for this grid's end
   if (threadIdx.x == 0) {
@@ -158,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], t.arrivals);
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], t.arrivals + (kCodes ? 1 : 0));     // (codes: the scales' copy)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     open[2 * warp].b = open[2 * warp + 1].b = -1;
@@ -258,8 +291,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
         unsigned char* dst = ring + st * S::kStageBytes;
         mbar_expect_tx(&bars[st], S::kStageBytes);
-        tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
-        tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+        if (kCodes) {
+          tma_load_3d(dst, &tmK, 0, row, page * a.Hkv + hk, &bars[st]);
+          tma_load_3d(dst + S::kTileBytes, &tmV, 0, row, page * a.Hkv + hk, &bars[st]);
+          const long long block = ((((long long)page * a.Hkv + hk) << a.page_shift) + row) / kScaleBlock;
+          asm volatile(
+              "cp.async.ca.shared.global [%0], [%1], 8;\n"
+              "cp.async.mbarrier.arrive.noinc.shared.b64 [%2];" ::"r"(smem_u32(&scales[st])),
+              "l"(a.scales + 2 * block), "r"(smem_u32(&bars[st]))
+              : "memory");
+        } else {
+          tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+          tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+        }
       }
       ++issued;
       ++ld_slice;
@@ -282,16 +326,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int rs = 0; rs < kRowSets; ++rs) {
         const int r = gq + 8 * rs;
-        const uint16_t* p = src + (long long)(h0 + (r < rows ? r : 0)) * a.q.head + 2 * quad;
+        const uint16_t* p = src + (long long)(h0 + (r < rows ? r : 0)) * a.q.head + (kCodes ? quad * (D / 4) : 2 * quad);
+        if (kCodes) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          q[kk][rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16) ^ t.flip : 0u;
-          q[kk][kRowSets + rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16 + 8) ^ t.flip : 0u;
+          for (int kk = 0; kk < D / 16; kk += 2) {
+            const uint4 w = r < rows ? *reinterpret_cast<const uint4*>(p + kk * 4) : make_uint4(0, 0, 0, 0);
+            q[kk][rs] = w.x ^ t.flip, q[kk][kRowSets + rs] = w.y ^ t.flip;
+            q[kk + 1][rs] = w.z ^ t.flip, q[kk + 1][kRowSets + rs] = w.w ^ t.flip;
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            q[kk][rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16) ^ t.flip : 0u;
+            q[kk][kRowSets + rs] = r < rows ? *reinterpret_cast<const uint32_t*>(p + kk * 16 + 8) ^ t.flip : 0u;
+          }
         }
+      }
+    };
+    // Codes are multiplied as f16: a row of bf16 queries comes to f16 times the
+    // power of two that brings its largest element to 2^14 .. 2^15, whose
+    // inverse joins the scale of its logits.  (Exact for elements down to 2^-28
+    // of the largest, and the rest, rounded to a 2^-39th of it, is below what
+    // fp32 sums keep.)
+    float unit_c[kRowSets];
+    auto settle_q = [&](uint32_t (&q)[D / 16][2 * kRowSets]) {
+#pragma unroll
+      for (int rs = 0; rs < kRowSets; ++rs) {
+        unit_c[rs] = t.c;
+        if (kF16 || !kCodes) continue;
+        uint32_t top = 0;                      // largest magnitude, as bits
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = q[kk][j * kRowSets + rs] & 0x7fff7fffu;
+            top = max(top, max(w >> 16, w & 0xffffu));
+          }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = (int)(top >> 7) - 127;   // an infinity or NaN: as it is
+        const int up = top == 0 || e == 128 ? 0 : min(14 - e, 60);
+        const float f = exp2i(up);
+        unit_c[rs] *= exp2i(-up);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t& w = q[kk][j * kRowSets + rs];
+            w = pack2<true>(bf16lo(w) * f, bf16hi(w) * f);
+          }
       }
     };
     uint32_t q[D / 16][2 * kRowSets];
     load_q(cur, q);
+    settle_q(q);
 
     while (cur.pos < we) {
       const int first = max(0, ws - cur.pos - kUnitCost), last = min(cur.slices, we - cur.pos - kUnitCost);
@@ -316,8 +404,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true, more = false;
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float slice_c[kRowSets], shift = 0.f, back = 1.0f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int rs = 0; rs < kRowSets; ++rs) slice_c[rs] = unit_c[rs];
+        if (kCodes) {
+          // logits times the keys' scale; the values' scale 2^e joins the
+          // exponent of the weights (P of the second product), l takes it back
+          const float2 f = scales[st];
+          const int ev = scale_exp(f.y);
+          const float fk = exp2i(scale_exp(f.x));
+          shift = (float)ev;
+          back = exp2i(-ev);
+#pragma unroll
+          for (int rs = 0; rs < kRowSets; ++rs) slice_c[rs] = fmaxf(unit_c[rs] * fk, 1.2e-38f);
+          uint32_t w[2][D / 16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+              const uint4 x = lds4(code_at<D>(kb, gq + 8 * h, quad * (D / 4) + 16 * i));
+              w[h][4 * i] = x.x, w[h][4 * i + 1] = x.y, w[h][4 * i + 2] = x.z, w[h][4 * i + 3] = x.w;
+            }
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t a1 = kWide ? q[kk][kRowSets - 1] : 0u, a3 = kWide ? q[kk][2 * kRowSets - 1] : 0u;
+            mma<true>(sc[0], q[kk][0], a1, q[kk][kRowSets], a3, codes2<0>(w[0][kk]), codes2<1>(w[0][kk]));
+            mma<true>(sc[1], q[kk][0], a1, q[kk][kRowSets], a3, codes2<0>(w[1][kk]), codes2<1>(w[1][kk]));
+          }
+        }
+#pragma unroll
+        for (int kk = 0; kk < (kCodes ? 0 : D / 16); ++kk) {
           uint32_t r[4];
           const int chunk = (kk & 3) * 2 + k_col;
           ldsm4(kb + (kk >> 2) * 1024 + k_at + ((chunk ^ (k_row & 7)) << 4), r);
@@ -342,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x = fmaxf(fmaxf(sc[0][2 * rs], sc[0][2 * rs + 1]), fmaxf(sc[1][2 * rs], sc[1][2 * rs + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          top[rs] = x * t.c;
+          top[rs] = kCodes ? fmaf(x, slice_c[rs], shift) : x * t.c;
           up |= top[rs] > m[rs] + kLag;
         }
         if (__any_sync(0xffffffffu, up)) {
@@ -361,12 +477,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int rs = 0; rs < kRowSets; ++rs) {
-          const float off = m[rs] == -INFINITY ? 0.f : m[rs];
+          const float off = m[rs] == -INFINITY ? 0.f : kCodes ? m[rs] - shift : m[rs];
+          const float c = kCodes ? slice_c[rs] : t.c;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(fmaf(sc[h][2 * rs], t.c, -off)), p1 = ex2(fmaf(sc[h][2 * rs + 1], t.c, -off));
-            l[rs] += p0 + p1;
-            p[2 * h + rs] = pack2<kF16>(p0, p1);
+            const float p0 = ex2(fmaf(sc[h][2 * rs], c, -off)), p1 = ex2(fmaf(sc[h][2 * rs + 1], c, -off));
+            if (kCodes) l[rs] = fmaf(p0 + p1, back, l[rs]);
+            else l[rs] += p0 + p1;
+            p[2 * h + rs] = pack2<kP16>(p0, p1);
           }
         }
         // values past the end may be anything: a weight of 0 does not silence NaN
@@ -376,8 +494,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           keep0 = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
           keep1 = (k0 + 8 < valid ? 0xffffu : 0u) | (k0 + 9 < valid ? 0xffff0000u : 0u);
         }
+        if (kCodes) {
+          // keys 2 quad + {0, 1, 8, 9}, the D / 8 values from gq D / 8 on: element
+          // i of them is column gq of the i-th product
+          uint32_t w[4][D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+          for (int k = 0; k < 4; ++k) {
+            const int key = 2 * quad + (k & 1) + 8 * (k >> 1);
+            const uint32_t at = code_at<D>(vb, key, gq * kCols);
+            if (D == 128) {
+              const uint4 x = lds4(at);
+              w[k][0] = x.x, w[k][1] = x.y, w[k][D / 32 - 2] = x.z, w[k][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = lds2(at);
+              w[k][0] = x.x, w[k][1] = x.y;
+            }
+            if (key >= valid)
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) w[k][i] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t a01 = __byte_perm(w[0][i], w[1][i], 0x5140), a23 = __byte_perm(w[0][i], w[1][i], 0x7362);
+            const uint32_t b01 = __byte_perm(w[2][i], w[3][i], 0x5140), b23 = __byte_perm(w[2][i], w[3][i], 0x7362);
+            mma<true>(o[4 * i], p[0], p[1], p[2], p[3], codes2<0>(a01), codes2<0>(b01));
+            mma<true>(o[4 * i + 1], p[0], p[1], p[2], p[3], codes2<1>(a01), codes2<1>(b01));
+            mma<true>(o[4 * i + 2], p[0], p[1], p[2], p[3], codes2<0>(a23), codes2<0>(b23));
+            mma<true>(o[4 * i + 3], p[0], p[1], p[2], p[3], codes2<1>(a23), codes2<1>(b23));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < (kCodes ? 0 : D / 16); ++i) {
           uint32_t r[4];
           const int chunk = (i & 3) * 2 + v_col;
           ldsm4_t(vb + (i >> 2) * 1024 + v_at + ((chunk ^ (v_row & 7)) << 4), r);
@@ -395,6 +542,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
         l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
       }
+      // O of the thread's row times f, to the row at `to`: columns 8 i + 2 quad +
+      // {0, 1}, with codes the D / 8 from 2 quad D / 8 and from (2 quad + 1) D / 8 on
+      auto put_part = [&](float* to, int rs, float f) {
+        if (kCodes) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < kCols; i += 4)
+              *reinterpret_cast<float4*>(to + (2 * quad + j) * kCols + i) =
+                  make_float4(o[i][2 * rs + j] * f, o[i + 1][2 * rs + j] * f, o[i + 2][2 * rs + j] * f,
+                              o[i + 3][2 * rs + j] * f);
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2*>(to + 8 * i + 2 * quad) = make_float2(o[i][2 * rs] * f, o[i][2 * rs + 1] * f);
+        }
+      };
       if (last <= first) {
         // none of its slices: the range ends before them
       } else if (first == 0 && last == cur.slices) {
@@ -409,16 +573,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = l[rs] > 0.f ? 1.0f / l[rs] : l[rs], lse = m[rs] + lg2(l[rs]);
           if (t.p.row_o) {
             if (lane == 0 && rs == 0) t.p.held[cur.b * units + cur.u] = make_int2(1, 0);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<float2*>(t.p.row_o + row * D + 8 * i + 2 * quad) =
-                  make_float2(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+            put_part(t.p.row_o + row * D, rs, inv);
             if (quad == 0) t.p.row_lse[row] = lse;
           } else {
+            if (kCodes) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<uint32_t*>(a.out + row * D + 8 * i + 2 * quad) =
-                  pack2<kF16>(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < kCols; i += 8)
+                  *reinterpret_cast<uint4*>(a.out + row * D + (2 * quad + j) * kCols + i) =
+                      make_uint4(pack2<kF16>(o[i][2 * rs + j] * inv, o[i + 1][2 * rs + j] * inv),
+                                 pack2<kF16>(o[i + 2][2 * rs + j] * inv, o[i + 3][2 * rs + j] * inv),
+                                 pack2<kF16>(o[i + 4][2 * rs + j] * inv, o[i + 5][2 * rs + j] * inv),
+                                 pack2<kF16>(o[i + 6][2 * rs + j] * inv, o[i + 7][2 * rs + j] * inv));
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint32_t*>(a.out + row * D + 8 * i + 2 * quad) =
+                    pack2<kF16>(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+            }
             if (a.lse && quad == 0) a.lse[row] = lse * 0.693147180559945f;
           }
         }
@@ -429,10 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* dst = reinterpret_cast<float*>(part ? ring : smem + S::kFirst + warp * S::kPart);
 #pragma unroll
         for (int rs = 0; rs < kRowSets; ++rs) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(dst + (gq + 8 * rs) * D + 8 * i + 2 * quad) =
-                make_float2(o[i][2 * rs], o[i][2 * rs + 1]);
+          put_part(dst + (gq + 8 * rs) * D, rs, 1.0f);
           if (quad == 0) stats[(2 * warp + part) * S::kRows + gq + 8 * rs] = make_float2(m[rs], l[rs]);
         }
         if (lane == 0) open[2 * warp + part] = Open{cur.b, cur.u, cur.slices, cur.pos};
@@ -446,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 2 * kRowSets; ++j) q[kk][j] = qn[kk][j];
       }
+      if (cur.pos < we) settle_q(q);
     }
     // after a timeout: the loads already issued land before the block exits
     if (late && lane == 0)
@@ -542,11 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0) pdl_wait();
 }
 
-template <int D, bool kF16, bool kWide>
+template <int D, bool kF16, bool kWide, bool kCodes>
 cudaError_t launch(const DecodeArgs& t, const CUtensorMap& k, const CUtensorMap& v, const Report& rep, bool beside,
                    int grid, cudaStream_t stream) {
-  auto kern = attn_decode_kernel<D, kF16, kWide>;
-  constexpr size_t smem = Shape<D, kWide>::kSmem;
+  auto kern = attn_decode_kernel<D, kF16, kWide, kCodes>;
+  constexpr size_t smem = Shape<D, kWide, kCodes>::kSmem;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   if (beside) return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, stream, k, v, t, rep);
@@ -573,12 +744,17 @@ cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const De
   t.arrivals = a.hold == kHoldDecode ? 2 : 1;
   t.p = p;
   CUtensorMap k, v;
-  if (!pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice)) return cudaErrorInvalidValue;
+  const bool codes = a.scales != nullptr;
+  if (codes ? !codes_map(&k, a.k_cache, a, kSlice) || !codes_map(&v, a.v_cache, a, kSlice)
+            : !pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice))
+    return cudaErrorInvalidValue;
   Report rep = shape;
   rep.blocks[rep.set] = num_sms;
   const bool wide = G > 8;
 #define DECODE_CASE(DD, F, W) \
-  if (a.D == DD && (a.f16 != 0) == F && wide == W) return launch<DD, F, W>(t, k, v, rep, beside.prefix, num_sms, stream);
+  if (a.D == DD && (a.f16 != 0) == F && wide == W)                                       \
+    return codes ? launch<DD, F, W, true>(t, k, v, rep, beside.prefix, num_sms, stream) \
+                 : launch<DD, F, W, false>(t, k, v, rep, beside.prefix, num_sms, stream);
   DECODE_CASE(64, false, false)
   DECODE_CASE(64, false, true)
   DECODE_CASE(64, true, false)

@@ -145,11 +145,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const void* sr
 
 // ------------------------------------------------------------------ host side
 inline bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+                   const cuuint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = encode_fn();
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn && fn(m, type, rank, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -175,6 +176,17 @@ inline bool pages_map(CUtensorMap* m, const uint16_t* cache, const AttnArgs& a, 
   const cuuint64_t strides[4] = {a.D * 2ull, 128, a.D * 16ull, page * 2};
   const cuuint32_t box[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)rows / 8, 1};
   return encode(m, cache, 5, dims, strides, box);
+}
+
+// A cache of codes [pages, Hkv, page_size, D] as {D, row, page * Hkv + head}: a
+// box of {D, rows, 1} brings `rows` rows of D bytes, one after the other,
+// swizzled by their own width.
+inline bool codes_map(CUtensorMap* m, const void* cache, const AttnArgs& a, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, 1ull << a.page_shift, (cuuint64_t)a.pages * a.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D, (cuuint64_t)a.D << a.page_shift};
+  const cuuint32_t box[3] = {(cuuint32_t)a.D, (cuuint32_t)rows, 1};
+  return encode(m, cache, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
