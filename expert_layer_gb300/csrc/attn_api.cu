@@ -182,7 +182,6 @@ int run_attn(AttnArgs& a, const moe_heads* q, int dtype, void* out, float* lse, 
   if (lse && !aligned(lse, 4)) return MOE_ERR_UNSUPPORTED;
   ATTN_TRY(need16(workspace));
   if (!(a.scale == a.scale) || a.scale > 3.0e38f || a.scale < -3.0e38f) return MOE_ERR_INVALID_ARG;
-  if (a.scales && (a.q_starts || a.prefix_len > 0)) return MOE_ERR_UNSUPPORTED;     // (to come)
   const Layout L = make_attn_layout(a.T, a.n_seq, a.Hq, a.Hkv, a.D);
   if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
   int sms = 0;

@@ -106,32 +106,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// Two e4m3 codes (the low or the high half of w) as f16
-template <int kHalf>
-__device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  uint32_t r;
-  if (kHalf) asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(w));
-  else asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
-  return r;
-}
-// The bytes of a row of codes in a tile as TMA leaves it: 16-byte pieces
-// swizzled by the row (128-byte rows by 128 bytes, 64-byte rows by 64)
-template <int D>
-__device__ __forceinline__ uint32_t code_at(uint32_t tile, int row, int byte) {
-  const int piece = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
-  return tile + row * D + piece * 16 + (byte & 15);
-}
-__device__ __forceinline__ uint4 lds4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 lds2(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
   const int n = a.kv_lens[b];
   return n < 0 || n > ((long long)a.table_pages << a.page_shift) ? 0 : n;

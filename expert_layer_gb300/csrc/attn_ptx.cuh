@@ -27,6 +27,38 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two e4m3 codes (the low or the high half of w) as f16
+template <int kHalf>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  uint32_t r;
+  if (kHalf) asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(w));
+  else asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(w));
+  return r;
+}
+// The bytes of a row of codes in a tile as TMA leaves it: 16-byte pieces
+// swizzled by the row (128-byte rows by 128 bytes, 64-byte rows by 64)
+template <int D>
+__device__ __forceinline__ uint32_t code_at(uint32_t tile, int row, int byte) {
+  const int piece = D == 128 ? (byte >> 4) ^ (row & 7) : (byte >> 4) ^ ((row >> 1) & 3);
+  return tile + row * D + piece * 16 + (byte & 15);
+}
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t w) {
+  float2 v;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(w));
+  return v;
+}
 // Two fp32 values in one 64-bit register and the paired operations on them
 __device__ __forceinline__ uint64_t pair(float a, float b) {
   uint64_t r;

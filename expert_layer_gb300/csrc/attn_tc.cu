@@ -55,11 +55,20 @@ constexpr int kKeys = 128;          // keys of a block
 constexpr int kItems = 4;           // ring of work items
 constexpr int kAskAhead = 3;        // key blocks before an item's end at which the next one is asked for
 constexpr int kSoftWarps = 8;       // two tiles x four warps, one row per thread
-constexpr int kThreads = (kSoftWarps + 4) * 32;
-// Registers per thread: 168 at launch (three warpgroups); the softmax
-// warpgroups, which hold a row of 128 logits, draw on the third one's.
-constexpr int kSoftRegs = 208, kLoadRegs = 88;
-static_assert(2 * kSoftRegs + kLoadRegs <= 3 * 168, "the shares come from the launch's registers");
+// A cache in 8 bits: another warpgroup makes codes operands.
+constexpr int kCodeWarps = 4;
+template <bool kCodes>
+constexpr int kThreads = (kSoftWarps + 4 + (kCodes ? kCodeWarps : 0)) * 32;
+// Registers per thread: 168 at launch (three warpgroups; 128 with four); the
+// softmax warpgroups, which hold a row of 128 logits, draw on the others'.
+template <bool kCodes>
+constexpr int kSoftRegs = kCodes ? 192 : 208;
+template <bool kCodes>
+constexpr int kLoadRegs = kCodes ? 64 : 88;
+static_assert(2 * kSoftRegs<false> + kLoadRegs<false> <= 3 * 168 && 2 * kSoftRegs<true> + 2 * kLoadRegs<true> <= 4 * 128,
+              "the shares come from the launch's registers");
+constexpr int kScaleSlots = 8;      // key blocks whose scales are kept (see the producer)
+constexpr int kScaleBlocks = kKeys / kScaleBlock;
 constexpr int kHalf = kKeys / 2;
 constexpr float kMost = 32768.0f;   // sum of a row's P over half a block that asks for a new scale
 constexpr uint32_t kTmemCols = 512;
@@ -79,7 +88,8 @@ struct Shape {
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
   static constexpr int kOut = kRing + kStages * kTileBytes;    // 32 rows of 128 bytes per softmax warp
   static constexpr int kBars = kOut + kSoftWarps * 32 * 128;
-  static constexpr size_t kSmem = kBars + 1024;
+  static constexpr int kScales = kBars + 1024;                 // codes: [slot][16 keys] (K, V)
+  static constexpr size_t kSmem = kScales + (kPaged ? kScaleSlots * kScaleBlocks * 8 : 0);
 };
 
 struct Item {
@@ -272,13 +282,25 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // One thread issues all MMAs of a tile, in order: a commit after S(j+1) also
 // covers O += P(j) V, so a softmax warp that has S(j+1) may rescale O without
 // waiting.
-template <int D, bool kF16, bool kPaged>
-__global__ void __launch_bounds__(kThreads, 1)
+//
+// A cache in 8 bits (kCodes, paged): TMA brings the codes of a tile to the upper
+// half of its stage, and four more warps (12-15) make them the operand, in
+// place: every code is in registers before the first element is written.  K
+// becomes the queries' type, times its scale where that is bf16 (f16 keeps the
+// codes as they are, and the logits of 16 keys take the scale); V becomes f16
+// without its scale 2^e, which joins the exponent of P instead,
+//   P = 2^{c S + e - m'},  O += P code,  l += 2^{-e} sum P,
+// so that m' follows what a key adds to O, and P and the codes stay within f16
+// whatever the scales.
+template <int D, bool kF16, bool kPaged, bool kCodes>
+__global__ void __launch_bounds__(kThreads<kCodes>, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const TcAttnArgs t,
                    const Report rep) {
   using S = Shape<D, kPaged>;
   constexpr int NS = S::kStages;
+  constexpr bool kP16 = kF16 || kCodes;                        // P and V in f16 (else bf16)
+  static_assert(kPaged || !kCodes, "codes are paged");
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t* kv_empty = kv_full + NS;
@@ -293,9 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;
   uint64_t* clc = drain + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clc + 1);
+  uint64_t* code_full = clc + 1;         // codes: a tile's codes (and with K's the scales) have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(code_full + (kCodes ? NS : 0));
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  Item* ring = reinterpret_cast<Item*>(clc + 2);
+  Item* ring = reinterpret_cast<Item*>(tmem_slot + 2);
+  float2* scales = reinterpret_cast<float2*>(smem + S::kScales);
   uint4* answer = reinterpret_cast<uint4*>(smem + S::kBars + 1024 - 16);
 
   const AttnArgs& a = t.a;
@@ -311,7 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     const Arrivals& n = t.arrivals;
-    for (int s = 0; s < NS; ++s) { mbar_init(&kv_full[s], s ? 1 : n.keys); mbar_init(&kv_empty[s], n.stage); }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kv_full[s], (s ? 1 : n.keys) + (kCodes ? kCodeWarps - 1 : 0));
+      mbar_init(&kv_empty[s], n.stage);
+      if (kCodes) mbar_init(&code_full[s], s % 2 ? 1 : 33);       // K tiles (even): and every lane's copy of scales
+    }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], n.query);
       mbar_init(&q_empty[x], 1);
@@ -322,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&h_done[x], n.half);
       mbar_init(&turn[x], n.turn);
     }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], n.item); mbar_init(&it_empty[i], kSoftWarps + 2); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], n.item); mbar_init(&it_empty[i], kSoftWarps + 2 + (kCodes ? kCodeWarps : 0)); }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     mbar_init(clc, n.next);
@@ -342,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs<kCodes>));
     if (warp == kSoftWarps) {
     // ------------------------------------------------------------ producer
     uint32_t kv = 0, nq[2] = {0, 0}, ni = 0;    // loads issued, items published
@@ -445,12 +473,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = kv % NS;
           ok = warp_spin(&kv_empty[s], ((kv / NS) & 1) ^ 1);
           if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
+          if (lane == 0) {
+            if (kCodes) mbar_expect_tx(&code_full[s], (uint32_t)(nbox * t.box * D));
+            else mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
+          }
           __syncwarp();
           if (lane < nbox) {
             unsigned char* dst = smem + S::kRing + s * S::kTileBytes;
             const int key = b * kKeys + lane * t.box;
-            if (kPaged) {
+            if (kCodes) {
+              const int row = key & ((1 << a.page_shift) - 1);
+              tma_load_3d(dst + S::kTileBytes / 2 + lane * t.box * D, w ? &tmV : &tmK, 0, row, page * a.Hkv + it.head,
+                          &code_full[s]);
+              // the scales of both, with the K tile.  Those of block j + NS/2 + 1
+              // come after V of block j was given back, when both softmaxes
+              // have used the ones of block j: kScaleSlots > NS/2 + 1
+              static_assert(NS / 2 + 1 < kScaleSlots, "slots of scales");
+              if (w == 0) {
+                const long long block = ((((long long)page * a.Hkv + it.head) << a.page_shift) + row) / kScaleBlock;
+                const float2* from = reinterpret_cast<const float2*>(a.scales) + block;
+                float2* to = scales + (kv / 2) % kScaleSlots * kScaleBlocks + lane * (t.box / kScaleBlock);
+                for (int i = 0; i < t.box / kScaleBlock; ++i)
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to + i)), "l"(from + i) : "memory");
+              }
+            } else if (kPaged) {
               tma_load_5d(dst + lane * (t.box / 8) * S::kGroup, w ? &tmV : &tmK, 0, 0, 0,
                           (key & ((1 << a.page_shift) - 1)) / 8, page * a.Hkv + it.head, &kv_full[s]);
             } else {
@@ -459,6 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(dst + hh * S::kHalfBytes, w ? &tmV : &tmK, hh * 64, k0 + key, it.head, &kv_full[s]);
             }
           }
+          if (kCodes && w == 0)
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&code_full[s])) : "memory");
         }
         page = next;
       }
@@ -476,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // The loads issued land before the block exits, also where another warp
       // gives up after this one's last item (in normal use they are all used).
-      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i) spin_wait(&kv_full[i % NS], (i / NS) & 1);
+      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i)
+        spin_wait(kCodes ? &code_full[i % NS] : &kv_full[i % NS], (i / NS) & 1);
       for (int x = 0; x < 2; ++x)
         if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
     }
@@ -486,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp runs the loop on values that are uniform to the compiler
     // (constants, loop counters, results of warp reductions); one elected lane
     // issues.
-    constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
+    constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kP16>(D, true);
     const int x = __reduce_max_sync(0xffffffffu, warp - kSoftWarps - 1);      // tile
     const uint32_t tS = x * kKeys, tO = 2 * kKeys + x * D;   // all 512 columns: the allocation starts at 0
     const uint32_t sQ = smem_u32(smem) + x * S::kTileBytes, sR = smem_u32(smem) + S::kRing;
@@ -587,9 +636,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     commit(&drain[x]);
     if (lane == 0) spin_wait(&drain[x], 0);
     __syncwarp();
+    } else if (kCodes && warp >= kSoftWarps + 4) {
+    // ------------------------------------------------------------ codes to operands
+    // A tile at a time, four of its sixteen groups of 8 keys per warp.  Whether
+    // to go on is agreed at the barrier, which every warp reaches within the
+    // limit of its wait.
+    constexpr int kPieces = D / 64;               // 16-byte pieces of a lane per group
+    const int cw = warp - kSoftWarps - 4;
+    auto agree = [&](bool mine) {
+      uint32_t all;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.and.pred p, 1, %2, q;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(all)
+          : "r"(mine ? 1u : 0u), "n"(kCodeWarps * 32)
+          : "memory");
+      return all != 0;
+    };
+    uint32_t kv = 0, ni = 0;
+    bool ok = true;
+    while (ok) {
+      const int slot = ni % kItems;
+      ok = agree(warp_spin(&it_full[slot], (ni / kItems) & 1) && !*(volatile int*)abort_flag);
+      if (!ok) break;
+      const int row0 = ring[slot].row0, n = max(ring[slot].n[0], ring[slot].n[1]);
+      const int left = ring[slot].len - ring[slot].b0 * kKeys;       // keys from the first block on
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      ++ni;
+      if (row0 < 0) break;
+#pragma unroll 1
+      for (int j = 0; j < 2 * n && ok; ++j, ++kv) {
+        const int s = kv % NS;
+        const bool value = j & 1;
+        const uint32_t tile = smem_u32(smem) + S::kRing + s * S::kTileBytes, codes = tile + S::kTileBytes / 2;
+        // this lane's piece of a group: row and 16 elements of it
+        constexpr int kRowPieces = D / 16;
+        const int r0 = lane / kRowPieces, c = lane % kRowPieces;
+        const bool got = warp_spin(&code_full[s], (kv / NS) & 1);
+        uint4 raw[4][kPieces];
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+            raw[g][i] = lds4(code_at<D>(codes, (cw * 4 + g) * 8 + r0 + i * (32 / kRowPieces), c * 16));
+        ok = agree(got);
+        if (!ok) break;
+        const float2* sc = scales + (kv / 2) % kScaleSlots * kScaleBlocks;
+        const int tail = left - (j / 2) * kKeys;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const float f = kF16 || value ? 1.0f : exp2i(scale_exp(sc[cw * 2 + g / 2].x));
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int rr = r0 + i * (32 / kRowPieces);
+            // values past the end: a weight of 0 does not silence what other data, or NaN, is there
+            const bool none = value && (cw * 4 + g) * 8 + rr >= tail;
+            const uint32_t w[4] = {raw[g][i].x, raw[g][i].y, raw[g][i].z, raw[g][i].w};
+            uint32_t e[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = none ? 0u : w[k];
+              e[2 * k] = codes2<0>(x), e[2 * k + 1] = codes2<1>(x);
+            }
+            if (!kF16 && !value) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float2 v = half2_floats(e[k]);
+                e[k] = pack2<false>(v.x * f, v.y * f);
+              }
+            }
+            const uint32_t to = tile + (cw * 4 + g) * S::kGroup + (c / 4) * 1024 + rr * 128;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (((2 * c + k) % 8) ^ rr) * 16),
+                           "r"(e[4 * k]), "r"(e[4 * k + 1]), "r"(e[4 * k + 2]), "r"(e[4 * k + 3])
+                           : "memory");
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(abort_flag, 1);
+    __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs<kCodes>));
     // ------------------------------------------------------------ softmax, epilogue
     const int x = warp >> 2;                                   // tile
     const int row = (warp & 3) * 32 + lane;                    // row of the tile
@@ -628,6 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
         const int b = it.b0 + j;
         const uint64_t c2 = pair(t.c, t.c);
+        const float2* sc = scales + (kv0 / 2 + j) % kScaleSlots * kScaleBlocks;
+        // codes: of 16 keys, the factor of their logits and the exponent of their values' scale
+        auto factor = [&](int i) { return kF16 ? t.c * exp2i(scale_exp(sc[i].x)) : t.c; };
         auto arrive = [&](int half) {
           tmem_wait_st();
           tc_fence_before();
@@ -652,13 +789,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * t.c : -INFINITY);
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * (kCodes ? factor(0) : t.c) : -INFINITY);
+          if (kCodes) top += (float)scale_exp(sc[0].y);
           if (m == -INFINITY) m = top;
           unset = __any_sync(0xffffffffu, live && m == -INFINITY);
         }
-        // 64 logits to P with the scale in use; the sum
-        auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32]) {
+        // 64 logits to P with the scale in use; the sum (and into `grown` that
+        // of the weights without their values' scales)
+        float grown = 0.f;
+        auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32], int half) {
           const float off = m == -INFINITY ? 0.f : -m;
+          if (kCodes) {
+            float all = 0.f;
+            grown = 0.f;
+#pragma unroll
+            for (int i = 0; i < kHalf / 16; ++i) {
+              const int e = scale_exp(sc[half * (kHalf / 16) + i].y);
+              const float f = factor(half * (kHalf / 16) + i), o = off + (float)e;
+              const uint64_t f2 = pair(f, f), o2 = pair(o, o);
+              uint64_t sum[2] = {0, 0};
+#pragma unroll
+              for (int k = 8 * i; k < 8 * i + 8; ++k) {
+                const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), f2, o2);
+                const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
+                sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+                p[k] = pack2<kP16>(p0, p1);
+              }
+              sum[0] = add2(sum[0], sum[1]);
+              const float part = lo(sum[0]) + hi(sum[0]);
+              all += part;
+              grown = fmaf(part, exp2i(-e), grown);
+            }
+            return all;
+          }
           const uint64_t off2 = pair(off, off);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -681,18 +844,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld64(tS, s0);
           tmem_wait_ld64(s0);
           tmem_ld64(tS + kHalf, s1);        // on its way meanwhile
-          float sum = form(s0, p);
+          float sum = form(s0, p, 0);
           tmem_wait_ld64(s1);
           if (!__any_sync(0xffffffffu, live && sum > kMost)) {
-            l += sum;
+            l += kCodes ? grown : sum;
             tmem_st32(tS, p);
             arrive(0);
             hand_over(0);
-            sum = form(s1, p);
+            sum = form(s1, p, 1);
             slow = 1;
             if (!__any_sync(0xffffffffu, live && sum > kMost)) {
               hand_over(1);
-              l += sum;
+              l += kCodes ? grown : sum;
               tmem_st32(tS + 32, p);
               arrive(1);
               slow = 2;
@@ -705,8 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rare cases written out twice a first block took 3500 cycles.)
         // Rows of V past the keys' end hold other data (or NaN), which a weight
         // of 0 does not silence: clear them (each tile that multiplies them).
+        // (codes: done where they become operands)
         const int tail = it.len - b * kKeys;
-        if (tail < kKeys) {
+        if (!kCodes && tail < kKeys) {
           const uint32_t i = kv0 + 2 * j + 1;
           if (!warp_spin(&kv_full[i % NS], (i / NS) & 1)) { ok = false; break; }
           if (row >= tail) {
@@ -733,13 +897,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             float sum;
 #pragma unroll 1
             for (int pass = 0;; ++pass) {
-              sum = form(s, p);
+              sum = form(s, p, half);
               const bool need = live && (sum > kMost || (m == -INFINITY && lim > from));
               if (pass || !__any_sync(0xffffffffu, need)) break;
               // a new scale for the rows that need one: their maximum
               float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int k = 0; k < kHalf; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k] * t.c);
+              for (int k = 0; k < kHalf; ++k) {
+                if (kCodes) {
+                  const int i = half * (kHalf / 16) + k / 16;
+                  mx[k & 3] = fmaxf(mx[k & 3], fmaf(s[k], factor(i), (float)scale_exp(sc[i].y)));
+                } else {
+                  mx[k & 3] = fmaxf(mx[k & 3], s[k] * t.c);
+                }
+              }
               const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               const bool up = need && top > m;
               const float f = up ? ex2(m - top) : 1.0f;              // m = -inf: 0
@@ -761,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            l += sum;
+            l += kCodes ? grown : sum;
           }
           tmem_st32(tS + half * 32, p);
           hand_over(half);
@@ -896,14 +1067,14 @@ bool out_map(CUtensorMap* m, const AttnArgs& a, float* part_o, int splits) {
                 part_o ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
 }
 
-template <int D, bool kF16, bool kPaged>
+template <int D, bool kF16, bool kPaged, bool kCodes>
 cudaError_t launch(const TcAttnArgs& t, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    const CUtensorMap& o, const Report& rep, int grid, cudaStream_t stream) {
-  auto kern = attn_tc_kernel<D, kF16, kPaged>;
+  auto kern = attn_tc_kernel<D, kF16, kPaged, kCodes>;
   constexpr size_t smem = Shape<D, kPaged>::kSmem;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  kern<<<grid, kThreads, smem, stream>>>(q, k, v, o, t, rep);
+  kern<<<grid, kThreads<kCodes>, smem, stream>>>(q, k, v, o, t, rep);
   return cudaGetLastError();
 }
 
@@ -946,7 +1117,9 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.c = a.scale * 1.4426950408889634f;
   // a scale of 0 (or so small that it would flush): so that a masked logit
   // stays one, and every other still counts as 0
-  if (t.c < 1.2e-38f && t.c > -1.2e-38f) t.c = 1.2e-38f;
+  // (codes: also times the smallest scale)
+  const float least = a.scales ? 1.2e-30f : 1.2e-38f;
+  if (t.c < least && t.c > -least) t.c = least;
   t.hidden = t.c > 0 ? -INFINITY : INFINITY;
   t.part_o = part_o;
   t.part_lse = part_lse;
@@ -957,13 +1130,17 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   // (parts of all splits are one tensor of splits * T tokens)
   t.out_box = 32 % box_heads(a) == 0 && (long long)a.T * splits < (1ll << 31);
   if (t.out_box && !out_map(&o, a, part_o, splits)) return cudaErrorInvalidValue;
-  if (paged ? !pages_map(&k, a.k_cache, a, t.box) || !pages_map(&v, a.v_cache, a, t.box)
+  const bool codes = a.scales != nullptr;
+  if (codes ? !codes_map(&k, a.k_cache, a, t.box) || !codes_map(&v, a.v_cache, a, t.box)
+      : paged ? !pages_map(&k, a.k_cache, a, t.box) || !pages_map(&v, a.v_cache, a, t.box)
             : !rows_map(&k, a.k, a, a.Tk, a.Hkv, kKeys) || !rows_map(&v, a.v, a, a.Tk, a.Hkv, kKeys))
     return cudaErrorInvalidValue;
   Report rep = shape;
   rep.blocks[rep.set] = items;
 #define TC_CASE(DD, F, P) \
-  if (a.D == DD && (a.f16 != 0) == F && paged == P) return launch<DD, F, P>(t, q, k, v, o, rep, items, stream);
+  if (a.D == DD && (a.f16 != 0) == F && paged == P)                                     \
+    return codes ? launch<DD, F, P, P>(t, q, k, v, o, rep, items, stream)              \
+                 : launch<DD, F, P, false>(t, q, k, v, o, rep, items, stream);
   TC_CASE(64, false, false)
   TC_CASE(64, false, true)
   TC_CASE(64, true, false)
