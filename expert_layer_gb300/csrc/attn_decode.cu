@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = (int)(top >> 7) - 127;   // an infinity or NaN: as it is
-        const int up = top == 0 || e == 128 ? 0 : min(14 - e, 60);
+        const int up = top == 0 || e == 128 ? 0 : min(14 - e, 126);
         const float f = exp2i(up);
         unit_c[rs] *= exp2i(-up);
 #pragma unroll

@@ -1117,8 +1117,8 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.c = a.scale * 1.4426950408889634f;
   // a scale of 0 (or so small that it would flush): so that a masked logit
   // stays one, and every other still counts as 0
-  // (codes: also times the smallest scale)
-  const float least = a.scales ? 1.2e-30f : 1.2e-38f;
+  // (f16 and codes: also times the smallest scale; f16 products stay below 4e9)
+  const float least = a.scales && a.f16 ? 1.2e-30f : 1.2e-38f;
   if (t.c < least && t.c > -least) t.c = least;
   t.hidden = t.c > 0 ? -INFINITY : INFINITY;
   t.part_o = part_o;
