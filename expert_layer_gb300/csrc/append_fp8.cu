@@ -109,7 +109,8 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
   const long long items = 2ll * slots * a.Hkv, warps = (long long)blocks * kWarps;
   const long long each = (items + warps - 1) / warps;
   const long long i0 = ((long long)block * kWarps + warp) * each, i1 = min(items, i0 + each);
-  int seen = -1, q0 = 0, len = 0, fresh = 0, first = 0, page = -1;   // of the slot in use
+  int seen = -1, q0 = 0, len = 0, fresh = 0, first = -1;             // of the slot in use
+  const int32_t* list = nullptr;
 #pragma unroll 1
   for (long long i = i0; i < i1; ++i) {
     const int slot = i >> 31 ? (int)(i / (2 * a.Hkv)) : f.by_Hkv2.of((int)i);
@@ -121,39 +122,37 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
       q0 = f.q_starts[s];
       const int q1 = f.q_starts[s + 1];
       len = f.kv_lens[s];
-      page = -1;
+      list = f.page_table + (long long)s * f.table_pages;
+      first = -1;
       if (q0 >= 0 && q1 > q0 && q1 <= a.T && len >= q1 - q0 && len <= room) {
         fresh = len - (q1 - q0);                       // the first new token
         const long long b = (long long)(fresh / kScaleBlock) + slot - slot_base(f, s);
-        if (b >= 0 && b * kScaleBlock < len) {         // (a slot that the sequence does not need)
-          first = (int)b * kScaleBlock;
-          page = f.page_table[(long long)s * f.table_pages + (first >> a.page_shift)];
-          if ((unsigned)page >= (unsigned)a.pages) bad = true, page = -1;
-        }
+        if (b >= 0 && b * kScaleBlock < len) first = (int)b * kScaleBlock;   // (else a slot that the sequence does not need)
       }
     }
-    if (page < 0) continue;
+    if (first < 0) continue;
+    const int r0 = max(0, fresh - first), r1 = min(kScaleBlock, len - first);      // the new rows
+    const int p0 = r0 / kRows, p1 = (r1 + kRows - 1) / kRows;
     // --- the rows as they were loaded
     const Heads& src = value ? a.v : a.k;
     const uint16_t* in = src.data + head * src.head;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {                  // rows that are not there are zeros
-      const int tok = first + p * kRows + sub;
-      const bool there = tok >= fresh && tok < len;
-      const uint16_t* row = in + (there ? (long long)(q0 + tok - fresh) * src.tok : 0);
+#pragma unroll 1
+    for (int p = p0; p < p1; ++p) {                      // rows that are not there are zeros
+      const int r = p * kRows + sub;
+      const bool there = r >= r0 && r < r1;
+      const uint16_t* row = in + (there ? (long long)(q0 + first + r - fresh) * src.tok : 0);
       load8(&rows_of[warp][p][0][lane], row + at.o1, there);
       load8(&rows_of[warp][p][1][lane], row + at.o2, there);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    const int page = list[first >> a.page_shift];
     // positions: lane r has those of row r
     Places mine;
     bool placed = true;
     {
-      const int tok = first + lane;
-      const bool live = !value && lane < kScaleBlock && tok >= fresh && tok < len;
 #pragma unroll
       for (int x = 0; x < kMaxAxes; ++x) mine.p[x] = 0;
-      if (live) placed = mine.load(a, axes, q0 + tok - fresh);
+      if (!value && lane >= r0 && lane < r1) placed = mine.load(a, axes, q0 + first + lane - fresh);
       if (!placed) {
         bad = true;
 #pragma unroll
@@ -161,11 +160,15 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
       }
     }
     const uint32_t lost = __ballot_sync(0xffffffffu, !placed);     // rows that are not written
+    if ((unsigned)page >= (unsigned)a.pages) {
+      bad = true;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      continue;
+    }
     const long long at_row = (((long long)page * a.Hkv + head) << a.page_shift) + (first & ((1 << a.page_shift) - 1));
     uint8_t* codes = (value ? f.v_codes : f.k_codes) + at_row * D;
     float* scale = f.scales + (at_row / kScaleBlock) * 2 + (value ? 1 : 0);
-    const int before = max(0, fresh - first);                      // rows of before
-    const int old = before > 0 ? scale_exp(*scale) : kScaleMin;
+    const int old = r0 > 0 ? scale_exp(*scale) : kScaleMin;        // rows of before
     auto row_values = [&](int p, uint64_t (&y)[kPart]) {
       Part raw[2];
 #pragma unroll
@@ -188,7 +191,7 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
     asm volatile("cp.async.wait_all;" ::: "memory");
     float top = 0.f;
 #pragma unroll 2
-    for (int p = 0; p < kPasses; ++p) {
+    for (int p = p0; p < p1; ++p) {
       uint64_t y[kPart];
       row_values(p, y);
 #pragma unroll
@@ -199,18 +202,18 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
     const int e = max(needed_exp(top), old);
     const uint64_t to = pair(exp2i(-e), exp2i(-e));
 #pragma unroll 2
-    for (int p = 0; p < kPasses; ++p) {
+    for (int p = p0; p < p1; ++p) {
       uint64_t y[kPart];
       row_values(p, y);
-      const int r = p * kRows + sub, tok = first + r;
-      if (tok < fresh || tok >= len || ((lost >> r) & 1)) continue;
+      const int r = p * kRows + sub;
+      if (r < r0 || r >= r1 || ((lost >> r) & 1)) continue;
       uint8_t* dst = codes + r * D;
       *reinterpret_cast<uint32_t*>(dst + at.o1) = to_codes(mul2(y[0], to), mul2(y[1], to));
       *reinterpret_cast<uint32_t*>(dst + at.o2) = to_codes(mul2(y[2], to), mul2(y[3], to));
     }
-    if (before > 0 && e > old) {
+    if (e > old) {
       const float g = exp2i(old - e);
-      for (int r = sub; r < before; r += kRows) {
+      for (int r = sub; r < r0; r += kRows) {
         uint2* w = reinterpret_cast<uint2*>(codes + r * D + (lane % kLanes) * 8);
         const uint2 v = *w;
         *w = make_uint2(rescaled(v.x, g), rescaled(v.y, g));
@@ -225,9 +228,10 @@ template <int D, int kHeads, bool kF16, bool kInter>
 __global__ void __launch_bounds__(kThreads, kResident)
     append_fp8_kernel(const RopeFp8Args f, const Report rep) {
   const bool axes = f.r.axes != nullptr;
-  const bool bad = (int)blockIdx.x < f.q_blocks
-                       ? rope_rows<D, kHeads, kF16, kInter, false>(f.r, axes, blockIdx.x, f.q_blocks)
-                       : append_blocks<D, kF16, kInter>(f, axes, blockIdx.x - f.q_blocks, gridDim.x - f.q_blocks);
+  const bool bad = (int)blockIdx.x < f.kv_blocks
+                       ? append_blocks<D, kF16, kInter>(f, axes, blockIdx.x, f.kv_blocks)
+                       : rope_rows<D, kHeads, kF16, kInter, false>(f.r, axes, blockIdx.x - f.kv_blocks,
+                                                                   gridDim.x - f.kv_blocks);
   const int any = __syncthreads_or(bad);
   if (threadIdx.x == 0) report(rep, blockIdx.x, any ? kStatusBounds : 0);
 }
@@ -243,14 +247,14 @@ cudaError_t launch(RopeFp8Args f, void* ws, int num_sms, cudaStream_t stream) {
   f.by_Hkv2.set(2 * a.Hkv);
   const long long q = ((long long)a.T * a.chunks + kGroups - 1) / kGroups;
   const long long kv = ((f.by_token ? a.T : by16) * 2 * a.Hkv + kWarps - 1) / kWarps;
-  const long long most = (long long)num_sms * kResident < kFlagsFirst ? (long long)num_sms * kResident : kFlagsFirst;
-  long long nq = q, nkv = kv;
-  if (q + kv > most) {          // shares by what the two read and write: 4 D bytes a row, 3 D
-    nkv = most * (6ll * a.Hkv) / (4ll * a.Hq + 6ll * a.Hkv);
-    nkv = nkv < 1 ? 1 : nkv > kv ? kv : nkv;
-    nq = most - nkv < q ? most - nkv : q;
-  }
-  f.q_blocks = (int)nq;
+  // k and v first, a warp for each scale block as far as the report's words go:
+  // a block of them is a chain of loads, which the rows of q then cover (with
+  // shares of one round of blocks by what is read, three or more scale blocks
+  // to a warp, 256 tokens took 19.0 us, 8 prompts of 1000 56.6)
+  const long long most = (long long)num_sms * kResident;
+  const long long nq = q < most ? q : most < kFlagsFirst / 2 ? most : kFlagsFirst / 2;
+  const long long nkv = kv < kFlagsFirst - nq ? kv : kFlagsFirst - nq;
+  f.kv_blocks = (int)nkv;
   const int grid = (int)(nq + nkv);
   const Report rep{ws, 0, {grid, 0}};
   auto kern = a.interleaved ? append_fp8_kernel<D, kHeads, kF16, true> : append_fp8_kernel<D, kHeads, kF16, false>;

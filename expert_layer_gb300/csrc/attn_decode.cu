@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += scan[w];
   }
   before += incl - mine;
-  const Line line(total, gridDim.x, t.few, t.head);
+  const Line line(total, gridDim.x, t.few, kCodes && t.few > 0 ? beside_head(total, gridDim.x, t.few, t.head) : t.head);
   const int start = line.at(blockIdx.x * kWarps), end = line.at((blockIdx.x + 1) * kWarps);
   const bool work = (int)blockIdx.x < line.blocks && start < end;
   if (work && start >= before && start < before + mine) {

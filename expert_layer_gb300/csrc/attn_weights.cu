@@ -118,8 +118,10 @@ __global__ void __launch_bounds__(kThreads, kResident) attn_weights_kernel(const
     int tiles = tiles_of(v, G), units = (v.len + kUnit - 1) / kUnit;
     // a unit belongs to the warp whose range holds its first place
     long long u = (begin - at + tiles + kUnitCost - 1) / (tiles + kUnitCost);
-#pragma unroll 1
-    while (true) {
+    // the unit after, and its pages, while one is computed
+    bool more = true;
+    int pages[kTiles];
+    auto fetch = [&]() {
       while (u >= (long long)units * a.Hkv) {      // to the next sequence with units
         if (++s >= a.n_seq) break;
         at += (long long)units * a.Hkv * (tiles + kUnitCost);
@@ -128,14 +130,28 @@ __global__ void __launch_bounds__(kThreads, kResident) attn_weights_kernel(const
         units = v.n ? (v.len + kUnit - 1) / kUnit : 0;
         u = 0;
       }
-      if (s >= a.n_seq || at + u * (tiles + kUnitCost) >= end) break;
-      const int head = (int)(u / units), k0 = (int)(u - (long long)head * units) * kUnit;
+      more = s < a.n_seq && at + u * (tiles + kUnitCost) < end;
+      if (!more) return;
+      const int k = (int)(u % units) * kUnit + gq;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+        pages[i] = k + 8 * i < v.len ? a.page_table[(long long)s * a.table_pages + ((k + 8 * i) >> a.page_shift)] : 0;
+    };
+    fetch();
+    uint32_t qf[2][kLoads][4];
+    float off[2];
+    int last[2];                                   // last key that a row sees
+    int held = -1;                                 // the only row tile of this unit's sequence and head is in hand
+#pragma unroll 1
+    while (more) {
+      const int seq = s, head = (int)(u / units), k0 = (int)(u - (long long)head * units) * kUnit, rowtiles = tiles;
+      const Seq cur = v;
       // --- the keys: those past the end are not read
       uint32_t kf[kTiles][kLoads][4];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
         const int key = k0 + 8 * i + gq;
-        int page = key < v.len ? a.page_table[(long long)s * a.table_pages + (key >> a.page_shift)] : 0;
+        int page = pages[i];
         if ((unsigned)page >= (unsigned)a.pages) bad = true, page = 0;
         const long long row =
             (((long long)page * a.Hkv + head) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
@@ -143,40 +159,42 @@ __global__ void __launch_bounds__(kThreads, kResident) attn_weights_kernel(const
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (key < v.len) w = ldg_nc_v4(src + x);
+          if (key < cur.len) w = ldg_nc_v4(src + x);
           kf[i][x][0] = w.x, kf[i][x][1] = w.y, kf[i][x][2] = w.z, kf[i][x][3] = w.w;
         }
       }
+      ++u;
+      fetch();
       // --- the rows that see any of them
-      const int shift = v.len - v.n;               // causal: token i sees the keys up to i + shift
+      const int shift = cur.len - cur.n;           // causal: token i sees the keys up to i + shift
       const int first = a.causal ? max(0, k0 - shift) : 0;
-      const int rows = v.n * G;
+      const int rows = cur.n * G;
       float sum[kTiles][2];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) sum[i][0] = sum[i][1] = 0.f;
 #pragma unroll 1
-      for (int t = (int)((long long)first * G / 16); t < tiles; ++t) {
-        uint32_t qf[2][kLoads][4];
-        float off[2];
-        int last[2];                               // last key that the row sees, from k0
+      for (int t = (int)((long long)first * G / 16); t < rowtiles; ++t) {
+        if (rowtiles > 1 || held != seq * a.Hkv + head) {
+          held = rowtiles > 1 ? -1 : seq * a.Hkv + head;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = 16 * t + 8 * x + gq;
-          const bool live = r < rows;
-          const int i = a.by_G.of(live ? r : 0), h = head * G + (live ? r : 0) - i * G;
-          const uint16_t* src = a.q.data + (v.q0 + i) * a.q.tok + h * a.q.head + quad * (D / 4);
-          const float l = live ? a.lse[(long long)(v.q0 + i) * a.Hq + h] : -INFINITY;
-          // a row without keys, and one that is not there, give nothing
-          off[x] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-          last[x] = (a.causal ? min(i + shift, v.len - 1) : v.len - 1) - k0;
+          for (int x = 0; x < 2; ++x) {
+            const int r = 16 * t + 8 * x + gq;
+            const bool live = r < rows;
+            const int i = a.by_G.of(live ? r : 0), h = head * G + (live ? r : 0) - i * G;
+            const uint16_t* src = a.q.data + (cur.q0 + i) * a.q.tok + h * a.q.head + quad * (D / 4);
+            const float l = live ? a.lse[(long long)(cur.q0 + i) * a.Hq + h] : -INFINITY;
+            // a row without keys, and one that is not there, give nothing
+            off[x] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+            last[x] = a.causal ? min(i + shift, cur.len - 1) : cur.len - 1;
 #pragma unroll
-          for (int y = 0; y < kLoads; ++y) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live) w = *(reinterpret_cast<const uint4*>(src) + y);
-            qf[x][y][0] = w.x, qf[x][y][1] = w.y, qf[x][y][2] = w.z, qf[x][y][3] = w.w;
+            for (int y = 0; y < kLoads; ++y) {
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (live) w = *(reinterpret_cast<const uint4*>(src) + y);
+              qf[x][y][0] = w.x, qf[x][y][1] = w.y, qf[x][y][2] = w.z, qf[x][y][3] = w.w;
+            }
           }
         }
-        const bool whole = __all_sync(0xffffffffu, last[0] >= kUnit - 1 && last[1] >= kUnit - 1);
+        const bool whole = __all_sync(0xffffffffu, last[0] >= k0 + kUnit - 1 && last[1] >= k0 + kUnit - 1);
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
           float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, kResident) attn_weights_kernel(const
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int x = y >> 1, key = 8 * i + 2 * quad + (y & 1);
+            const int x = y >> 1, key = k0 + 8 * i + 2 * quad + (y & 1);
             float e = ex2(fmaf(c[y], a.c, off[x]));
             if (off[x] == -INFINITY || (!whole && key > last[x])) e = 0.f;
             sum[i][y & 1] += e;
@@ -207,11 +225,10 @@ __global__ void __launch_bounds__(kThreads, kResident) attn_weights_kernel(const
           if (gq == 2 * i + y) add = e;
         }
       const int key = k0 + 8 * (gq >> 1) + 2 * quad + (gq & 1);
-      if (key < v.len) {
-        float* w = a.weights + ((long long)s * a.Hkv + head) * a.capacity + key;
+      if (key < cur.len) {
+        float* w = a.weights + ((long long)seq * a.Hkv + head) * a.capacity + key;
         *w += add;
       }
-      ++u;
     }
   }
   const int any = __syncthreads_or(bad);
