@@ -48,7 +48,7 @@ struct Shape {
   static constexpr int kTileBytes = kCodes ? kSlice * D : 2 * kGroup;   // K or V of a slice
   static constexpr int kStageBytes = 2 * kTileBytes;
   // slices in flight per warp
-  static constexpr int kStages = kCodes ? (D == 64 ? 8 : kWide ? 4 : 5) : D == 64 ? 5 : kWide ? 2 : 3;
+  static constexpr int kStages = kCodes ? (D == 64 ? 8 : 4) : D == 64 ? 5 : kWide ? 2 : 3;
   static constexpr int kRing = kStages * kStageBytes;              // of one warp
   static constexpr int kPart = kRows * D * 4;                      // O of one unit
   static_assert(kPart <= kRing, "a warp's last part takes the place of its ring");
@@ -106,6 +106,12 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t transposed(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
+}
+
 __device__ __forceinline__ int seq_len(const AttnArgs& a, int b) {
   const int n = a.kv_lens[b];
   return n < 0 || n > ((long long)a.table_pages << a.page_shift) ? 0 : n;
@@ -142,9 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const DecodeArgs t, const Report rep) {
   using S = Shape<D, kWide, kCodes>;
-  constexpr bool kP16 = kF16 || kCodes;              // operands of the products: f16 (else bf16)
-  constexpr int kCols = D / 8;                       // codes: elements of a column of a fragment
   constexpr int kRowSets = kWide ? 2 : 1;            // rows g and (wide) g + 8 of a thread
+  // Heads that a thread has the statistics and parts of O of: those rows; with
+  // codes, whose products have the heads as columns, 2q, 2q + 1 and (wide) 8 more
+  constexpr int kSets = kCodes ? 2 * kRowSets : kRowSets;
+  constexpr int kCols = D / 8;                       // codes: consecutive elements of O that a thread has of a head
+  constexpr int kTiles = kCodes ? kRowSets * kCols / 2 : D / 8;
   constexpr int kStages = S::kStages;
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
   float2* stats = reinterpret_cast<float2*>(smem + S::kStats);         // [warp][part][row]: m, l
@@ -256,7 +265,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     fetch();
     auto issue = [&]() {
       if (!more) return;
-      if (lane == 0) {
+      if constexpr (kCodes) {
+        // (what one lane does while the others wait is kept short)
+        const bool there = (unsigned)page < (unsigned)a.pages;
+        bad |= !there;
+        const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
+        const int at = (there ? page : 0) * a.Hkv + (t.chunks == 1 ? ld.u : ld.u / t.chunks);
+        const float* from = a.scales + 2 * (((long long)at << (a.page_shift - 4)) + (row >> 4));
+        unsigned char* dst = ring + st * S::kStageBytes;
+        if (lane == 0) {
+          mbar_expect_tx(&bars[st], S::kStageBytes);
+          tma_load_3d(dst, &tmK, 0, row, at, &bars[st]);
+          tma_load_3d(dst + S::kTileBytes, &tmV, 0, row, at, &bars[st]);
+          asm volatile(
+              "cp.async.ca.shared.global [%0], [%1], 8;\n"
+              "cp.async.mbarrier.arrive.noinc.shared.b64 [%2];" ::"r"(smem_u32(&scales[st])),
+              "l"(from), "r"(smem_u32(&bars[st]))
+              : "memory");
+        }
+      } else if (lane == 0) {
         if ((unsigned)page >= (unsigned)a.pages) {
           bad = true;
           page = 0;
@@ -265,19 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
         unsigned char* dst = ring + st * S::kStageBytes;
         mbar_expect_tx(&bars[st], S::kStageBytes);
-        if (kCodes) {
-          tma_load_3d(dst, &tmK, 0, row, page * a.Hkv + hk, &bars[st]);
-          tma_load_3d(dst + S::kTileBytes, &tmV, 0, row, page * a.Hkv + hk, &bars[st]);
-          const long long block = ((((long long)page * a.Hkv + hk) << a.page_shift) + row) / kScaleBlock;
-          asm volatile(
-              "cp.async.ca.shared.global [%0], [%1], 8;\n"
-              "cp.async.mbarrier.arrive.noinc.shared.b64 [%2];" ::"r"(smem_u32(&scales[st])),
-              "l"(a.scales + 2 * block), "r"(smem_u32(&bars[st]))
-              : "memory");
-        } else {
-          tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
-          tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
-        }
+        tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+        tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
       }
       ++issued;
       ++ld_slice;
@@ -292,6 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v_row = (lane & 7) + (lane & 8), v_col = lane >> 4;
     const int k_at = (k_row >> 3) * S::kGroup + (k_row & 7) * 128, v_at = (v_row >> 3) * S::kGroup + (v_row & 7) * 128;
     const int quad = lane & 3, gq = lane >> 2;
+    // codes: where this lane's pieces of a slice are
+    uint32_t k_off[2][D / 64], v_off[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) k_off[h][i] = code_at<D>(0, gq + 8 * h, quad * (D / 4) + 16 * i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v_off[k] = code_at<D>(0, 2 * quad + (k & 1) + 8 * (k >> 1), gq * kCols);
     uint32_t used = 0;
     auto load_q = [&](const Cursor& c, uint32_t (&q)[D / 16][2 * kRowSets]) {
       const int hk = t.chunks == 1 ? c.u : c.u / t.chunks;
@@ -322,33 +346,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // inverse joins the scale of its logits.  (Exact for elements down to 2^-28
     // of the largest, and the rest, rounded to a 2^-39th of it, is below what
     // fp32 sums keep.)
-    float unit_c[kRowSets];
+    float unit_c[kSets];
     auto settle_q = [&](uint32_t (&q)[D / 16][2 * kRowSets]) {
 #pragma unroll
-      for (int rs = 0; rs < kRowSets; ++rs) {
-        unit_c[rs] = t.c;
-        if (kF16 || !kCodes) continue;
-        uint32_t top = 0;                      // largest magnitude, as bits
+      for (int x = 0; x < kSets; ++x) unit_c[x] = t.c;
+      if constexpr (kCodes && !kF16) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+        for (int rs = 0; rs < kRowSets; ++rs) {
+          uint32_t top = 0;                      // largest magnitude, as bits
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w = q[kk][j * kRowSets + rs] & 0x7fff7fffu;
-            top = max(top, max(w >> 16, w & 0xffffu));
-          }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = (int)(top >> 7) - 127;   // an infinity or NaN: as it is
-        const int up = top == 0 || e == 128 ? 0 : min(14 - e, 126);
-        const float f = exp2i(up);
-        unit_c[rs] *= exp2i(-up);
+          for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = q[kk][j * kRowSets + rs] & 0x7fff7fffu;
+              top = max(top, max(w >> 16, w & 0xffffu));
+            }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = (int)(top >> 7) - 127;   // an infinity or NaN: as it is
+          const int up = top == 0 || e == 128 ? 0 : min(14 - e, 126);
+          const float f = exp2i(up);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t& w = q[kk][j * kRowSets + rs];
-            w = pack2<true>(bf16lo(w) * f, bf16hi(w) * f);
-          }
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t& w = q[kk][j * kRowSets + rs];
+              w = pack2<true>(bf16lo(w) * f, bf16hi(w) * f);
+            }
+          // (row gq + 8 rs of a fragment: the thread's heads are 2 quad + {0, 1})
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            unit_c[(2 * rs + j) % kSets] *= exp2i(-__shfl_sync(0xffffffffu, up, 4 * (2 * quad + j)));
+        }
       }
     };
     uint32_t q[D / 16][2 * kRowSets];
@@ -361,14 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       advance(lens, nxt, units);
       uint32_t qn[D / 16][2 * kRowSets];             // the next unit's, under way meanwhile
       if (!kWide && nxt.pos < we) load_q(nxt, qn);
-      float o[D / 8][4];
-      float m[kRowSets], l[kRowSets];
+      float o[kTiles][4];
+      float m[kSets], l[kSets];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 #pragma unroll
-      for (int rs = 0; rs < kRowSets; ++rs) m[rs] = -INFINITY, l[rs] = 0.f;
+      for (int rs = 0; rs < kSets; ++rs) m[rs] = -INFINITY, l[rs] = 0.f;
 
 #pragma unroll 1
       for (int s = first; s < last; ++s) {
@@ -377,37 +406,115 @@ __global__ void __launch_bounds__(kThreads, 1)
         // landed must not be loaded again, nor its barrier be armed again
         if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true, more = false;
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        float slice_c[kRowSets], shift = 0.f, back = 1.0f;
-#pragma unroll
-        for (int rs = 0; rs < kRowSets; ++rs) slice_c[rs] = unit_c[rs];
-        if (kCodes) {
-          // logits times the keys' scale; the values' scale 2^e joins the
-          // exponent of the weights (P of the second product), l takes it back
+        const int valid = cur.len - s * kSlice;
+        if constexpr (kCodes) {
+          // S' = K Q': a thread has keys gq, gq + 8 of heads 2 quad + {0, 1} (+ 8).
+          // Logits times the keys' scale; the values' scale 2^e joins the exponent
+          // of the weights (P of the second product), l takes it back
           const float2 f = scales[st];
           const int ev = scale_exp(f.y);
-          const float fk = exp2i(scale_exp(f.x));
-          shift = (float)ev;
-          back = exp2i(-ev);
+          const float fk = exp2i(scale_exp(f.x)), shift = (float)ev, back = exp2i(-ev);
+          float slice_c[kSets];
 #pragma unroll
-          for (int rs = 0; rs < kRowSets; ++rs) slice_c[rs] = fmaxf(unit_c[rs] * fk, 1.2e-38f);
+          for (int x = 0; x < kSets; ++x) slice_c[x] = fmaxf(unit_c[x] * fk, 1.2e-38f);
           uint32_t w[2][D / 16];
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
-              const uint4 x = lds4(code_at<D>(kb, gq + 8 * h, quad * (D / 4) + 16 * i));
+              const uint4 x = lds4(kb + k_off[h][i]);
               w[h][4 * i] = x.x, w[h][4 * i + 1] = x.y, w[h][4 * i + 2] = x.z, w[h][4 * i + 3] = x.w;
             }
+          float sc[kRowSets][2][4];                  // two chains of products
+#pragma unroll
+          for (int i = 0; i < kRowSets * 8; ++i) sc[i / 8][i / 4 % 2][i % 4] = 0.f;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t a1 = kWide ? q[kk][kRowSets - 1] : 0u, a3 = kWide ? q[kk][2 * kRowSets - 1] : 0u;
-            mma<true>(sc[0], q[kk][0], a1, q[kk][kRowSets], a3, codes2<0>(w[0][kk]), codes2<1>(w[0][kk]));
-            mma<true>(sc[1], q[kk][0], a1, q[kk][kRowSets], a3, codes2<0>(w[1][kk]), codes2<1>(w[1][kk]));
-          }
-        }
+            const uint32_t a0 = codes2<0>(w[0][kk]), a1 = codes2<0>(w[1][kk]), a2 = codes2<1>(w[0][kk]),
+                           a3 = codes2<1>(w[1][kk]);
 #pragma unroll
-        for (int kk = 0; kk < (kCodes ? 0 : D / 16); ++kk) {
+            for (int rs = 0; rs < kRowSets; ++rs) mma<true>(sc[rs][kk & 1], a0, a1, a2, a3, q[kk][rs], q[kk][kRowSets + rs]);
+          }
+          // the values meanwhile: keys 2 quad + {0, 1, 8, 9}, the D / 8 from gq D / 8 on
+          uint32_t wv[4][D / 32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (D == 128) {
+              const uint4 x = lds4(vb + v_off[k]);
+              wv[k][0] = x.x, wv[k][1] = x.y, wv[k][D / 32 - 2] = x.z, wv[k][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = lds2(vb + v_off[k]);
+              wv[k][0] = x.x, wv[k][1] = x.y;
+            }
+          float y[kSets][2];                         // of the two keys
+#pragma unroll
+          for (int x = 0; x < kSets; ++x)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) y[x][h] = sc[x / 2][0][2 * h + x % 2] + sc[x / 2][1][2 * h + x % 2];
+          if (valid < kSlice) {
+            // codes past the end may be anything: a weight of 0 does not silence NaN
+#pragma unroll
+            for (int x = 0; x < kSets; ++x) {
+              if (gq >= valid) y[x][0] = -INFINITY;
+              if (gq + 8 >= valid) y[x][1] = -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (2 * quad + (k & 1) + 8 * (k >> 1) >= valid)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) wv[k][i] = 0;
+          }
+          bool up = false;
+#pragma unroll
+          for (int x = 0; x < kSets; ++x) up |= fmaf(fmaxf(y[x][0], y[x][1]), slice_c[x], shift) > m[x] + kLag;
+          if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+            for (int x = 0; x < kSets; ++x) {
+              float top = fmaxf(y[x][0], y[x][1]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              top = fmaf(top, slice_c[x], shift);
+              const bool g = top > m[x] + kLag;
+              const float f = g ? ex2(m[x] - top) : 1.0f;
+              if (g) m[x] = top;
+              l[x] *= f;
+#pragma unroll
+              for (int i = 0; i < kCols / 2; ++i) {
+                o[x / 2 * (kCols / 2) + i][x % 2] *= f;
+                o[x / 2 * (kCols / 2) + i][2 + x % 2] *= f;
+              }
+            }
+          }
+          uint32_t p[kRowSets][2];
+#pragma unroll
+          for (int x = 0; x < kSets; ++x) {
+            const float off = m[x] == -INFINITY ? 0.f : m[x] - shift;
+            y[x][0] = ex2(fmaf(y[x][0], slice_c[x], -off));
+            y[x][1] = ex2(fmaf(y[x][1], slice_c[x], -off));
+            l[x] = fmaf(y[x][0] + y[x][1], back, l[x]);
+          }
+          // P as the second operand: keys to the rows of a fragment's column
+#pragma unroll
+          for (int rs = 0; rs < kRowSets; ++rs)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) p[rs][h] = transposed(pack2<true>(y[2 * rs % kSets][h], y[(2 * rs + 1) % kSets][h]));
+          // O' += V' P': rows gq and gq + 8 of product i are the thread's elements 2 i and 2 i + 1
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t a01 = __byte_perm(wv[0][i], wv[1][i], 0x5140), a23 = __byte_perm(wv[0][i], wv[1][i], 0x7362);
+            const uint32_t b01 = __byte_perm(wv[2][i], wv[3][i], 0x5140), b23 = __byte_perm(wv[2][i], wv[3][i], 0x7362);
+#pragma unroll
+            for (int rs = 0; rs < kRowSets; ++rs) {
+              float (&o0)[4] = o[(rs * (kCols / 2) + 2 * i) % kTiles];
+              float (&o1)[4] = o[(rs * (kCols / 2) + 2 * i + 1) % kTiles];
+              mma<true>(o0, codes2<0>(a01), codes2<1>(a01), codes2<0>(b01), codes2<1>(b01), p[rs][0], p[rs][1]);
+              mma<true>(o1, codes2<0>(a23), codes2<1>(a23), codes2<0>(b23), codes2<1>(b23), p[rs][0], p[rs][1]);
+            }
+          }
+        } else {
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
           uint32_t r[4];
           const int chunk = (kk & 3) * 2 + k_col;
           ldsm4(kb + (kk >> 2) * 1024 + k_at + ((chunk ^ (k_row & 7)) << 4), r);
@@ -416,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma<kF16>(sc[1], q[kk][0], a1, q[kk][kRowSets], a3, r[2], r[3]);
         }
         // keys of this thread: 2 quad + {0, 1} of each half of the slice
-        const int valid = cur.len - s * kSlice;
         if (valid < kSlice) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -432,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float x = fmaxf(fmaxf(sc[0][2 * rs], sc[0][2 * rs + 1]), fmaxf(sc[1][2 * rs], sc[1][2 * rs + 1]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          top[rs] = kCodes ? fmaf(x, slice_c[rs], shift) : x * t.c;
+          top[rs] = x * t.c;
           up |= top[rs] > m[rs] + kLag;
         }
         if (__any_sync(0xffffffffu, up)) {
@@ -451,14 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int rs = 0; rs < kRowSets; ++rs) {
-          const float off = m[rs] == -INFINITY ? 0.f : kCodes ? m[rs] - shift : m[rs];
-          const float c = kCodes ? slice_c[rs] : t.c;
+          const float off = m[rs] == -INFINITY ? 0.f : m[rs];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = ex2(fmaf(sc[h][2 * rs], c, -off)), p1 = ex2(fmaf(sc[h][2 * rs + 1], c, -off));
-            if (kCodes) l[rs] = fmaf(p0 + p1, back, l[rs]);
-            else l[rs] += p0 + p1;
-            p[2 * h + rs] = pack2<kP16>(p0, p1);
+            const float p0 = ex2(fmaf(sc[h][2 * rs], t.c, -off)), p1 = ex2(fmaf(sc[h][2 * rs + 1], t.c, -off));
+            l[rs] += p0 + p1;
+            p[2 * h + rs] = pack2<kF16>(p0, p1);
           }
         }
         // values past the end may be anything: a weight of 0 does not silence NaN
@@ -468,42 +572,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           keep0 = (k0 < valid ? 0xffffu : 0u) | (k0 + 1 < valid ? 0xffff0000u : 0u);
           keep1 = (k0 + 8 < valid ? 0xffffu : 0u) | (k0 + 9 < valid ? 0xffff0000u : 0u);
         }
-        if (kCodes) {
-          // keys 2 quad + {0, 1, 8, 9}, the D / 8 values from gq D / 8 on: element
-          // i of them is column gq of the i-th product
-          uint32_t w[4][D / 32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int key = 2 * quad + (k & 1) + 8 * (k >> 1);
-            const uint32_t at = code_at<D>(vb, key, gq * kCols);
-            if (D == 128) {
-              const uint4 x = lds4(at);
-              w[k][0] = x.x, w[k][1] = x.y, w[k][D / 32 - 2] = x.z, w[k][D / 32 - 1] = x.w;
-            } else {
-              const uint2 x = lds2(at);
-              w[k][0] = x.x, w[k][1] = x.y;
-            }
-            if (key >= valid)
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) w[k][i] = 0;
-          }
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint32_t a01 = __byte_perm(w[0][i], w[1][i], 0x5140), a23 = __byte_perm(w[0][i], w[1][i], 0x7362);
-            const uint32_t b01 = __byte_perm(w[2][i], w[3][i], 0x5140), b23 = __byte_perm(w[2][i], w[3][i], 0x7362);
-            mma<true>(o[4 * i], p[0], p[1], p[2], p[3], codes2<0>(a01), codes2<0>(b01));
-            mma<true>(o[4 * i + 1], p[0], p[1], p[2], p[3], codes2<1>(a01), codes2<1>(b01));
-            mma<true>(o[4 * i + 2], p[0], p[1], p[2], p[3], codes2<0>(a23), codes2<0>(b23));
-            mma<true>(o[4 * i + 3], p[0], p[1], p[2], p[3], codes2<1>(a23), codes2<1>(b23));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < (kCodes ? 0 : D / 16); ++i) {
+        for (int i = 0; i < D / 16; ++i) {
           uint32_t r[4];
           const int chunk = (i & 3) * 2 + v_col;
           ldsm4_t(vb + (i >> 2) * 1024 + v_at + ((chunk ^ (v_row & 7)) << 4), r);
           mma<kF16>(o[2 * i], p[0], p[1], p[2], p[3], r[0] & keep0, r[1] & keep1);
           mma<kF16>(o[2 * i + 1], p[0], p[1], p[2], p[3], r[2] & keep0, r[3] & keep1);
+        }
         }
         __syncwarp();            // every lane has read the stage
         ++used;
@@ -512,25 +588,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // --- the end of this warp's part of the unit
 #pragma unroll
-      for (int rs = 0; rs < kRowSets; ++rs) {
-        l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 1);
-        l[rs] += __shfl_xor_sync(0xffffffffu, l[rs], 2);
-      }
-      // O of the thread's row times f, to the row at `to`: columns 8 i + 2 quad +
-      // {0, 1}, with codes the D / 8 from 2 quad D / 8 and from (2 quad + 1) D / 8 on
-      auto put_part = [&](float* to, int rs, float f) {
-        if (kCodes) {
+      for (int x = 0; x < kSets; ++x)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+        for (int d = kCodes ? 4 : 1; d < (kCodes ? 32 : 4); d <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
+      // the heads of the thread's sets; one thread of those that have a head writes its statistics
+      auto head_of = [&](int x) { return kCodes ? 8 * (x >> 1) + 2 * quad + (x & 1) : gq + 8 * x; };
+      const bool leader = kCodes ? gq == 0 : quad == 0;
+      // O of a set times f, to the row at `to`
+      auto put_part = [&](float* to, int x, float f) {
+        if constexpr (kCodes) {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 4)
-              *reinterpret_cast<float4*>(to + (2 * quad + j) * kCols + i) =
-                  make_float4(o[i][2 * rs + j] * f, o[i + 1][2 * rs + j] * f, o[i + 2][2 * rs + j] * f,
-                              o[i + 3][2 * rs + j] * f);
+          for (int i = 0; i < kCols; i += 4) {
+            const float (&o0)[4] = o[x / 2 * (kCols / 2) + i / 2], (&o1)[4] = o[x / 2 * (kCols / 2) + i / 2 + 1];
+            *reinterpret_cast<float4*>(to + gq * kCols + i) =
+                make_float4(o0[x % 2] * f, o0[2 + x % 2] * f, o1[x % 2] * f, o1[2 + x % 2] * f);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<float2*>(to + 8 * i + 2 * quad) = make_float2(o[i][2 * rs] * f, o[i][2 * rs + 1] * f);
+            *reinterpret_cast<float2*>(to + 8 * i + 2 * quad) = make_float2(o[i][2 * x] * f, o[i][2 * x + 1] * f);
         }
       };
       if (last <= first) {
@@ -539,34 +615,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = t.chunks == 1 ? cur.u : cur.u / t.chunks;
         const int h0 = hk * G + (cur.u - hk * t.chunks) * 16, rows = min(16, hk * G + G - h0);
 #pragma unroll
-        for (int rs = 0; rs < kRowSets; ++rs) {
-          const int r = gq + 8 * rs;
+        for (int x = 0; x < kSets; ++x) {
+          const int r = head_of(x);
           if (r >= rows) continue;
           const long long row = (long long)cur.b * a.Hq + h0 + r;
           // (every logit -inf: a weight of 0 and a log-sum of -inf, as without keys)
-          const float inv = l[rs] > 0.f ? 1.0f / l[rs] : l[rs], lse = m[rs] + lg2(l[rs]);
+          const float inv = l[x] > 0.f ? 1.0f / l[x] : l[x], lse = m[x] + lg2(l[x]);
           if (t.p.row_o) {
-            if (lane == 0 && rs == 0) t.p.held[cur.b * units + cur.u] = make_int2(1, 0);
-            put_part(t.p.row_o + row * D, rs, inv);
-            if (quad == 0) t.p.row_lse[row] = lse;
+            if (lane == 0 && x == 0) t.p.held[cur.b * units + cur.u] = make_int2(1, 0);
+            put_part(t.p.row_o + row * D, x, inv);
+            if (leader) t.p.row_lse[row] = lse;
           } else {
-            if (kCodes) {
+            if constexpr (kCodes) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < kCols; i += 8)
-                  *reinterpret_cast<uint4*>(a.out + row * D + (2 * quad + j) * kCols + i) =
-                      make_uint4(pack2<kF16>(o[i][2 * rs + j] * inv, o[i + 1][2 * rs + j] * inv),
-                                 pack2<kF16>(o[i + 2][2 * rs + j] * inv, o[i + 3][2 * rs + j] * inv),
-                                 pack2<kF16>(o[i + 4][2 * rs + j] * inv, o[i + 5][2 * rs + j] * inv),
-                                 pack2<kF16>(o[i + 6][2 * rs + j] * inv, o[i + 7][2 * rs + j] * inv));
+              for (int i = 0; i < kCols / 2; i += 4) {
+                const float (*v)[4] = &o[x / 2 * (kCols / 2) + i];
+                *reinterpret_cast<uint4*>(a.out + row * D + gq * kCols + 2 * i) =
+                    make_uint4(pack2<kF16>(v[0][x % 2] * inv, v[0][2 + x % 2] * inv),
+                               pack2<kF16>(v[1][x % 2] * inv, v[1][2 + x % 2] * inv),
+                               pack2<kF16>(v[2][x % 2] * inv, v[2][2 + x % 2] * inv),
+                               pack2<kF16>(v[3][x % 2] * inv, v[3][2 + x % 2] * inv));
+              }
             } else {
 #pragma unroll
               for (int i = 0; i < D / 8; ++i)
                 *reinterpret_cast<uint32_t*>(a.out + row * D + 8 * i + 2 * quad) =
-                    pack2<kF16>(o[i][2 * rs] * inv, o[i][2 * rs + 1] * inv);
+                    pack2<kF16>(o[i][2 * x] * inv, o[i][2 * x + 1] * inv);
             }
-            if (a.lse && quad == 0) a.lse[row] = lse * 0.693147180559945f;
+            if (a.lse && leader) a.lse[row] = lse * 0.693147180559945f;
           }
         }
       } else {
@@ -575,9 +651,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int part = first > 0 ? 0 : 1;
         float* dst = reinterpret_cast<float*>(part ? ring : smem + S::kFirst + warp * S::kPart);
 #pragma unroll
-        for (int rs = 0; rs < kRowSets; ++rs) {
-          put_part(dst + (gq + 8 * rs) * D, rs, 1.0f);
-          if (quad == 0) stats[(2 * warp + part) * S::kRows + gq + 8 * rs] = make_float2(m[rs], l[rs]);
+        for (int x = 0; x < kSets; ++x) {
+          put_part(dst + head_of(x) * D, x, 1.0f);
+          if (leader) stats[(2 * warp + part) * S::kRows + head_of(x)] = make_float2(m[x], l[x]);
         }
         if (lane == 0) open[2 * warp + part] = Open{cur.b, cur.u, cur.slices, cur.pos};
       }
