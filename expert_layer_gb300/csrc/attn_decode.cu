@@ -106,6 +106,9 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t w) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
@@ -168,13 +171,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* scales = reinterpret_cast<float2*>(smem + S::kScales) + warp * kStages;
   bool bad = false, late = false;
   pdl_trigger();     // the merge kernel may become resident; it waits for this grid's end
-  if (threadIdx.x == 0) {
+  if (!kCodes && threadIdx.x == 0) {
     prefetch_map(&tmK);
     prefetch_map(&tmV);
   }
 
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], t.arrivals + (kCodes ? 1 : 0));     // (codes: the scales' copy)
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], t.arrivals);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     open[2 * warp].b = open[2 * warp + 1].b = -1;
@@ -263,37 +266,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) page = a.page_table[(long long)ld.b * a.table_pages + ((ld_slice * kSlice) >> a.page_shift)];
     };
     fetch();
+    // codes: where the lane's pieces go, swizzled as code_at has them
+    uint32_t to[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) to[i] = code_at<D>(0, i * (512 / D) + lane * 16 / D, lane * 16 % D) - i * 512;
     auto issue = [&]() {
-      if (!more) return;
       if constexpr (kCodes) {
-        // (what one lane does while the others wait is kept short)
-        const bool there = (unsigned)page < (unsigned)a.pages;
-        bad |= !there;
-        const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
-        const int at = (there ? page : 0) * a.Hkv + (t.chunks == 1 ? ld.u : ld.u / t.chunks);
-        const float* from = a.scales + 2 * (((long long)at << (a.page_shift - 4)) + (row >> 4));
-        unsigned char* dst = ring + st * S::kStageBytes;
+        // Every lane copies 16 bytes of a row at a time (a copy group per slice,
+        // empty ones at the end, so that a wait leaves a fixed number of them).
+        // A box of TMA costs some 95 cycles of an SM whatever its size, and 16
+        // rows of codes are half the bytes: 128 sequences of 2000 to 8192 keys
+        // 98.3 us with boxes, now 98.1; 63 of 4579 with heads of 64 36.5 and 30.3.
+        // (Two slices to a step, so that each hides the other's latency: 99.8 and
+        // 30.2, and 0.4 us more for a few short sequences.)
+        if (more) {
+          const bool there = (unsigned)page < (unsigned)a.pages;
+          bad |= !there;
+          const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
+          const int at = (there ? page : 0) * a.Hkv + (t.chunks == 1 ? ld.u : ld.u / t.chunks);
+          const long long first = ((long long)at << a.page_shift) + row;
+          const uint32_t dst = smem_u32(ring + st * S::kStageBytes);
+          const unsigned char* k = reinterpret_cast<const unsigned char*>(a.k_cache) + first * D + lane * 16;
+          const unsigned char* v = reinterpret_cast<const unsigned char*>(a.v_cache) + first * D + lane * 16;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            copy16(dst + i * 512 + to[i % 2], k + i * 512);
+            copy16(dst + S::kTileBytes + i * 512 + to[i % 2], v + i * 512);
+          }
+          if (lane == 0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&scales[st])),
+                         "l"(a.scales + 2 * (first / kScaleBlock))
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (!more) return;
+      } else {
+        if (!more) return;
         if (lane == 0) {
+          if ((unsigned)page >= (unsigned)a.pages) {
+            bad = true;
+            page = 0;
+          }
+          const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
+          const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
+          unsigned char* dst = ring + st * S::kStageBytes;
           mbar_expect_tx(&bars[st], S::kStageBytes);
-          tma_load_3d(dst, &tmK, 0, row, at, &bars[st]);
-          tma_load_3d(dst + S::kTileBytes, &tmV, 0, row, at, &bars[st]);
-          asm volatile(
-              "cp.async.ca.shared.global [%0], [%1], 8;\n"
-              "cp.async.mbarrier.arrive.noinc.shared.b64 [%2];" ::"r"(smem_u32(&scales[st])),
-              "l"(from), "r"(smem_u32(&bars[st]))
-              : "memory");
+          tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
+          tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
         }
-      } else if (lane == 0) {
-        if ((unsigned)page >= (unsigned)a.pages) {
-          bad = true;
-          page = 0;
-        }
-        const int st = issued % kStages, row = (ld_slice * kSlice) & ((1 << a.page_shift) - 1);
-        const int hk = t.chunks == 1 ? ld.u : ld.u / t.chunks;
-        unsigned char* dst = ring + st * S::kStageBytes;
-        mbar_expect_tx(&bars[st], S::kStageBytes);
-        tma_load_5d(dst, &tmK, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
-        tma_load_5d(dst + S::kTileBytes, &tmV, 0, 0, 0, row / 8, page * a.Hkv + hk, &bars[st]);
       }
       ++issued;
       ++ld_slice;
@@ -404,7 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int st = used % kStages;
         // after a timeout nothing more is loaded: a stage whose load has not
         // landed must not be loaded again, nor its barrier be armed again
-        if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) late = true, more = false;
+        if constexpr (kCodes) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+          __syncwarp();
+        } else if (!late && !warp_spin(&bars[st], (used / kStages) & 1)) {
+          late = true, more = false;
+        }
         const uint32_t kb = smem_u32(ring + st * S::kStageBytes), vb = kb + S::kTileBytes;
         const int valid = cur.len - s * kSlice;
         if constexpr (kCodes) {
@@ -793,10 +818,9 @@ cudaError_t launch_attn_decode(const AttnArgs& a, const Beside& beside, const De
   t.head = beside.head;
   t.arrivals = a.hold == kHoldDecode ? 2 : 1;
   t.p = p;
-  CUtensorMap k, v;
+  CUtensorMap k = {}, v = {};
   const bool codes = a.scales != nullptr;
-  if (codes ? !codes_map(&k, a.k_cache, a, kSlice) || !codes_map(&v, a.v_cache, a, kSlice)
-            : !pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice))
+  if (!codes && (!pages_map(&k, a.k_cache, a, kSlice) || !pages_map(&v, a.v_cache, a, kSlice)))
     return cudaErrorInvalidValue;
   Report rep = shape;
   rep.blocks[rep.set] = num_sms;
