@@ -208,7 +208,9 @@ struct WeightArgs {
   float* weights;             // [n_seq, Hkv, capacity]
   int capacity;
   Divisor by_G;
+  int hold;                   // Hold
 };
+cudaError_t launch_attn_weights_tc(const WeightArgs& a, void* ws, int num_sms, cudaStream_t stream);
 cudaError_t launch_attn_weights(const WeightArgs& a, void* ws, int num_sms, cudaStream_t stream);
 
 // kv_evict.cu

@@ -417,6 +417,7 @@ int moe_attn_key_weights(const moe_heads* q, const void* k_cache, int pages, int
   a.c = scale * 1.4426950408889634f;
   a.lse = lse; a.weights = weights; a.capacity = capacity;
   a.by_G.set(Hq / Hkv);
+  a.hold = g_hold.load(std::memory_order_relaxed);
   return cuda_status(launch_attn_weights(a, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -150,6 +150,12 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
+// Keys [keys][D] as an operand of the product with queries: K-major, 128-byte swizzle,
+// groups of 8 keys `group` bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_k(uint32_t saddr, uint32_t group) {
+  return (umma_desc(saddr) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)(group >> 4) << 32;
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
@@ -186,6 +192,14 @@ inline bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3-D map over the queries: {D, head, token}; box {64, G, tt}.
+inline bool q_map(CUtensorMap* m, const Heads& q, int T, int Hq, int Hkv, int D, int tt) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {q.head * 2ull, q.tok * 2ull};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(Hq / Hkv), (cuuint32_t)tt};
+  return encode(m, q.data, 3, dims, strides, box);
+}
+
 // Packed rows [tokens, heads, D] as {D, token, head}: a box of {64, rows, 1}
 // is one 128-byte wide swizzled column of a tile.
 inline bool rows_map(CUtensorMap* m, const Heads& v, const AttnArgs& a, long long tokens, int heads, int box) {
@@ -202,12 +216,15 @@ inline bool rows_map(CUtensorMap* m, const Heads& v, const AttnArgs& a, long lon
 // (With a box per 64 columns a 16-row page takes two boxes of 2 KB, and the
 // copy engine spends ~95 cycles on a box: causal 8192 from 16-row pages then took
 // 22% longer than from pages of 128; now 322 us against 316.)
-inline bool pages_map(CUtensorMap* m, const uint16_t* cache, const AttnArgs& a, int rows) {
-  const cuuint64_t page = (cuuint64_t)a.D << a.page_shift;
-  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, 1ull << (a.page_shift - 3), (cuuint64_t)a.pages * a.Hkv};
-  const cuuint64_t strides[4] = {a.D * 2ull, 128, a.D * 16ull, page * 2};
-  const cuuint32_t box[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)rows / 8, 1};
+inline bool pages_map(CUtensorMap* m, const uint16_t* cache, int D, int page_shift, int pages, int Hkv, int rows) {
+  const cuuint64_t page = (cuuint64_t)D << page_shift;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)D / 64, 1ull << (page_shift - 3), (cuuint64_t)pages * Hkv};
+  const cuuint64_t strides[4] = {D * 2ull, 128, D * 16ull, page * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)D / 64, (cuuint32_t)rows / 8, 1};
   return encode(m, cache, 5, dims, strides, box);
+}
+inline bool pages_map(CUtensorMap* m, const uint16_t* cache, const AttnArgs& a, int rows) {
+  return pages_map(m, cache, a.D, a.page_shift, a.pages, a.Hkv, rows);
 }
 
 // A cache of codes [pages, Hkv, page_size, D] as {D, row, page * Hkv + head}: a

@@ -153,11 +153,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Keys [keys][D] as the B operand of S = Q K^T: K-major, 128-byte swizzle,
-// groups of 8 keys `group` bytes apart.
-__device__ __forceinline__ uint64_t umma_desc_k(uint32_t saddr, uint32_t group) {
-  return (umma_desc(saddr) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)(group >> 4) << 32;
-}
 // Values [keys][D] as the B operand of O += P V: D-major ("transposed"),
 // 128-byte swizzle; the next 64 columns of D `column` bytes on (leading
 // offset), the next 8 keys `group` bytes on (stride offset).
@@ -1044,14 +1039,6 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// 3-D map over the queries: {D, head, token}; box {64, G, tt}.
-bool q_map(CUtensorMap* m, const AttnArgs& a, int tt) {
-  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
-  const cuuint64_t strides[2] = {a.q.head * 2ull, a.q.tok * 2ull};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(a.Hq / a.Hkv), (cuuint32_t)tt};
-  return encode(m, a.q.data, 3, dims, strides, box);
-}
-
 // 3-D map over the output, or over the parts in fp32: boxes of 32 rows x 128
 // bytes, heads fastest.
 int box_heads(const AttnArgs& a) {
@@ -1126,7 +1113,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.arrivals = Arrivals(a.hold);
   const bool paged = a.page_table != nullptr;
   CUtensorMap q, k, v, o = {};
-  if (!q_map(&q, a, t.tt)) return cudaErrorInvalidValue;
+  if (!q_map(&q, a.q, a.T, a.Hq, a.Hkv, a.D, t.tt)) return cudaErrorInvalidValue;
   // (parts of all splits are one tensor of splits * T tokens)
   t.out_box = 32 % box_heads(a) == 0 && (long long)a.T * splits < (1ll << 31);
   if (t.out_box && !out_map(&o, a, part_o, splits)) return cudaErrorInvalidValue;

@@ -413,3 +413,18 @@ def test_served_from_8_bits(D, page, dtype):
                         for x, c in ((0, kc), (1, vc)))
             o, le, to, tl = c8.attend(q[s:s + 1], k64, v64, D ** -0.5)
             ref.check(out[s:s + 1], o, to, "decode")
+
+
+@pytest.mark.parametrize("wait", [2, 4, 5])
+@pytest.mark.parametrize("D", [128, 64])
+def test_key_weights_waits_that_give_up(wait, D):
+    """Loads of keys and rows and the products of the tensor cores' kernel: a barrier that never completes ends the call
+    with a report, and the next call on the workspace is right."""
+    import test_gpu_attention_waits as waits
+    q_lens, kv_lens, Hq, Hkv = [40, 60], [700, 900], 8, 2
+    kc, _, table, _ = page_pool(kv_lens, 16, Hkv, D, BF, 35)
+    q = rand(gen_of(36), 100, Hq, D)
+    lse = torch.full((100, Hq), 5.0, device="cuda")
+    ws = moe.alloc_attn_workspace(100, 2, Hq, Hkv, D)
+    waits.times_out(lambda: moe.attn_key_weights(q, kc, table, starts(q_lens), ints(kv_lens), lse,
+                                                 torch.zeros(2, Hkv, 900, device="cuda"), workspace=ws), ws, wait)
