@@ -41,6 +41,8 @@
 // epilogue 1.6).
 #include <cuda.h>
 
+#include <cmath>
+
 #include "attn.h"
 #include "attn_ptx.cuh"
 
@@ -55,28 +57,54 @@ constexpr int kKeys = 128;          // keys of a block
 constexpr int kItems = 4;           // ring of work items
 constexpr int kAskAhead = 3;        // key blocks before an item's end at which the next one is asked for
 constexpr int kSoftWarps = 8;       // two tiles x four warps, one row per thread
-// A cache in 8 bits: another warpgroup makes codes operands.
+// A cache in 8 bits: another warpgroup makes queries and values operands.
 constexpr int kCodeWarps = 4;
 template <bool kCodes>
 constexpr int kThreads = (kSoftWarps + 4 + (kCodes ? kCodeWarps : 0)) * 32;
 // Registers per thread: 168 at launch (three warpgroups; 128 with four); the
 // softmax warpgroups, which hold a row of 128 logits, draw on the others'.
 template <bool kCodes>
-constexpr int kSoftRegs = kCodes ? 192 : 208;
+constexpr int kSoftRegs = kCodes ? 184 : 208;
 template <bool kCodes>
-constexpr int kLoadRegs = kCodes ? 64 : 88;
+constexpr int kLoadRegs = kCodes ? 72 : 88;
 static_assert(2 * kSoftRegs<false> + kLoadRegs<false> <= 3 * 168 && 2 * kSoftRegs<true> + 2 * kLoadRegs<true> <= 4 * 128,
               "the shares come from the launch's registers");
-constexpr int kScaleSlots = 8;      // key blocks whose scales are kept (see the producer)
+constexpr int kScaleSlots = 8;      // key blocks whose scales are kept
 constexpr int kScaleBlocks = kKeys / kScaleBlock;
 constexpr int kHalf = kKeys / 2;
 constexpr float kMost = 32768.0f;   // sum of a row's P over half a block that asks for a new scale
 constexpr uint32_t kTmemCols = 512;
 
+// Scales of a block of codes: K's, of 16 keys; V's are 2^(top - down), top: the
+// largest of those of keys that there are.  `down` comes with V, the rest with K.
+struct __align__(16) Scales {
+  float k[kScaleBlocks];
+  int down[kScaleBlocks];
+  float top, inv;                  // inv: 2^-top
+};
+// Lane i has the scale of V of 16 keys of block b; all lanes of the warp take part
+__device__ __forceinline__ int top_exp(float scale, int b, int len) {
+  const int lane = threadIdx.x & 31;
+  const bool there = lane < kScaleBlocks && b * kKeys + lane * kScaleBlock < len;
+  return __reduce_max_sync(0xffffffffu, there ? scale_exp(scale) : kScaleMin);
+}
+// Scales in the cache of lane i's 16 keys of block b, whose page is `page`, and that
+// page (-1: none).  Pages out of range are reported where codes are loaded.
+__device__ __forceinline__ float2 load_scales(const AttnArgs& a, int b, int page, int head) {
+  if ((unsigned)page >= (unsigned)a.pages) return make_float2(0.f, 0.f);
+  const int row = (b * kKeys + (threadIdx.x & 31) * kScaleBlock) & ((1 << a.page_shift) - 1);
+  return reinterpret_cast<const float2*>(a.scales)[((((long long)page * a.Hkv + head) << a.page_shift) + row) / kScaleBlock];
+}
+__device__ __forceinline__ int scales_page(const AttnArgs& a, const int32_t* list, int b, int len) {
+  const int lane = threadIdx.x & 31, key = b * kKeys + lane * kScaleBlock;
+  return lane < kScaleBlocks && key < len ? list[key >> a.page_shift] : -1;
+}
+
 // Tiles in shared memory: rows of 64 elements in 1 KB swizzle atoms of 8.  Q,
 // and K and V from packed rows: one column of atoms after the other.  K and V
-// from pages: atoms of the same 8 rows side by side (pages_map).
-template <int D, bool kPaged>
+// from pages: atoms of the same 8 rows side by side (pages_map).  With codes a
+// stage of K holds their tile alone, and Q its parts (split_rows).
+template <int D, bool kPaged, bool kCodes, bool kF16>
 struct Shape {
   static constexpr int kHalves = D / 64;                       // 128-byte wide swizzled columns
   static constexpr int kHalfBytes = kRows * 128;               // 16 KB: a column
@@ -84,12 +112,18 @@ struct Shape {
   static constexpr int kGroup = kPaged ? kHalves * 1024 : 1024;   // from 8 rows of K or V to the next
   static constexpr int kTileBytes = kHalves * kHalfBytes;      // a Q, K or V tile
   // ring of K and V tiles: 8192 causal with 3 and 4 stages of 32 KB 421 and 324 us
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;             // K and V tiles in turns
+  static constexpr int kKeyBytes = kCodes ? kKeys * D : kTileBytes;
   static constexpr int kRing = 2 * kTileBytes;                 // the ring follows the two Q tiles
-  static constexpr int kOut = kRing + kStages * kTileBytes;    // 32 rows of 128 bytes per softmax warp
+  static constexpr int kThird = kRing + kStages / 2 * (kKeyBytes + kTileBytes);         // codes and f16: Q's third part
+  static constexpr int kOut = kThird + (kCodes && kF16 ? 2 * kHalfBytes : 0);   // 32 rows of 128 bytes per softmax warp
   static constexpr int kBars = kOut + kSoftWarps * 32 * 128;
-  static constexpr int kScales = kBars + 1024;                 // codes: [slot][16 keys] (K, V)
-  static constexpr size_t kSmem = kScales + (kPaged ? kScaleSlots * kScaleBlocks * 8 : 0);
+  static constexpr int kScales = kBars + 1024;                 // codes: [slot]
+  static constexpr int kExps = kScales + kScaleSlots * (int)sizeof(Scales);             // [item & 1][tile][row]
+  static constexpr size_t kSmem = kCodes ? kExps + 2 * 2 * kRows : kScales;
+  __device__ static constexpr int stage(int s) {
+    return kRing + (kCodes ? (s >> 1) * (kKeyBytes + kTileBytes) + (s & 1) * kKeyBytes : s * kTileBytes);
+  }
 };
 
 struct Item {
@@ -101,6 +135,7 @@ struct Item {
   int len;         // keys of the sequence
   int seen;        // keys that token row0 sees (causal; may be <= 0), else len
   int split;
+  int seq;
 };
 
 // Arrivals that the barriers wait for, one too many where a test holds one
@@ -119,6 +154,7 @@ struct TcAttnArgs {
   int tt, slots, splits;
   int box;                       // rows of a K / V box
   float c;                       // scale log2 e, not 0
+  int exp_low, exp_high;         // of a row's scale (codes): its factors are normal
   float hidden;                  // a masked logit: c times it is -inf
   int out_box;                   // 32 rows of a tile are whole heads of whole tokens
   float* part_o;                 // [splits, T, Hq, D], null when the result is final
@@ -159,6 +195,19 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ uint64_t umma_desc_v(uint32_t saddr, uint32_t column, uint32_t group) {
   return (umma_desc_k(saddr, group) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(column >> 4) << 16;
 }
+// A tile of keys as codes: K-major rows of D bytes, swizzled as they are wide
+template <int D>
+__device__ __forceinline__ uint64_t umma_desc_codes(uint32_t saddr) {
+  const uint64_t d = umma_desc_k(saddr, 8 * D);
+  return D == 128 ? d : (d & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+__device__ __forceinline__ void umma_codes(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum));
+}
 __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accum) {
   asm volatile(
@@ -171,6 +220,100 @@ template <bool kF16>
 __device__ __forceinline__ constexpr uint32_t idesc_of(int n, bool b_t) {
   return (1u << 4) | ((kF16 ? 0u : 1u) << 7) | ((kF16 ? 0u : 1u) << 10) | ((b_t ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+// kind::f8f6f4, e4m3 both, fp32 accumulators
+__device__ __forceinline__ constexpr uint32_t idesc_codes(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ queries and codes
+// The product of queries and codes takes both in e4m3.  A row of Q, times the
+// power of two 2^-e that brings its largest element to (224, 448], is a sum of
+// parts, each the rounding of what those before it leave:
+//   q 2^-e = hi + lo (+ third, f16),   S = K hi + K lo (+ K third)
+// A part takes 4 bits of 8 (bf16) or 11 (f16), so that the sum is exact but for
+// elements whose last bit lies below 2^-9, the smallest e4m3: they are off by at
+// most 2^-10, 2^-17.8 of the row's largest (a key is off by 2^-4 of itself).  A
+// row that holds an infinity or NaN becomes NaN.
+//
+// In place: `tile` as TMA leaves it (64 elements of a row in each column of
+// atoms), a lane for 64 elements; hi and lo then are the columns (D = 128) or the
+// halves of a row (D = 64), the third part's rows lie at `third`.  Tiles' rows are
+// divided among the four warps; exps: e of each row.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t code_pair(float a, float b) {
+  uint32_t r;
+  asm("{\n .reg .b16 l;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.u32.u16 %0, l;\n}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Four elements' codes; y becomes what they leave
+__device__ __forceinline__ uint32_t take_part(float (&y)[4]) {
+  const uint32_t w = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
+  const float2 a = half2_floats(codes2<0>(w)), b = half2_floats(codes2<1>(w));
+  y[0] -= a.x, y[1] -= a.y, y[2] -= b.x, y[3] -= b.y;
+  return w;
+}
+__device__ __forceinline__ void sts4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+template <int D, bool kF16>
+__device__ __forceinline__ void split_rows(uint32_t tile, uint32_t third, int8_t* exps, int cw) {
+  constexpr int kLanes = D / 64, kStep = 32 / kLanes;          // lanes of a row, rows of a step
+  const int lane = threadIdx.x & 31, h = lane / kStep;
+#pragma unroll 1
+  for (int i = 0; i < kLanes; ++i) {
+    const int r = (cw * kLanes + i) * kStep + lane % kStep;
+    const uint32_t row = tile + r * 128;
+    uint4 raw[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) raw[c] = lds4(row + h * (kRows * 128) + ((c ^ (r & 7)) * 16));
+    uint32_t most = 0;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      most = max_u16x2(most, max_u16x2(max_u16x2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu),
+                                       max_u16x2(raw[c].z & 0x7fff7fffu, raw[c].w & 0x7fff7fffu)));
+    most = max(most & 0xffffu, most >> 16);
+    if (kLanes == 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, kStep));
+    const uint32_t top = kF16 ? __float_as_uint(half2_floats(most).x) : most << 16;
+    // the smallest e with top <= 448 2^e (448 = 1.75 2^8); 2^-e stays normal
+    const int e = max(-126, (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
+    const float by = top < 0x7f800000u ? exp2i(-e) : __uint_as_float(0x7fffffffu);
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w[8] = {raw[2 * k].x,     raw[2 * k].y,     raw[2 * k].z,     raw[2 * k].w,
+                             raw[2 * k + 1].x, raw[2 * k + 1].y, raw[2 * k + 1].z, raw[2 * k + 1].w};
+      uint32_t last[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 a = floats2<kF16>(w[2 * u]), b = floats2<kF16>(w[2 * u + 1]);
+        float y[4] = {a.x * by, a.y * by, b.x * by, b.y * by};
+        hi[k][u] = take_part(y);
+        if (kF16) lo[k][u] = take_part(y), last[u] = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
+        else lo[k][u] = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
+      }
+      if (kF16) sts4(third + r * 128 + (((h * 4 + k) ^ (r & 7)) * 16), last);
+    }
+    __syncwarp();                                              // a row's lanes have read it
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      sts4(row + (((h * 4 + k) ^ (r & 7)) * 16), hi[k]);
+      if (D == 128) sts4(row + kRows * 128 + (((h * 4 + k) ^ (r & 7)) * 16), lo[k]);
+      else sts4(row + (((4 + k) ^ (r & 7)) * 16), lo[k]);
+    }
+    if (h == 0) exps[r] = (int8_t)e;
+  }
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // ------------------------------------------------------------------ work items
@@ -266,8 +409,8 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // ------------------------------------------------------------------ the kernel
 // warps 0-3, 4-7   softmax and epilogue of tile 0 and 1 (thread = row)
 // warp 8           work items, TMA loads of Q, K and V
-// warps 9, 10      issue the MMAs of tile 0 and 1 (warp 11 only completes the
-//                  warpgroup): per key block O += P V, half by half as P
+// warps 9, 10      issue the MMAs of tile 0 and 1 (warp 11 completes the
+//                  warpgroup; of codes, it loads V): per key block O += P V, half by half as P
 //                  comes, then S = Q K' of the next block; one tile's softmax
 //                  runs while the other multiplies.  A barrier costs an
 //                  issuing warp ~200 cycles even when it is complete (the MMAs'
@@ -278,21 +421,29 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // covers O += P(j) V, so a softmax warp that has S(j+1) may rescale O without
 // waiting.
 //
-// A cache in 8 bits (kCodes, paged): TMA brings the codes of a tile to the upper
-// half of its stage, and four more warps (12-15) make them the operand, in
-// place: every code is in registers before the first element is written.  K
-// becomes the queries' type, times its scale where that is bf16 (f16 keeps the
-// codes as they are, and the logits of 16 keys take the scale); V becomes f16
-// without its scale 2^e, which joins the exponent of P instead,
-//   P = 2^{c S + e - m'},  O += P code,  l += 2^{-e} sum P,
-// so that m' follows what a key adds to O, and P and the codes stay within f16
-// whatever the scales.
+// A cache in 8 bits (kCodes, paged): K's codes are an operand as TMA leaves them,
+// and four more warps (12-15) make the queries parts in e4m3 (split_rows).  A
+// row's scale and that of 16 keys, both powers of two, join the factor of the
+// logits.  V's codes land in the upper half of their stage, and the same warps
+// make them f16, in place: every code is in registers before the first element
+// is written.  They take the tile's largest scale 2^e out, which joins the
+// exponent of P instead,
+//   P = 2^{c S + e - m'},  O += P (V 2^-e),  l += 2^{-e} sum P,
+// so that m' follows what a tile adds to O, and P and the values stay within f16
+// whatever the scales: a value is off by at most 2^-25 of 2^e, 2^-32 of the tile's
+// largest.  (Both K and V made bf16 or f16 by those warps, and a scale of V for
+// each 16 keys in the softmax: 4096 rows over 8192 keys, bf16, 408 us; K as codes
+// 348; scales from the loading warps, one of V for the tile 326; now 321.  K and V
+// in bf16 take 250: the four warps' work on a tile of V, ~1200 cycles beside the
+// softmax, is what is left, and what they do not have to do shows: V's codes by
+// shifts in place of conversions, which share a pipe with the exponentials, but
+// are more instructions, 384.)
 template <int D, bool kF16, bool kPaged, bool kCodes>
 __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const TcAttnArgs t,
                    const Report rep) {
-  using S = Shape<D, kPaged>;
+  using S = Shape<D, kPaged, kCodes, kF16>;
   constexpr int NS = S::kStages;
   constexpr bool kP16 = kF16 || kCodes;                        // P and V in f16 (else bf16)
   static_assert(kPaged || !kCodes, "codes are paged");
@@ -310,11 +461,13 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
   uint64_t* it_empty = it_full + kItems;
   uint64_t* drain = it_empty + kItems;
   uint64_t* clc = drain + 2;
-  uint64_t* code_full = clc + 1;         // codes: a tile's codes (and with K's the scales) have landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(code_full + (kCodes ? NS : 0));
+  uint64_t* code_full = clc + 1;         // codes: those of V have landed
+  uint64_t* q_parts = code_full + (kCodes ? NS : 0);           // codes: [tile]: its queries are split
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_parts + (kCodes ? 2 : 0));
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   Item* ring = reinterpret_cast<Item*>(tmem_slot + 2);
-  float2* scales = reinterpret_cast<float2*>(smem + S::kScales);
+  Scales* scales = reinterpret_cast<Scales*>(smem + S::kScales);
+  int8_t* q_exps = reinterpret_cast<int8_t*>(smem + S::kExps);
   uint4* answer = reinterpret_cast<uint4*>(smem + S::kBars + 1024 - 16);
 
   const AttnArgs& a = t.a;
@@ -331,13 +484,14 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
   if (threadIdx.x == 0) {
     const Arrivals& n = t.arrivals;
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], (s ? 1 : n.keys) + (kCodes ? kCodeWarps - 1 : 0));
+      mbar_init(&kv_full[s], (s ? 1 : n.keys) + (kCodes && s % 2 ? kCodeWarps - 1 : 0));
       mbar_init(&kv_empty[s], n.stage);
-      if (kCodes) mbar_init(&code_full[s], s % 2 ? 1 : 33);       // K tiles (even): and every lane's copy of scales
+      if (kCodes) mbar_init(&code_full[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], n.query);
       mbar_init(&q_empty[x], 1);
+      if (kCodes) mbar_init(&q_parts[x], kCodeWarps);
       mbar_init(&s_full[x], n.s);
       mbar_init(&p_full[2 * x], n.p);
       mbar_init(&p_full[2 * x + 1], n.p);
@@ -345,7 +499,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
       mbar_init(&h_done[x], n.half);
       mbar_init(&turn[x], n.turn);
     }
-    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], n.item); mbar_init(&it_empty[i], kSoftWarps + 2 + (kCodes ? kCodeWarps : 0)); }
+    for (int i = 0; i < kItems; ++i) { mbar_init(&it_full[i], n.item); mbar_init(&it_empty[i], kSoftWarps + 2 + (kCodes ? kCodeWarps + 1 : 0)); }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     mbar_init(clc, n.next);
@@ -433,9 +587,16 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
         bad = true;
         return 0;
       };
-      int page = it.n[0] + it.n[1] > 0 && !end ? fetch(it.b0) : 0;       // under way while Q is loaded
+      // codes: scales of a block are loaded a block ahead of their use, their pages
+      // another one
+      float2 sc = make_float2(0.f, 0.f);
+      int group = -1;
+      const bool any = it.n[0] + it.n[1] > 0 && !end;
+      int page = any ? fetch(it.b0) : 0;                // under way while Q is loaded
+      if (kCodes && any) group = scales_page(a, list, it.b0, it.len);
       const int slot = ni % kItems;
       if (!warp_spin(&it_empty[slot], ((ni / kItems) & 1) ^ 1)) { ok = false; break; }
+      it.seq = seq;
       if (lane == 0) {
         ring[slot] = it;
         mbar_arrive(&it_full[slot]);
@@ -456,41 +617,49 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           }
           if (ok) ++nq[x];
         }
+      if (kCodes) {
+        sc = load_scales(a, it.b0, group, it.head);
+        group = n > 1 ? scales_page(a, list, it.b0 + 1, it.len) : -1;
+      }
       for (int j = 0; j < n && ok; ++j) {
         const int b = it.b0 + j;
         page = checked(page);
         const int next = j + 1 < n ? fetch(b + 1) : 0;
+        float2 sc_next = sc;
+        if (kCodes) {
+          sc_next = load_scales(a, b + 1, group, it.head);
+          group = j + 2 < n ? scales_page(a, list, b + 2, it.len) : -1;
+        }
         if (j > 0 && n - j == kAskAhead) ask();
         // boxes that hold keys of the sequence; the rest of the tile is not read
         const int nbox = min(boxes, (it.len - b * kKeys + t.box - 1) / t.box);
 #pragma unroll 1
         for (int w = 0; w < 2; ++w, ++kv) {
+          if (kCodes && w) continue;                   // V: warp 11
           const int s = kv % NS;
           ok = warp_spin(&kv_empty[s], ((kv / NS) & 1) ^ 1);
           if (!ok) break;
+          if (kCodes) {
+            // Slot of block j: both softmaxes are done with block j - kScaleSlots, as
+            // both tiles have had S of block j - NS / 2 (the slot's `down` is V's)
+            static_assert(NS / 2 < kScaleSlots, "slots of scales");
+            const int top = top_exp(sc.y, b, it.len);
+            Scales& to = scales[(kv / 2) % kScaleSlots];
+            if (lane < kScaleBlocks) to.k[lane] = exp2i(scale_exp(sc.x));
+            if (lane == 0) to.top = (float)top, to.inv = exp2i(-top);
+            __syncwarp();
+          }
           if (lane == 0) {
-            if (kCodes) mbar_expect_tx(&code_full[s], (uint32_t)(nbox * t.box * D));
+            if (kCodes) mbar_expect_tx(&kv_full[s], (uint32_t)(nbox * t.box * D));
             else mbar_expect_tx(&kv_full[s], (uint32_t)(S::kHalves * nbox * t.box * 128));
           }
           __syncwarp();
           if (lane < nbox) {
-            unsigned char* dst = smem + S::kRing + s * S::kTileBytes;
+            unsigned char* dst = smem + S::stage(s);
             const int key = b * kKeys + lane * t.box;
             if (kCodes) {
-              const int row = key & ((1 << a.page_shift) - 1);
-              tma_load_3d(dst + S::kTileBytes / 2 + lane * t.box * D, w ? &tmV : &tmK, 0, row, page * a.Hkv + it.head,
-                          &code_full[s]);
-              // the scales of both, with the K tile.  Those of block j + NS/2 + 1
-              // come after V of block j was given back, when both softmaxes
-              // have used the ones of block j: kScaleSlots > NS/2 + 1
-              static_assert(NS / 2 + 1 < kScaleSlots, "slots of scales");
-              if (w == 0) {
-                const long long block = ((((long long)page * a.Hkv + it.head) << a.page_shift) + row) / kScaleBlock;
-                const float2* from = reinterpret_cast<const float2*>(a.scales) + block;
-                float2* to = scales + (kv / 2) % kScaleSlots * kScaleBlocks + lane * (t.box / kScaleBlock);
-                for (int i = 0; i < t.box / kScaleBlock; ++i)
-                  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to + i)), "l"(from + i) : "memory");
-              }
+              tma_load_3d(dst + lane * t.box * D, &tmK, 0, key & ((1 << a.page_shift) - 1), page * a.Hkv + it.head,
+                          &kv_full[s]);
             } else if (kPaged) {
               tma_load_5d(dst + lane * (t.box / 8) * S::kGroup, w ? &tmV : &tmK, 0, 0, 0,
                           (key & ((1 << a.page_shift) - 1)) / 8, page * a.Hkv + it.head, &kv_full[s]);
@@ -500,10 +669,9 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
                 tma_load_3d(dst + hh * S::kHalfBytes, w ? &tmV : &tmK, hh * 64, k0 + key, it.head, &kv_full[s]);
             }
           }
-          if (kCodes && w == 0)
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&code_full[s])) : "memory");
         }
         page = next;
+        sc = sc_next;
       }
       if (*(volatile int*)abort_flag) ok = false;
       if (ok) idx = taken();
@@ -519,8 +687,8 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
       }
       // The loads issued land before the block exits, also where another warp
       // gives up after this one's last item (in normal use they are all used).
-      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; ++i)
-        spin_wait(kCodes ? &code_full[i % NS] : &kv_full[i % NS], (i / NS) & 1);
+      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 0; i < kv; i += kCodes ? 2 : 1)
+        spin_wait(&kv_full[i % NS], (i / NS) & 1);
       for (int x = 0; x < 2; ++x)
         if (nq[x]) spin_wait(&q_full[x], (nq[x] - 1) & 1);
     }
@@ -533,17 +701,30 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kP16>(D, true);
     const int x = __reduce_max_sync(0xffffffffu, warp - kSoftWarps - 1);      // tile
     const uint32_t tS = x * kKeys, tO = 2 * kKeys + x * D;   // all 512 columns: the allocation starts at 0
-    const uint32_t sQ = smem_u32(smem) + x * S::kTileBytes, sR = smem_u32(smem) + S::kRing;
+    const uint32_t s0 = smem_u32(smem), sQ = s0 + x * S::kTileBytes;
     int ks = 0;                      // ring stage and phase of the next K tile; V tiles alternate with K tiles
     uint32_t kph = 0, ni = 0, qph = 0, pph = 0;
     bool ok = true;
     auto product_s = [&](int s) {
       if (elect_one()) {
-        const uint64_t dq = umma_desc(sQ), dk = umma_desc_k(sR + s * S::kTileBytes, S::kGroup);
+        const uint64_t dq = umma_desc(sQ);
+        if constexpr (kCodes) {
+          const uint64_t dk = umma_desc_codes<D>(s0 + S::stage(s));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_id(tS, dq + (((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4),
-                       dk + (((kk / 4) * S::kColumn + (kk % 4) * 32) >> 4), kIdS, kk ? 1u : 0u);
+          for (int part = 0; part < (kF16 ? 3 : 2); ++part) {
+            const uint64_t dp = part == 2 ? umma_desc(s0 + S::kThird + x * S::kHalfBytes)
+                                          : dq + ((part * (D == 128 ? S::kHalfBytes : 64)) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_codes(tS, dp + ((kk * 32) >> 4), dk + ((kk * 32) >> 4), idesc_codes(kKeys), part + kk ? 1u : 0u);
+          }
+        } else {
+          const uint64_t dk = umma_desc_k(s0 + S::stage(s), S::kGroup);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_id(tS, dq + (((kk / 4) * S::kHalfBytes + (kk % 4) * 32) >> 4),
+                         dk + (((kk / 4) * S::kColumn + (kk % 4) * 32) >> 4), kIdS, kk ? 1u : 0u);
+        }
         umma_commit(&s_full[x]);
       }
       __syncwarp();
@@ -551,7 +732,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     // one half (64 keys) of a block
     auto product_o = [&](int half, int s, uint32_t add) {
       if (elect_one()) {
-        const uint64_t dv = umma_desc_v(sR + s * S::kTileBytes, S::kColumn, S::kGroup);
+        const uint64_t dv = umma_desc_v(s0 + S::stage(s), S::kColumn, S::kGroup);
 #pragma unroll
         for (int i = 0; i < kKeys / 32; ++i) {
           const int kk = half * (kKeys / 32) + i;
@@ -585,7 +766,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
       if (n == 0) continue;
       ok = warp_spin(&kv_full[ks], kph);
       if (ok && nx > 0) {
-        ok = warp_spin(&q_full[x], qph);
+        ok = warp_spin(kCodes ? &q_parts[x] : &q_full[x], qph);
         qph ^= 1;
         tc_fence_after();
         if (ok) product_s(ks);
@@ -631,12 +812,63 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     commit(&drain[x]);
     if (lane == 0) spin_wait(&drain[x], 0);
     __syncwarp();
+    } else if (kCodes && warp == kSoftWarps + 3) {
+    // ------------------------------------------------------------ codes of V
+    // (one warp for K and V: a box costs ~95 cycles to issue, 16 of them and the
+    // scales 3000 cycles for a block of 16-row pages, the period of the whole loop)
+    uint32_t kv = 1, ni = 0;
+    bool ok = true;
+    const int boxes = kKeys / t.box;
+    while (ok) {
+      const int slot = ni % kItems;
+      ok = warp_spin(&it_full[slot], (ni / kItems) & 1) && !*(volatile int*)abort_flag;
+      if (!ok) break;
+      const int row0 = ring[slot].row0, n = max(ring[slot].n[0], ring[slot].n[1]), b0 = ring[slot].b0;
+      const int len = ring[slot].len, head = ring[slot].head, seq = ring[slot].seq;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&it_empty[slot]);
+      ++ni;
+      if (row0 < 0) break;
+      const int32_t* list = a.prefix_table ? a.prefix_table : a.page_table + (long long)seq * a.table_pages;
+      auto fetch = [&](int b) {
+        const int key = b * kKeys + lane * t.box;
+        return lane < boxes && key < len ? list[key >> a.page_shift] : 0;
+      };
+      int page = n > 0 ? fetch(b0) : 0, group = n > 0 ? scales_page(a, list, b0, len) : -1;
+      float2 sc = load_scales(a, b0, group, head);
+      group = n > 1 ? scales_page(a, list, b0 + 1, len) : -1;
+      for (int j = 0; j < n && ok; ++j, kv += 2) {
+        const int b = b0 + j, s = kv % NS;
+        if ((unsigned)page >= (unsigned)a.pages) page = 0;             // reported with K
+        const int next = j + 1 < n ? fetch(b + 1) : 0;
+        const float2 sc_next = load_scales(a, b + 1, group, head);
+        group = j + 2 < n ? scales_page(a, list, b + 2, len) : -1;
+        const int nbox = min(boxes, (len - b * kKeys + t.box - 1) / t.box);
+        ok = warp_spin(&kv_empty[s], ((kv / NS) & 1) ^ 1);
+        if (!ok) break;
+        const int top = top_exp(sc.y, b, len);
+        if (lane < kScaleBlocks) scales[(kv / 2) % kScaleSlots].down[lane] = max(0, top - scale_exp(sc.y));
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(&code_full[s], (uint32_t)(nbox * t.box * D));
+        __syncwarp();
+        if (lane < nbox)
+          tma_load_3d(smem + S::stage(s) + S::kTileBytes / 2 + lane * t.box * D, &tmV, 0,
+                      (b * kKeys + lane * t.box) & ((1 << a.page_shift) - 1), page * a.Hkv + head, &code_full[s]);
+        page = next;
+        sc = sc_next;
+      }
+    }
+    if (lane == 0) {
+      if (!ok) atomicOr(abort_flag, 1);
+      for (uint32_t i = kv > (uint32_t)NS ? kv - NS : 1; i < kv; i += 2) spin_wait(&code_full[i % NS], (i / NS) & 1);
+    }
+    __syncwarp();
     } else if (kCodes && warp >= kSoftWarps + 4) {
     // ------------------------------------------------------------ codes to operands
-    // A tile at a time, four of its sixteen groups of 8 keys per warp.  Whether
-    // to go on is agreed at the barrier, which every warp reaches within the
-    // limit of its wait.
-    constexpr int kPieces = D / 64;               // 16-byte pieces of a lane per group
+    // The item's queries, then a tile of V at a time, four of its sixteen groups of
+    // 8 keys per warp.  Whether to go on is agreed at the barrier, which every warp
+    // reaches within the limit of its wait.
+    constexpr int kPieces = D / 32;               // pieces of a lane per group
     const int cw = warp - kSoftWarps - 4;
     auto agree = [&](bool mine) {
       uint32_t all;
@@ -648,65 +880,79 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           : "memory");
       return all != 0;
     };
-    uint32_t kv = 0, ni = 0;
+    uint32_t kv = 0, ni = 0, nq[2] = {0, 0};
     bool ok = true;
     while (ok) {
       const int slot = ni % kItems;
       ok = agree(warp_spin(&it_full[slot], (ni / kItems) & 1) && !*(volatile int*)abort_flag);
       if (!ok) break;
-      const int row0 = ring[slot].row0, n = max(ring[slot].n[0], ring[slot].n[1]);
+      const int row0 = ring[slot].row0, rows0 = ring[slot].n[0], rows1 = ring[slot].n[1], n = max(rows0, rows1);
       const int left = ring[slot].len - ring[slot].b0 * kKeys;       // keys from the first block on
       __syncwarp();
       if (lane == 0) mbar_arrive(&it_empty[slot]);
       ++ni;
       if (row0 < 0) break;
+      bool split = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (split && (x ? rows1 : rows0) > 0) {
+          split = warp_spin(&q_full[x], nq[x] & 1);
+          split_rows<D, kF16>(smem_u32(smem) + x * S::kTileBytes, smem_u32(smem) + S::kThird + x * S::kHalfBytes,
+                              q_exps + ((nq[x] & 1) * 2 + x) * kRows, cw);
+          ++nq[x];
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && split) mbar_arrive(&q_parts[x]);
+        }
 #pragma unroll 1
-      for (int j = 0; j < 2 * n && ok; ++j, ++kv) {
-        const int s = kv % NS;
-        const bool value = j & 1;
-        const uint32_t tile = smem_u32(smem) + S::kRing + s * S::kTileBytes, codes = tile + S::kTileBytes / 2;
-        // this lane's piece of a group: row and 16 elements of it
-        constexpr int kRowPieces = D / 16;
+      for (int j = 0; j < n && ok; ++j) {
+        kv += 2;
+        const int s = (kv - 1) % NS;
+        const uint32_t tile = smem_u32(smem) + S::stage(s), codes = tile + S::kTileBytes / 2;
+        // this lane's piece of a group: row and 8 elements of it, a chunk of 16 bytes
+        // of the operand: a store of eight lanes takes all banks (16 codes and two
+        // chunks to a lane: two lanes to a bank)
+        constexpr int kRowPieces = D / 8;
         const int r0 = lane / kRowPieces, c = lane % kRowPieces;
-        const bool got = warp_spin(&code_full[s], (kv / NS) & 1);
-        uint4 raw[4][kPieces];
+        const bool got = split && warp_spin(&code_full[s], ((kv - 1) / NS) & 1);
+        uint2 raw[4][kPieces];
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
           for (int i = 0; i < kPieces; ++i)
-            raw[g][i] = lds4(code_at<D>(codes, (cw * 4 + g) * 8 + r0 + i * (32 / kRowPieces), c * 16));
+            raw[g][i] = lds2(code_at<D>(codes, (cw * 4 + g) * 8 + r0 + i * (32 / kRowPieces), c * 8));
         ok = agree(got);
         if (!ok) break;
-        const float2* sc = scales + (kv / 2) % kScaleSlots * kScaleBlocks;
-        const int tail = left - (j / 2) * kKeys;
+        const int tail = left - j * kKeys;
+        if (tail < kKeys) {
+          // values past the end: a weight of 0 does not silence what other data, or NaN, is there
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+              if ((cw * 4 + g) * 8 + r0 + i * (32 / kRowPieces) >= tail) raw[g][i] = make_uint2(0, 0);
+        }
+        const Scales& sc = scales[(kv / 2 - 1) % kScaleSlots];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float f = kF16 || value ? 1.0f : exp2i(scale_exp(sc[cw * 2 + g / 2].x));
+          // 2^-down in two factors (the first product is exact; the second factor is
+          // subnormal from 2^-15 on, down is at most kScaleMax - kScaleMin = 31)
+          const int down = sc.down[cw * 2 + g / 2];
+          const uint32_t by = (uint32_t)(15 - min(down, 14)) << 10, by2 = by | by << 16;
+          const int rest = down - 14;
+          const uint32_t more = rest > 14 ? 0x400u >> (rest - 14) : (uint32_t)(15 - max(rest, 0)) << 10;
+          const uint32_t more2 = more | more << 16;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             const int rr = r0 + i * (32 / kRowPieces);
-            // values past the end: a weight of 0 does not silence what other data, or NaN, is there
-            const bool none = value && (cw * 4 + g) * 8 + rr >= tail;
-            const uint32_t w[4] = {raw[g][i].x, raw[g][i].y, raw[g][i].z, raw[g][i].w};
-            uint32_t e[8];
+            uint32_t e[4] = {codes2<0>(raw[g][i].x), codes2<1>(raw[g][i].x), codes2<0>(raw[g][i].y), codes2<1>(raw[g][i].y)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = none ? 0u : w[k];
-              e[2 * k] = codes2<0>(x), e[2 * k + 1] = codes2<1>(x);
+            for (int k = 0; k < 4; ++k) e[k] = mul_f16x2(e[k], by2);
+            if (down > 14) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) e[k] = mul_f16x2(e[k], more2);
             }
-            if (!kF16 && !value) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float2 v = half2_floats(e[k]);
-                e[k] = pack2<false>(v.x * f, v.y * f);
-              }
-            }
-            const uint32_t to = tile + (cw * 4 + g) * S::kGroup + (c / 4) * 1024 + rr * 128;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (((2 * c + k) % 8) ^ rr) * 16),
-                           "r"(e[4 * k]), "r"(e[4 * k + 1]), "r"(e[4 * k + 2]), "r"(e[4 * k + 3])
-                           : "memory");
+            sts4(tile + (cw * 4 + g) * S::kGroup + (c / 8) * 1024 + rr * 128 + ((c % 8) ^ rr) * 16, e);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -725,7 +971,8 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     const int token = t.by_G.of(row), g = row - token * G;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + x * kKeys, tO = tmem + lanes + 2 * kKeys + x * D;
-    uint32_t ni = 0, ns = 0, no = 0, nt = 0, kv = 0;
+    uint32_t ni = 0, ns = 0, no = 0, nt = 0, kv = 0, nq = 0;
+    float c = t.c;                                             // codes: times the scale of the row's queries
     bool ok = true;
     while (ok) {
       const int slot = ni % kItems;
@@ -748,6 +995,10 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
       for (int j = 0; j < n; ++j, ++ns) {
         if (!warp_spin(&s_full[x], ns & 1)) { ok = false; break; }
         tc_fence_after();
+        const Scales& sc = scales[(kv0 / 2 + j) % kScaleSlots];
+        // codes: the scale of the row's queries (such that no factor flushes or overflows)
+        if (kCodes && j == 0)
+          c = t.c * exp2i(min(max((int)q_exps[((nq++ & 1) * 2 + x) * kRows + row], t.exp_low), t.exp_high));
         // Turns: left alone the two tiles fall into step, with the tensor core
         // idle while both compute P and the reverse (8192 x 8192 keys, D = 128:
         // 668 us).  A tile hands over when all its P is formed (594 us; after
@@ -756,10 +1007,6 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
         // the first half.
         if (j < both && !warp_spin(&turn[x], (nt & 1) ^ (x ? 0 : 1))) { ok = false; break; }
         const int b = it.b0 + j;
-        const uint64_t c2 = pair(t.c, t.c);
-        const float2* sc = scales + (kv0 / 2 + j) % kScaleSlots * kScaleBlocks;
-        // codes: of 16 keys, the factor of their logits and the exponent of their values' scale
-        auto factor = [&](int i) { return kF16 ? t.c * exp2i(scale_exp(sc[i].x)) : t.c; };
         auto arrive = [&](int half) {
           tmem_wait_st();
           tc_fence_before();
@@ -784,47 +1031,27 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           tmem_wait_ld();
           float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * (kCodes ? factor(0) : t.c) : -INFINITY);
-          if (kCodes) top += (float)scale_exp(sc[0].y);
+          for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * (kCodes ? c * sc.k[0] : t.c) : -INFINITY);
+          if (kCodes) top += sc.top;
           if (m == -INFINITY) m = top;
           unset = __any_sync(0xffffffffu, live && m == -INFINITY);
         }
-        // 64 logits to P with the scale in use; the sum (and into `grown` that
-        // of the weights without their values' scales)
-        float grown = 0.f;
+        // 64 logits to P with the scale in use; the sum
         auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32], int half) {
-          const float off = m == -INFINITY ? 0.f : -m;
-          if (kCodes) {
-            float all = 0.f;
-            grown = 0.f;
-#pragma unroll
-            for (int i = 0; i < kHalf / 16; ++i) {
-              const int e = scale_exp(sc[half * (kHalf / 16) + i].y);
-              const float f = factor(half * (kHalf / 16) + i), o = off + (float)e;
-              const uint64_t f2 = pair(f, f), o2 = pair(o, o);
-              uint64_t sum[2] = {0, 0};
-#pragma unroll
-              for (int k = 8 * i; k < 8 * i + 8; ++k) {
-                const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), f2, o2);
-                const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
-                sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-                p[k] = pack2<kP16>(p0, p1);
-              }
-              sum[0] = add2(sum[0], sum[1]);
-              const float part = lo(sum[0]) + hi(sum[0]);
-              all += part;
-              grown = fmaf(part, exp2i(-e), grown);
-            }
-            return all;
-          }
+          float off = m == -INFINITY ? 0.f : -m;
+          if (kCodes) off += sc.top;
           const uint64_t off2 = pair(off, off);
-          uint64_t sum[2] = {0, 0};
+          uint64_t sum[2] = {0, 0}, f2 = pair(t.c, t.c);
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), c2, off2);
+            if (kCodes && k % (kScaleBlock / 2) == 0) {
+              const float f = c * sc.k[half * (kHalf / kScaleBlock) + k / (kScaleBlock / 2)];
+              f2 = pair(f, f);
+            }
+            const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), f2, off2);
             const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
             sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-            p[k] = pack2<kF16>(p0, p1);
+            p[k] = pack2<kP16>(p0, p1);
           }
           sum[0] = add2(sum[0], sum[1]);
           return lo(sum[0]) + hi(sum[0]);
@@ -842,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           float sum = form(s0, p, 0);
           tmem_wait_ld64(s1);
           if (!__any_sync(0xffffffffu, live && sum > kMost)) {
-            l += kCodes ? grown : sum;
+            l += kCodes ? sum * sc.inv : sum;
             tmem_st32(tS, p);
             arrive(0);
             hand_over(0);
@@ -850,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
             slow = 1;
             if (!__any_sync(0xffffffffu, live && sum > kMost)) {
               hand_over(1);
-              l += kCodes ? grown : sum;
+              l += kCodes ? sum * sc.inv : sum;
               tmem_st32(tS + 32, p);
               arrive(1);
               slow = 2;
@@ -869,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           const uint32_t i = kv0 + 2 * j + 1;
           if (!warp_spin(&kv_full[i % NS], (i / NS) & 1)) { ok = false; break; }
           if (row >= tail) {
-            uint4* v = reinterpret_cast<uint4*>(smem + S::kRing + (i % NS) * S::kTileBytes + (row / 8) * S::kGroup +
+            uint4* v = reinterpret_cast<uint4*>(smem + S::stage(i % NS) + (row / 8) * S::kGroup +
                                                 (row % 8) * 128);
 #pragma unroll 4
             for (int u = 0; u < S::kHalves * 8; ++u) v[(u / 8) * (S::kColumn / 16) + u % 8] = make_uint4(0, 0, 0, 0);
@@ -900,13 +1127,13 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
 #pragma unroll
               for (int k = 0; k < kHalf; ++k) {
                 if (kCodes) {
-                  const int i = half * (kHalf / 16) + k / 16;
-                  mx[k & 3] = fmaxf(mx[k & 3], fmaf(s[k], factor(i), (float)scale_exp(sc[i].y)));
+                  mx[k & 3] = fmaxf(mx[k & 3], s[k] * (c * sc.k[half * (kHalf / kScaleBlock) + k / kScaleBlock]));
                 } else {
                   mx[k & 3] = fmaxf(mx[k & 3], s[k] * t.c);
                 }
               }
-              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              if (kCodes) top += sc.top;
               const bool up = need && top > m;
               const float f = up ? ex2(m - top) : 1.0f;              // m = -inf: 0
               if (up) m = top;
@@ -927,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
                 }
               }
             }
-            l += kCodes ? grown : sum;
+            l += kCodes ? sum * sc.inv : sum;
           }
           tmem_st32(tS + half * 32, p);
           hand_over(half);
@@ -1058,7 +1285,7 @@ template <int D, bool kF16, bool kPaged, bool kCodes>
 cudaError_t launch(const TcAttnArgs& t, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                    const CUtensorMap& o, const Report& rep, int grid, cudaStream_t stream) {
   auto kern = attn_tc_kernel<D, kF16, kPaged, kCodes>;
-  constexpr size_t smem = Shape<D, kPaged>::kSmem;
+  constexpr size_t smem = Shape<D, kPaged, kCodes, kF16>::kSmem;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   kern<<<grid, kThreads<kCodes>, smem, stream>>>(q, k, v, o, t, rep);
@@ -1104,9 +1331,12 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   t.c = a.scale * 1.4426950408889634f;
   // a scale of 0 (or so small that it would flush): so that a masked logit
   // stays one, and every other still counts as 0
-  // (f16 and codes: also times the smallest scale; f16 products stay below 4e9)
-  const float least = a.scales && a.f16 ? 1.2e-30f : 1.2e-38f;
-  if (t.c < least && t.c > -least) t.c = least;
+  if (t.c < 1.2e-38f && t.c > -1.2e-38f) t.c = 1.2e-38f;
+  // codes: factors c 2^(e + e'), kScaleMin <= e' <= kScaleMax, stay normal; where
+  // that raises one its logits still count as 0 (|S| < 2^26, a factor below 2^-94)
+  const int c_exp = std::ilogb(t.c);
+  t.exp_low = -126 - kScaleMin - c_exp;
+  t.exp_high = 127 - kScaleMax - (c_exp > 0 ? c_exp : 0);
   t.hidden = t.c > 0 ? -INFINITY : INFINITY;
   t.part_o = part_o;
   t.part_lse = part_lse;

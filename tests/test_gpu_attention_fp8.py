@@ -71,7 +71,7 @@ def prefill_check(q, q_lens, kv_lens, kc, vc, sc, table, causal, scale, out, lse
     for s, n in enumerate(q_lens):
         k, v = rows(kc, vc, sc, table[s], kv_lens[s])
         seen = ref.causal(n, kv_lens[s], q.device) if causal else None
-        o, le, to, tl = c8.attend(q[at:at + n], k, v, scale, seen)
+        o, le, to, tl = c8.attend(q[at:at + n], k, v, scale, seen, parts=True)
         ref.check(out[at:at + n], o, to, f"out of sequence {s}")
         ref.check(lse[at:at + n], le, tl, f"lse of sequence {s}")
         at += n
@@ -196,6 +196,23 @@ def test_scales_far_apart(dtype):
     decode_check(q, kv_lens, 0, kc, vc, sc, table, None, D ** -0.5, out, lse)
     out = moe.attn_prefill_paged_fp8(q, kc, vc, sc, table, ints([0, 1, 2]), ints(kv_lens), lse=lse)
     prefill_check(q, [1, 1], kv_lens, kc, vc, sc, table, True, D ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF), (64, HF), (128, BF), (128, HF)])
+def test_scales_and_queries_far_apart(D, dtype):
+    """Scales of values from one end of their range to the other within a tile, and rows of queries with one element
+    that is 2^6 to 2^12 times the others."""
+    kv_lens, q_lens, Hq, Hkv, page = [400, 1000], [90, 1], 8, 2, 32
+    kc, vc, sc, table, _ = pool(kv_lens, page, Hkv, D, 61, spread=14)
+    q = rand(gen_of(62), sum(q_lens), Hq, D, dtype=dtype)
+    high = torch.arange(Hq, device="cuda")
+    q[:, high, high * 5] = 2.0 ** (6 + high % 7).to(dtype)
+    scale = 0.25 * D ** -0.5
+    lse = torch.empty(q.shape[0], Hq, device="cuda")
+    out = moe.attn_prefill_paged_fp8(q, kc, vc, sc, table, starts(q_lens), ints(kv_lens), scale=scale, lse=lse)
+    prefill_check(q, q_lens, kv_lens, kc, vc, sc, table, True, scale, out, lse)
+    out = moe.attn_decode_fp8(q[-2:], kc, vc, sc, table, ints(kv_lens), scale=scale, lse=lse[-2:])
+    decode_check(q[-2:], kv_lens, 0, kc, vc, sc, table, None, scale, out, lse[-2:])
 
 
 @pytest.mark.parametrize("mul", [1e-30, 1e-6, 1e6, 1e30])

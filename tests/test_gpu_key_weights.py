@@ -401,7 +401,7 @@ def test_served_from_8_bits(D, page, dtype):
             m = shared + have[s]
             k64, v64 = c8.rows(kc, sc, 0, both[s], m), c8.rows(vc, sc, 1, both[s], m)
             rows = slice(qs[s], qs[s + 1])
-            o, le, to, tl = c8.attend(q[rows], k64, v64, D ** -0.5, ref.causal(chunk[s], m, q.device))
+            o, le, to, tl = c8.attend(q[rows], k64, v64, D ** -0.5, ref.causal(chunk[s], m, q.device), parts=True)
             ref.check(out[rows], o, to, "prompt rows")
             ref.check(lse[rows], le, tl, "their log-sums")
     for _ in range(4):
