@@ -232,7 +232,9 @@ def attn_decode(q, k_cache, v_cache, page_table, kv_lens, prefix_table=None, pre
 def attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal=True, scale=None,
                            out=None, lse=None, workspace=None, stream=None):
     """``attn_prefill_paged`` over a cache in 8 bits (``alloc_fp8_cache``):
-    codes are multiplied exactly, sums and softmax statistics are fp32."""
+    codes are multiplied as they are, sums and softmax statistics are fp32.
+    Elements of a query head below 2^-9.8 of its largest (f16: 2^-6.8) are
+    rounded, to 2^-17.8 of that; a head that holds an infinity gives NaN."""
     return _load().attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal, scale,
                                           out, lse, workspace, stream)
 
@@ -240,8 +242,8 @@ def attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv
 def attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table=None, prefix_len=0, scale=None,
                     out=None, lse=None, workspace=None, stream=None):
     """``attn_decode`` over a cache in 8 bits (``alloc_fp8_cache``), its shared
-    prefix there too: codes are multiplied exactly, sums and softmax
-    statistics are fp32."""
+    prefix there too (with the roundings of ``attn_prefill_paged_fp8``): codes
+    are multiplied as they are, sums and softmax statistics are fp32."""
     return _load().attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table, prefix_len, scale,
                                    out, lse, workspace, stream)
 

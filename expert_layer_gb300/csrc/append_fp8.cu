@@ -152,7 +152,7 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
     {
 #pragma unroll
       for (int x = 0; x < kMaxAxes; ++x) mine.p[x] = 0;
-      if (!value && lane >= r0 && lane < r1) placed = mine.load(a, axes, q0 + first + lane - fresh);
+      if (lane >= r0 && lane < r1) placed = mine.load(a, axes, q0 + first + lane - fresh);
       if (!placed) {
         bad = true;
 #pragma unroll
@@ -194,6 +194,7 @@ __device__ __forceinline__ bool append_blocks(const RopeFp8Args& f, const bool a
     for (int p = p0; p < p1; ++p) {
       uint64_t y[kPart];
       row_values(p, y);
+      if ((lost >> (p * kRows + sub)) & 1) continue;
 #pragma unroll
       for (int j = 0; j < kPart; ++j) top = fmaxf(top, fmaxf(fabsf(lo(y[j])), fabsf(hi(y[j]))));   // NaN is passed over
     }

@@ -1334,7 +1334,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int splits, float* part_o, float* 
   if (t.c < 1.2e-38f && t.c > -1.2e-38f) t.c = 1.2e-38f;
   // codes: factors c 2^(e + e'), kScaleMin <= e' <= kScaleMax, stay normal; where
   // that raises one its logits still count as 0 (|S| < 2^26, a factor below 2^-94)
-  const int c_exp = std::ilogb(t.c);
+  const int c_exp = std::isfinite(t.c) ? std::ilogb(t.c) : 127;
   t.exp_low = -126 - kScaleMin - c_exp;
   t.exp_high = 127 - kScaleMax - (c_exp > 0 ? c_exp : 0);
   t.hidden = t.c > 0 ? -INFINITY : INFINITY;

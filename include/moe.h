@@ -530,8 +530,11 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
 
 /*
  * moe_attn_prefill_paged and moe_attn_decode over a cache in 8 bits; queries
- * and outputs are bf16 or f16, codes are multiplied exactly, every sum and
- * softmax statistic is fp32.
+ * and outputs are bf16 or f16, codes are multiplied as they are, every sum and
+ * softmax statistic is fp32.  Elements of a query head far below its largest
+ * are rounded: prefill, those below 2^-9.8 of it (f16: 2^-6.8) to 2^-17.8 of it;
+ * decode, bf16, those below 2^-28 of it to 2^-39.  In prefill a query head that
+ * holds an infinity gives NaN.
  */
 int moe_attn_prefill_paged_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,
                                const int32_t *page_table, int table_pages, const int32_t *q_starts,

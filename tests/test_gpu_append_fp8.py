@@ -336,6 +336,30 @@ def test_what_is_out_of_range_is_reported_and_left():
     assert status == MOE_ERR_DEVICE and same(got, clean, 0) and same(got, clean, 2)
 
 
+def test_a_token_without_a_position_leaves_its_row_and_the_scales():
+    """Its key and its value stay as they were, as in the 16-bit append, and its size counts for no scale."""
+    case = ([5, 20, 40], [30, 9, 3], 4, 2, 64, 32, False, False, 1, 16, BF)
+    q, k, v, table, pos, pages, qs, lens, kc, vc, sc, (qn, kn), axes = append_case(case)
+    k, v = k.contiguous(), v.contiguous()
+    k[35], v[35] = 0, 0                                      # sequence 1: its token 25, on page 1, row 9
+    clean = [x.clone() for x in (kc, vc, sc)]
+    moe.rope_append_fp8(q, k, v, table, pos, pages, qs, lens, *clean)
+    k[35], v[35] = 3000, -3000
+    bad = pos.clone()
+    bad[35] = -1
+    ws = moe.alloc_attn_workspace(q.shape[0], 3, 4, 2, 64)
+    got = [x.clone() for x in (kc, vc, sc)]
+    moe.rope_append_fp8(q, k, v, table, bad, pages, qs, lens, *got, workspace=ws)
+    assert moe.read_status(ws) == MOE_ERR_DEVICE
+    assert torch.equal(got[2], clean[2])
+    for x, y, before in zip(got, clean, (kc, vc)):
+        x, y, before = (t.view(torch.uint8).clone() for t in (x, y, before))
+        p = int(pages[1, 1])
+        assert torch.equal(x[p, :, 9], before[p, :, 9])
+        x[p, :, 9] = y[p, :, 9]
+        assert torch.equal(x, y)
+
+
 def test_captured_and_on_another_stream():
     case = APPEND[2]
     q, k, v, table, pos, pages, qs, lens, kc, vc, sc, (qn, kn), axes = append_case(case)
