@@ -201,6 +201,10 @@ EVICT = [
     ([3000, 2500], 1000, 0, 5, 4, 128, 16, BF, "odd", 7),
     ([20000], 3000, 4, 64, 2, 128, 64, BF, "near", 0),                   # differ in the last bits alone
     ([60] * 1100, 20, 1, 2, 2, 64, 16, BF, "tail", 0),                   # more heads than blocks of the grid
+    ([9000, 16384, 4097, 16383], 2900, 4, 64, 2, 64, 64, BF, "tail", 0),  # long, counted in registers
+    ([16000, 6000, 2050], 2000, 0, 0, 1, 128, 128, HF, "odd", 9),
+    ([12000, 8192], 777, 2, 1, 2, 64, 16, BF, "near", 0),
+    ([16384, 3500], 1500, 1, 0, 2, 64, 256, BF, "few", 0),
 ]
 
 
