@@ -59,10 +59,9 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
       : "r"(w));
   return v;
 }
-// Two elements
-template <bool kF16>
-__device__ __forceinline__ float2 floats2(uint32_t w) {
-  return kF16 ? half2_floats(w) : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+// Two bf16 elements
+__device__ __forceinline__ float2 bf16_floats(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 // Two fp32 values in one 64-bit register and the paired operations on them
 __device__ __forceinline__ uint64_t pair(float a, float b) {

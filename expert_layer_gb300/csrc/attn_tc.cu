@@ -246,16 +246,23 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t code_pair(float a, float b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("{\n .reg .b16 l;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.u32.u16 %0, l;\n}" : "=r"(r) : "f"(a), "f"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Four elements' codes; y becomes what they leave
-__device__ __forceinline__ uint32_t take_part(float (&y)[4]) {
-  const uint32_t w = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
-  const float2 a = half2_floats(codes2<0>(w)), b = half2_floats(codes2<1>(w));
-  y[0] -= a.x, y[1] -= a.y, y[2] -= b.x, y[3] -= b.y;
+// Codes of four f16 elements; y becomes what they leave (exact)
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&y)[2]) {
+  uint32_t w;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n mov.b32 %0, {l, h};\n}"
+      : "=r"(w)
+      : "r"(y[0]), "r"(y[1]));
+  return w;
+}
+__device__ __forceinline__ uint32_t take_part(uint32_t (&y)[2]) {
+  const uint32_t w = codes_of(y);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y[0]) : "r"(codes2<0>(w)));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y[1]) : "r"(codes2<1>(w)));
   return w;
 }
 __device__ __forceinline__ void sts4(uint32_t addr, const uint32_t (&w)[4]) {
@@ -280,10 +287,14 @@ __device__ __forceinline__ void split_rows(uint32_t tile, uint32_t third, int8_t
     most = max(most & 0xffffu, most >> 16);
     if (kLanes == 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, kStep));
     const uint32_t top = kF16 ? __float_as_uint(half2_floats(most).x) : most << 16;
-    // the smallest e with top <= 448 2^e (448 = 1.75 2^8); 2^-e stays normal
-    const int e = max(-126, (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
-    const float by = top < 0x7f800000u ? exp2i(-e) : __uint_as_float(0x7fffffffu);
-    uint32_t hi[4][4], lo[4][4];
+    // the smallest e with top <= 448 2^e (448 = 1.75 2^8); 2^-e stays normal (f16: 2^-24 takes -32)
+    const int e = max(kF16 ? -32 : -126, (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
+    const bool finite = top < 0x7f800000u;
+    const float by = finite ? exp2i(-e) : __uint_as_float(0x7fffffffu);
+    // f16: 2^-e, -8 <= -e <= 32, in factors
+    const uint32_t f1 = finite ? (uint32_t)(15 + max(-8, min(-e, 15))) << 10 : 0x7fffu;
+    const uint32_t f2 = (uint32_t)(15 + max(0, min(-e - 15, 15))) << 10, f3 = (uint32_t)(15 + max(0, -e - 30)) << 10;
+    uint32_t high[4][4], low[4][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t w[8] = {raw[2 * k].x,     raw[2 * k].y,     raw[2 * k].z,     raw[2 * k].w,
@@ -291,29 +302,34 @@ __device__ __forceinline__ void split_rows(uint32_t tile, uint32_t third, int8_t
       uint32_t last[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float2 a = floats2<kF16>(w[2 * u]), b = floats2<kF16>(w[2 * u + 1]);
-        float y[4] = {a.x * by, a.y * by, b.x * by, b.y * by};
-        hi[k][u] = take_part(y);
-        if (kF16) lo[k][u] = take_part(y), last[u] = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
-        else lo[k][u] = code_pair(y[0], y[1]) | code_pair(y[2], y[3]) << 16;
+        // (in f16: the 8 bits of bf16 fit, and 2^-24 is far below the last part's 2^-9)
+        uint32_t y[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (kF16) {
+            y[v] = mul_f16x2(mul_f16x2(w[2 * u + v], f1 | f1 << 16), f2 | f2 << 16);
+            if (f3 != 0x3c00u) y[v] = mul_f16x2(y[v], f3 | f3 << 16);
+          } else {
+            const float2 q = bf16_floats(w[2 * u + v]);
+            const uint64_t x = mul2(pair(q.x, q.y), pair(by, by));
+            y[v] = pack2<true>(lo(x), hi(x));
+          }
+        }
+        high[k][u] = take_part(y);
+        if (kF16) low[k][u] = take_part(y), last[u] = codes_of(y);
+        else low[k][u] = codes_of(y);
       }
       if (kF16) sts4(third + r * 128 + (((h * 4 + k) ^ (r & 7)) * 16), last);
     }
     __syncwarp();                                              // a row's lanes have read it
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      sts4(row + (((h * 4 + k) ^ (r & 7)) * 16), hi[k]);
-      if (D == 128) sts4(row + kRows * 128 + (((h * 4 + k) ^ (r & 7)) * 16), lo[k]);
-      else sts4(row + (((4 + k) ^ (r & 7)) * 16), lo[k]);
+      sts4(row + (((h * 4 + k) ^ (r & 7)) * 16), high[k]);
+      if (D == 128) sts4(row + kRows * 128 + (((h * 4 + k) ^ (r & 7)) * 16), low[k]);
+      else sts4(row + (((4 + k) ^ (r & 7)) * 16), low[k]);
     }
     if (h == 0) exps[r] = (int8_t)e;
   }
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // ------------------------------------------------------------------ work items
