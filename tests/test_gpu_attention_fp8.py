@@ -245,6 +245,26 @@ def test_nan_stays_with_its_rows():
     check(moe.attn_decode_fp8(q[::3].contiguous(), kc, vc, sc, table, ints(kv_lens)))
 
 
+@pytest.mark.parametrize("D,dtype", [(64, BF), (64, HF), (128, BF), (128, HF)])
+def test_an_infinite_query_stays_with_its_head(D, dtype):
+    kv_lens, q_lens, Hq, Hkv, page = [300, 40], [70, 40], 8, 2, 16
+    kc, vc, sc, table, _ = pool(kv_lens, page, Hkv, D, 83)
+    q = rand(gen_of(84), sum(q_lens), Hq, D, dtype=dtype)
+    q[3] = 0                                                      # rows of zeros are rows like others
+
+    def call():
+        return moe.attn_prefill_paged_fp8(q, kc, vc, sc, table, starts(q_lens), ints(kv_lens))
+    want = call()
+    assert not want.isnan().any()
+    for at, x in ((5, float("inf")), (33, -float("inf")), (80, float("nan"))):
+        q[at, 2, at % D] = x
+    got = call()
+    for at in (5, 33, 80):
+        assert got[at, 2].isnan().all()
+        got[at, 2] = want[at, 2]
+    assert torch.equal(got, want)
+
+
 def test_what_is_out_of_range_is_reported():
     kv_lens, q_lens, Hq, Hkv, D, page = [100, 50, 70], [3, 5, 2], 4, 2, 64, 16
     kc, vc, sc, table, pre = pool(kv_lens, page, Hkv, D, 91, prefix=40)
