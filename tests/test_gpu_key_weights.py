@@ -432,3 +432,41 @@ def test_key_weights_waits_that_give_up(wait, D):
     ws = moe.alloc_attn_workspace(100, 2, Hq, Hkv, D)
     waits.times_out(lambda: moe.attn_key_weights(q, kc, table, starts(q_lens), ints(kv_lens), lse,
                                                  torch.zeros(2, Hkv, 900, device="cuda"), workspace=ws), ws, wait)
+
+
+def test_offsets_beyond_32_bits():
+    """The same calls with a sequence's pages at the start of a cache of more than 2^32 elements and at its end: the same
+    bits."""
+    Hq, Hkv, D, page, n = 16, 8, 128, 256, 700
+    pages = (1 << 32) // (Hkv * page * D) + 12
+    low, spare = ints([[1, 4, 2]]), ints([[6]])
+    high, high_spare = low + (pages - 8), spare + (pages - 8)
+    g = gen_of(41)
+    table = moe.rope_table(1024, D)
+    q, k, v = (rand(g, n, h, D) for h in (Hq, Hkv, Hkv))
+    qs, lens, pos = ints([0, n]), ints([n]), torch.arange(n, dtype=torch.int32, device="cuda")
+    k8, v8 = (torch.empty(pages, Hkv, page, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    sc = torch.empty(pages, Hkv, page // 16, 2, device="cuda")
+    got = []
+    for t in (low, high):
+        x = moe.rope_append_fp8(q, k, v, table, pos, t, qs, lens, k8, v8, sc)
+        ws = moe.alloc_attn_workspace(n, 1, Hq, Hkv, D)
+        got.append([moe.attn_prefill_paged_fp8(x, k8, v8, sc, t, qs, lens, workspace=ws),
+                    moe.attn_decode_fp8(x[-1:], k8, v8, sc, t, lens)])
+        assert moe.read_status(ws) == 0 and not any(o.isnan().any() for o in got[-1])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    del k8, v8, sc
+    kc, vc = (torch.empty(pages, Hkv, page, D, dtype=BF, device="cuda") for _ in range(2))
+    got = []
+    for t, to in ((low, spare), (high, high_spare)):
+        slots = (t[0].long()[pos.long() // page] * page + pos.long() % page).to(torch.int32)
+        x = moe.rope_append(q, k, v, table, pos, slots, kc, vc)
+        lse = torch.empty(n, Hq, device="cuda")
+        moe.attn_prefill_paged(x, kc, vc, t, qs, lens, lse=lse)
+        many, few = torch.zeros(1, Hkv, n, device="cuda"), torch.zeros(1, Hkv, n, device="cuda")
+        moe.attn_key_weights(x, kc, t, qs, lens, lse, many)
+        moe.attn_key_weights(x[-3:], kc, t, ints([0, 3]), lens, lse[-3:], few)
+        out = moe.kv_evict(kc, vc, t, lens, many, to, 200, 4, 30)
+        got.append([many, few, *out, kc[int(to)].clone()[:, :200], vc[int(to)].clone()[:, :200]])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert bool((got[0][0] > 0).any()) and int(got[0][2]) == 200
