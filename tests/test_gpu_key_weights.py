@@ -205,6 +205,7 @@ EVICT = [
     ([16000, 6000, 2050], 2000, 0, 0, 1, 128, 128, HF, "odd", 9),
     ([12000, 8192], 777, 2, 1, 2, 64, 16, BF, "near", 0),
     ([16384, 3500], 1500, 1, 0, 2, 64, 256, BF, "few", 0),
+    ([0, 5000, 90, 4097, 90] + [200 + 7 * i % 300 for i in range(45)], 150, 3, 9, 4, 64, 16, BF, "tail", 0),  # two to an SM
 ]
 
 
