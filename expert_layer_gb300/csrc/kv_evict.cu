@@ -12,8 +12,9 @@
 // pages that sequences share as they were.
 // Bound: HBM for the copy (8 D bytes a kept key and head), latency for the first:
 // 64 sequences, 4 heads of 128, 16,384 keys at most, 1024 kept: 62 us, the copy 34
-// of them; the first kernel's time is that of the SMs that
-// hold two long items.  One kernel for both: 90 us, rows wait for their search.
+// of them; the first kernel's time is the chain of a long item, up to 16 counts
+// with a barrier each (long and short items paired on the SMs: equal).  One kernel
+// for both: 90 us, rows wait for their search.
 #include "attn.h"
 #include "attn_ptx.cuh"
 
