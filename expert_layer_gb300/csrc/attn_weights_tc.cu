@@ -52,7 +52,7 @@ struct Unit {
   int t0, tiles;       // first row tile that sees a key, and their number
 };
 struct RowMeta {
-  int whole;           // every row is one of the sequence's, with keys
+  int whole;           // each of the tt G rows is one of the sequence's, with keys
   int least;           // the first key that some row does not see, less one
 };
 
@@ -334,7 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float4* off = reinterpret_cast<const float4*>(smem + S::kRowsAt + rs * 1024);
         const int4* lim = reinterpret_cast<const int4*>(off + kRows / 4);
         const int parts = active ? (min(tt, it.n - t * tt) * G + 31) / 32 : 0;      // of 32 rows
-        const bool plain = m.whole && m.least >= first + 127;
+        // parts without a masked row; the rows from tt G on, which are zeros, count as
+        // masked (times a key's infinity they are NaN)
+        const int plain = m.whole && m.least >= first + 127 ? tt * G / 32 : 0;
 #pragma unroll 1
         for (int part = 0; part < parts; ++part) {
           float s[32];
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[p]);
           }
-          if (plain) {
+          if (part < plain) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float4 o = off[part * 8 + k];
