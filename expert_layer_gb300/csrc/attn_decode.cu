@@ -40,6 +40,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSlice = 16;          // keys
 constexpr int kWindow = kThreads;   // sequences whose lengths a block keeps in shared memory
 constexpr float kLag = 8.0f;        // log2 of how far the maximum in use may lag
+// Codes: and of how far it may lie above a slice's largest weight times value scale
+// before it comes down to that, but not below 2^-kReach of the largest so far: O stays
+// below 2^(kReach + 8) * 448 * keys, l below 2^(kReach + 8 + 24) * keys.
+constexpr float kDrop = 4.0f, kReach = 64.0f;
 
 template <int D, bool kWide, bool kCodes>
 struct Shape {
@@ -413,12 +417,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kWide && nxt.pos < we) load_q(nxt, qn);
       float o[kTiles][4];
       float m[kSets], l[kSets];
+      float most[kSets];                             // codes: the largest m so far
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
 #pragma unroll
-      for (int rs = 0; rs < kSets; ++rs) m[rs] = -INFINITY, l[rs] = 0.f;
+      for (int rs = 0; rs < kSets; ++rs) m[rs] = most[rs] = -INFINITY, l[rs] = 0.f;
 
 #pragma unroll 1
       for (int s = first; s < last; ++s) {
@@ -490,19 +495,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) wv[k][i] = 0;
           }
-          bool up = false;
+          // The scale 2^m of a head's P follows its slices up and down, so that what a slice
+          // of small values adds is not lost in f16 beside a larger scale before it (of
+          // which a large value without weight, or a heavy key without a value, is enough).
+          bool move = false;
 #pragma unroll
-          for (int x = 0; x < kSets; ++x) up |= fmaf(fmaxf(y[x][0], y[x][1]), slice_c[x], shift) > m[x] + kLag;
-          if (__any_sync(0xffffffffu, up)) {
+          for (int x = 0; x < kSets; ++x) {
+            const float own = fmaf(fmaxf(y[x][0], y[x][1]), slice_c[x], shift);
+            move |= own > m[x] + kLag;
+            // (the eight lanes of a quad's place have the heads' keys)
+            move |= (__ballot_sync(0xffffffffu, own >= m[x] - kDrop) & (0x11111111u << quad)) == 0;
+          }
+          if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int x = 0; x < kSets; ++x) {
               float top = fmaxf(y[x][0], y[x][1]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
               top = fmaf(top, slice_c[x], shift);
-              const bool g = top > m[x] + kLag;
-              const float f = g ? ex2(m[x] - top) : 1.0f;
-              if (g) m[x] = top;
+              float to = m[x];
+              if (top > m[x] + kLag) to = top;
+              if (top < m[x] - kDrop && top > most[x] - kReach - 24.0f) to = fminf(m[x], fmaxf(top, most[x] - kReach));
+              const float f = to == m[x] ? 1.0f : ex2(m[x] - to);    // m = -inf: 0
+              m[x] = to;
+              most[x] = fmaxf(most[x], to);
               l[x] *= f;
 #pragma unroll
               for (int i = 0; i < kCols / 2; ++i) {
