@@ -75,19 +75,12 @@ constexpr int kHalf = kKeys / 2;
 constexpr float kMost = 32768.0f;   // sum of a row's P over half a block that asks for a new scale
 constexpr uint32_t kTmemCols = 512;
 
-// Scales of a block of codes: K's, of 16 keys; V's are 2^(top - down), top: the
-// largest of those of keys that there are.  `down` comes with V, the rest with K.
+// Scales of a block of codes, of 16 keys each: K's, and V's as two f16 elements.
+// Each is written by the warp that loads those codes.
 struct __align__(16) Scales {
   float k[kScaleBlocks];
-  int down[kScaleBlocks];
-  float top, inv;                  // inv: 2^-top
+  uint32_t v[kScaleBlocks];
 };
-// Lane i has the scale of V of 16 keys of block b; all lanes of the warp take part
-__device__ __forceinline__ int top_exp(float scale, int b, int len) {
-  const int lane = threadIdx.x & 31;
-  const bool there = lane < kScaleBlocks && b * kKeys + lane * kScaleBlock < len;
-  return __reduce_max_sync(0xffffffffu, there ? scale_exp(scale) : kScaleMin);
-}
 // Scales in the cache of lane i's 16 keys of block b, whose page is `page`, and that
 // page (-1: none).  Pages out of range are reported where codes are loaded.
 __device__ __forceinline__ float2 load_scales(const AttnArgs& a, int b, int page, int head) {
@@ -250,6 +243,20 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+// 2^e as two f16 elements, -24 <= e <= 15 (subnormal below 2^-14)
+__device__ __forceinline__ uint32_t f16_scale(int e) {
+  const uint32_t h = e < -14 ? 1u << (e + 24) : (uint32_t)(e + 15) << 10;
+  return h | h << 16;
+}
+// Two f16 elements that hold codes times two that hold a scale, as bf16 (exact)
+__device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
+  float x, y;
+  asm("{\n .reg .b16 l, h, f, g;\n mov.b32 {l, h}, %2;\n mov.b32 {f, g}, %3;\n fma.rn.f32.f16 %0, l, f, 0f00000000;\n"
+      " fma.rn.f32.f16 %1, h, g, 0f00000000;\n}"
+      : "=f"(x), "=f"(y)
+      : "r"(a), "r"(b));
+  return pack2<false>(x, y);
 }
 // Codes of four f16 elements; y becomes what they leave (exact)
 __device__ __forceinline__ uint32_t codes_of(const uint32_t (&y)[2]) {
@@ -441,19 +448,13 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // and four more warps (12-15) make the queries parts in e4m3 (split_rows).  A
 // row's scale and that of 16 keys, both powers of two, join the factor of the
 // logits.  V's codes land in the upper half of their stage, and the same warps
-// make them f16, in place: every code is in registers before the first element
-// is written.  They take the tile's largest scale 2^e out, which joins the
-// exponent of P instead,
-//   P = 2^{c S + e - m'},  O += P (V 2^-e),  l += 2^{-e} sum P,
-// so that m' follows what a tile adds to O, and P and the values stay within f16
-// whatever the scales: a value is off by at most 2^-25 of 2^e, 2^-32 of the tile's
-// largest.  (Both K and V made bf16 or f16 by those warps, and a scale of V for
-// each 16 keys in the softmax: 4096 rows over 8192 keys, bf16, 408 us; K as codes
-// 348; scales from the loading warps, one of V for the tile 326; now 321.  K and V
-// in bf16 take 250: the four warps' work on a tile of V, ~1200 cycles beside the
-// softmax, is what is left, and what they do not have to do shows: V's codes by
-// shifts in place of conversions, which share a pipe with the exponentials, but
-// are more instructions, 384.)
+// make them elements of the call's type, in place: every code is in registers
+// before the first element is written.  code * 2^e is exact in bf16; in f16 it
+// is on a grid of 2^-24, which is the outputs' too (and whatever was appended from
+// f16 lies on it).  So P and V round as over a 16-bit cache, whatever the scales
+// of other keys.  (P in f16 with a tile's largest scale in its exponent, and the
+// values in f16 under that scale, lost what keys of small scales add beside a
+// large one, and let a row depend on keys that it does not see.)
 template <int D, bool kF16, bool kPaged, bool kCodes>
 __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -461,7 +462,6 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
                    const Report rep) {
   using S = Shape<D, kPaged, kCodes, kF16>;
   constexpr int NS = S::kStages;
-  constexpr bool kP16 = kF16 || kCodes;                        // P and V in f16 (else bf16)
   static_assert(kPaged || !kCodes, "codes are paged");
   extern __shared__ __align__(1024) unsigned char smem[];      // swizzle atoms of 1 KB
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::kBars);
@@ -657,12 +657,9 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           if (!ok) break;
           if (kCodes) {
             // Slot of block j: both softmaxes are done with block j - kScaleSlots, as
-            // both tiles have had S of block j - NS / 2 (the slot's `down` is V's)
+            // both tiles have had S of block j - NS / 2 (the slot's `v` comes with V)
             static_assert(NS / 2 < kScaleSlots, "slots of scales");
-            const int top = top_exp(sc.y, b, it.len);
-            Scales& to = scales[(kv / 2) % kScaleSlots];
-            if (lane < kScaleBlocks) to.k[lane] = exp2i(scale_exp(sc.x));
-            if (lane == 0) to.top = (float)top, to.inv = exp2i(-top);
+            if (lane < kScaleBlocks) scales[(kv / 2) % kScaleSlots].k[lane] = exp2i(scale_exp(sc.x));
             __syncwarp();
           }
           if (lane == 0) {
@@ -714,7 +711,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     // The whole warp runs the loop on values that are uniform to the compiler
     // (constants, loop counters, results of warp reductions); one elected lane
     // issues.
-    constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kP16>(D, true);
+    constexpr uint32_t kIdS = idesc_of<kF16>(kKeys, false), kIdO = idesc_of<kF16>(D, true);
     const int x = __reduce_max_sync(0xffffffffu, warp - kSoftWarps - 1);      // tile
     const uint32_t tS = x * kKeys, tO = 2 * kKeys + x * D;   // all 512 columns: the allocation starts at 0
     const uint32_t s0 = smem_u32(smem), sQ = s0 + x * S::kTileBytes;
@@ -862,8 +859,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
         const int nbox = min(boxes, (len - b * kKeys + t.box - 1) / t.box);
         ok = warp_spin(&kv_empty[s], ((kv / NS) & 1) ^ 1);
         if (!ok) break;
-        const int top = top_exp(sc.y, b, len);
-        if (lane < kScaleBlocks) scales[(kv / 2) % kScaleSlots].down[lane] = max(0, top - scale_exp(sc.y));
+        if (lane < kScaleBlocks) scales[(kv / 2) % kScaleSlots].v[lane] = f16_scale(scale_exp(sc.y));
         __syncwarp();
         if (lane == 0) mbar_expect_tx(&code_full[s], (uint32_t)(nbox * t.box * D));
         __syncwarp();
@@ -951,23 +947,13 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
         const Scales& sc = scales[(kv / 2 - 1) % kScaleSlots];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          // 2^-down in two factors (the first product is exact; the second factor is
-          // subnormal from 2^-15 on, down is at most kScaleMax - kScaleMin = 31)
-          const int down = sc.down[cw * 2 + g / 2];
-          const uint32_t by = (uint32_t)(15 - min(down, 14)) << 10, by2 = by | by << 16;
-          const int rest = down - 14;
-          const uint32_t more = rest > 14 ? 0x400u >> (rest - 14) : (uint32_t)(15 - max(rest, 0)) << 10;
-          const uint32_t more2 = more | more << 16;
+          const uint32_t by = sc.v[cw * 2 + g / 2];
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             const int rr = r0 + i * (32 / kRowPieces);
             uint32_t e[4] = {codes2<0>(raw[g][i].x), codes2<1>(raw[g][i].x), codes2<0>(raw[g][i].y), codes2<1>(raw[g][i].y)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) e[k] = mul_f16x2(e[k], by2);
-            if (down > 14) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) e[k] = mul_f16x2(e[k], more2);
-            }
+            for (int k = 0; k < 4; ++k) e[k] = kF16 ? mul_f16x2(e[k], by) : times_bf16(e[k], by);
             sts4(tile + (cw * 4 + g) * S::kGroup + (c / 8) * 1024 + rr * 128 + ((c % 8) ^ rr) * 16, e);
           }
         }
@@ -1048,14 +1034,12 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 16; ++k) top = fmaxf(top, k < lim ? u[k] * (kCodes ? c * sc.k[0] : t.c) : -INFINITY);
-          if (kCodes) top += sc.top;
           if (m == -INFINITY) m = top;
           unset = __any_sync(0xffffffffu, live && m == -INFINITY);
         }
         // 64 logits to P with the scale in use; the sum
         auto form = [&](const float (&s)[kHalf], uint32_t (&p)[32], int half) {
-          float off = m == -INFINITY ? 0.f : -m;
-          if (kCodes) off += sc.top;
+          const float off = m == -INFINITY ? 0.f : -m;
           const uint64_t off2 = pair(off, off);
           uint64_t sum[2] = {0, 0}, f2 = pair(t.c, t.c);
 #pragma unroll
@@ -1067,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
             const uint64_t y = fma2(pair(s[2 * k], s[2 * k + 1]), f2, off2);
             const float p0 = ex2(lo(y)), p1 = ex2(hi(y));
             sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-            p[k] = pack2<kP16>(p0, p1);
+            p[k] = pack2<kF16>(p0, p1);
           }
           sum[0] = add2(sum[0], sum[1]);
           return lo(sum[0]) + hi(sum[0]);
@@ -1085,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
           float sum = form(s0, p, 0);
           tmem_wait_ld64(s1);
           if (!__any_sync(0xffffffffu, live && sum > kMost)) {
-            l += kCodes ? sum * sc.inv : sum;
+            l += sum;
             tmem_st32(tS, p);
             arrive(0);
             hand_over(0);
@@ -1093,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
             slow = 1;
             if (!__any_sync(0xffffffffu, live && sum > kMost)) {
               hand_over(1);
-              l += kCodes ? sum * sc.inv : sum;
+              l += sum;
               tmem_st32(tS + 32, p);
               arrive(1);
               slow = 2;
@@ -1148,8 +1132,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
                   mx[k & 3] = fmaxf(mx[k & 3], s[k] * t.c);
                 }
               }
-              float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              if (kCodes) top += sc.top;
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               const bool up = need && top > m;
               const float f = up ? ex2(m - top) : 1.0f;              // m = -inf: 0
               if (up) m = top;
@@ -1170,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads<kCodes>, 1)
                 }
               }
             }
-            l += kCodes ? sum * sc.inv : sum;
+            l += sum;
           }
           tmem_st32(tS + half * 32, p);
           hand_over(half);

@@ -120,7 +120,7 @@ def set_scale(sc, table, s, block, head, which, exponent):
 
 
 SHAPES = [(64, BF), (64, HF), (128, BF), (128, HF)]
-KERNELS = ["decode"]
+KERNELS = ["decode", "prefill"]
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
@@ -160,6 +160,23 @@ def test_blocks_of_zeros_under_a_large_scale(kernel, D, dtype):
                 for j in range(16 * b, min(16 * b + 16, m)):
                     put(vc, table, s, j, 0, (slice(None), 0.0))
     check(kernel, q, kc, vc, sc, table, q_lens, kv_lens)
+
+
+@pytest.mark.parametrize("D,dtype", SHAPES)
+@pytest.mark.parametrize("order", ["small first", "large first"])
+def test_a_row_does_not_depend_on_later_tokens(D, dtype, order):
+    """Causal rows of one block of keys: the first 64 tokens' values have the smallest scale, those behind them the
+    largest (and the other way round)."""
+    n, Hq, Hkv, page = 128, 8, 2, 16
+    q, kc, vc, sc, table = setup([n], [n], Hq, Hkv, D, page, dtype, 121)
+    for h in range(Hkv):
+        for b in range(n // 16):
+            set_scale(sc, table, 0, b, h, 1, (-24 if b < 4 else 7) if order == "small first" else (7 if b < 4 else -24))
+    check("prefill", q, kc, vc, sc, table, [n], [n])
+    # and the first rows are the same as of a call without the others
+    some = moe.attn_prefill_paged_fp8(q, kc, vc, sc, table, ints([0, n]), ints([n]))[:64]
+    alone = moe.attn_prefill_paged_fp8(q[:64].contiguous(), kc, vc, sc, table, ints([0, 64]), ints([64]))
+    assert torch.equal(some, alone)
 
 
 @pytest.mark.parametrize("kernel", KERNELS)
