@@ -273,7 +273,8 @@ def kv_evict(k_cache, v_cache, page_table, kv_lens, weights, out_table, budget, 
 
     Returns (new_lens int32 [n_seq], new_weights fp32 [n_seq, Hkv, budget],
     kept int32 [n_seq, Hkv, budget]): min(kv_lens, budget), the weights of the
-    kept keys (0 behind them) and their places before (-1 behind them).  Keys
+    kept keys (0 behind them) and their places before (-1 behind them).
+    ``new_lens`` may be ``kv_lens`` itself.  Keys
     keep the positions they were rotated by; a sequence's next token goes on
     counting from its own position, and its slot from new_lens."""
     return _load().kv_evict(k_cache, v_cache, page_table, kv_lens, weights, out_table, budget, keep_first, keep_last,

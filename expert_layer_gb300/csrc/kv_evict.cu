@@ -30,6 +30,13 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Keys of a sequence; none (and `bad`) where its length is out of range
+__device__ __forceinline__ int keys_of(const EvictArgs& a, int s, bool& bad) {
+  int n = a.kv_lens[s];
+  if (n < 0 || n > a.capacity || n > ((long long)a.table_pages << a.page_shift)) bad = true, n = 0;
+  return n;
+}
+
 // Sum over the threads before this one, and over all
 template <int kWarps>
 __device__ __forceinline__ int block_scan(int v, int* warps, int& total) {
@@ -69,13 +76,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
   pdl_trigger();                            // the copy kernel waits for this grid's end
   for (int item = blockIdx.x; item < a.n_seq * a.Hkv; item += gridDim.x) {
     const int s = a.by_Hkv.of(item), head = item - s * a.Hkv;
-    int n = a.kv_lens[s];
-    if (n < 0 || n > a.capacity || n > ((long long)a.table_pages << a.page_shift)) bad = true, n = 0;
+    const int n = keys_of(a, s, bad);
     const float* w = a.weights + (long long)item * a.capacity;
     float* to = a.new_weights + (long long)item * a.budget;
     int32_t* kept = a.kept + (long long)item * a.budget;
     const int m = min(n, a.budget);
-    if (head == 0 && threadIdx.x == 0) a.new_lens[s] = m;
     for (int i = m + threadIdx.x; i < a.budget; i += kThreads) {
       to[i] = 0.f;
       kept[i] = -1;
@@ -302,18 +307,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
   if (threadIdx.x == 0) report(rep, blockIdx.x, any ? kStatusBounds : 0);
 }
 
-// Rows of the kept keys, 16 bytes of K and of V per thread
+// Rows of the kept keys, 16 bytes of K and of V per thread.  A last block writes the
+// new lengths, when every head's selection has read the old ones: they may be one array.
 constexpr int kCopyThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictArgs a, const Report rep) {
   constexpr int kLanes = D / 8;
   pdl_wait();
   bool bad = false;
+  if (blockIdx.x == gridDim.x - 1) {                 // (what is out of range has been reported)
+    for (int s = threadIdx.x; s < a.n_seq; s += kCopyThreads) a.new_lens[s] = min(keys_of(a, s, bad), a.budget);
+    return;
+  }
   const int lane = threadIdx.x % kLanes;
   const long long rows = (long long)a.n_seq * a.Hkv * a.budget;
   const int in_page = (1 << a.page_shift) - 1;
   for (long long r = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) / kLanes; r < rows;
-       r += (long long)gridDim.x * (kCopyThreads / kLanes)) {
+       r += (long long)(gridDim.x - 1) * (kCopyThreads / kLanes)) {
     const int key = a.kept[r];
     if (key < 0) continue;
     const int item = r >> 31 ? (int)(r / a.budget) : a.by_budget.of((int)r), place = (int)(r - (long long)item * a.budget);
@@ -361,7 +371,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, void* ws, int num_sms, cudaStrea
   const long long rows = (long long)items * a.budget, blocks = (rows * (a.D / 8) + kCopyThreads - 1) / kCopyThreads;
   const long long most = 16ll * num_sms;
   auto kern = a.D == 64 ? evict_copy_kernel<64> : evict_copy_kernel<128>;
-  return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kCopyThreads), 0, stream, a, rep);
+  return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most) + 1), dim3(kCopyThreads), 0, stream, a, rep);
 }
 
 }  // namespace attn
