@@ -107,6 +107,10 @@ struct Divisor {
 
 constexpr int kMaxAxes = 4;
 
+// Keys of a sequence, heads of a batch: their 32-bit indices are rounded up to a
+// tile and stepped by a block's tile or a grid's blocks, 2^14 at most
+constexpr long long kMostIndex = (1ll << 31) - (1 << 16);
+
 struct RopeArgs {
   Heads q, k, v;
   const float* q_norm;        // [D] or null

@@ -223,6 +223,7 @@ int prefill_paged(const moe_heads* q, const Cache* cache, const int32_t* page_ta
   a.k_cache = static_cast<const uint16_t*>(cache->k);
   a.v_cache = static_cast<const uint16_t*>(cache->v);
   a.scales = scales_of(cache);
+  if (a.scales && ((long long)table_pages << a.page_shift) > kMostIndex) return MOE_ERR_UNSUPPORTED;
   a.pages = cache->pages;
   a.page_table = page_table; a.table_pages = table_pages; a.q_starts = q_starts; a.kv_lens = kv_lens;
   a.n_seq = n_seq; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.causal = causal != 0; a.scale = scale;
@@ -246,6 +247,7 @@ int decode(const moe_heads* q, const Cache* cache, const int32_t* page_table, in
   a.k_cache = static_cast<const uint16_t*>(cache->k);
   a.v_cache = static_cast<const uint16_t*>(cache->v);
   a.scales = scales_of(cache);
+  if (a.scales && ((long long)table_pages << a.page_shift) > kMostIndex) return MOE_ERR_UNSUPPORTED;
   a.pages = cache->pages;
   a.page_table = page_table; a.table_pages = table_pages; a.kv_lens = kv_lens;
   a.prefix_table = prefix_table; a.prefix_len = prefix_len;
@@ -395,6 +397,7 @@ int moe_attn_key_weights(const moe_heads* q, const void* k_cache, int pages, int
   ATTN_TRY(check_type(dtype));
   if (table_pages <= 0 || capacity <= 0 || (T > 0 && n_seq == 0)) return MOE_ERR_INVALID_ARG;
   if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return MOE_ERR_INVALID_ARG;
+  if (capacity > kMostIndex || (long long)n_seq * Hkv > kMostIndex) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   WeightArgs a{};
   ATTN_TRY(check_heads(q, T, Hq, D, &a.q));
@@ -429,7 +432,7 @@ int moe_kv_evict(const moe_kv_cache* cache, const int32_t* page_table, int table
   if (table_pages <= 0 || capacity <= 0 || out_pages <= 0 || budget <= 0 || keep_first < 0 || keep_last < 0)
     return MOE_ERR_INVALID_ARG;
   if ((long long)keep_first + keep_last > budget) return MOE_ERR_INVALID_ARG;
-  if ((long long)n_seq * Hkv >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  if (capacity > kMostIndex || budget > kMostIndex || (long long)n_seq * Hkv > kMostIndex) return MOE_ERR_UNSUPPORTED;
   if (n_seq == 0) return MOE_OK;
   EvictArgs a{};
   ATTN_TRY(check_cache(cache, &a.page_shift));

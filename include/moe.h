@@ -529,7 +529,8 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * moe_attn_prefill_paged and moe_attn_decode over a cache in 8 bits; queries
+ * moe_attn_prefill_paged and moe_attn_decode over a cache in 8 bits, with page
+ * tables of at most 2^31 - 2^16 tokens (table_pages * page_size); queries
  * and outputs are bf16 or f16, codes are multiplied as they are, every sum and
  * softmax statistic is fp32.  Elements of a query head far below its largest
  * are rounded: prefill, those below 2^-9.8 of it (f16: 2^-6.8) to 2^-17.8 of it;
@@ -557,7 +558,8 @@ int moe_attn_decode_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,
  * behind a sequence's keys stay as they were.
  *   k_cache [pages, Hkv, page_size, D] of the type of q (the keys alone)
  *   lse     [T, Hq] fp32, as the attention call over the same rows gave it
- *   weights [n_seq, Hkv, capacity] fp32, kv_lens[s] <= capacity (4-byte aligned)
+ *   weights [n_seq, Hkv, capacity] fp32, kv_lens[s] <= capacity (4-byte aligned);
+ *           capacity and n_seq * Hkv at most 2^31 - 2^16
  * A decode batch is one row per sequence: q_starts 0, 1, .. B.
  */
 int moe_attn_key_weights(const moe_heads *q, const void *k_cache, int pages, int page_size,
@@ -573,7 +575,8 @@ int moe_attn_key_weights(const moe_heads *q, const void *k_cache, int pages, int
  * first; NaN counts as the smallest).  The kept keys and values are copied, in
  * their order, to rows 0 .. m - 1 of the pages out_table[s]; the pages they
  * come from stay as they were.
- *   weights     [n_seq, Hkv, capacity] fp32
+ *   weights     [n_seq, Hkv, capacity] fp32; capacity, budget and n_seq * Hkv at
+ *               most 2^31 - 2^16
  *   out_table   [n_seq, out_pages] int32, budget <= out_pages * page_size; none
  *               of these pages may be one that a sequence of the call reads
  *   new_lens    [n_seq] int32 (out): m; may be kv_lens itself
