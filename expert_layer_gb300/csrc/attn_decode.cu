@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = (int)(top >> 7) - 127;   // an infinity or NaN: as it is
-          const int up = top == 0 || e == 128 ? 0 : min(14 - e, 126);
+          // (beside an infinity, which stays one, every finite element stays finite)
+          const int e = min((int)(top >> 7) - 127, 127);
+          const int up = top == 0 ? 0 : min(14 - e, 126);
           const float f = exp2i(up);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)

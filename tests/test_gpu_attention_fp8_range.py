@@ -208,3 +208,28 @@ def test_a_heavy_key_without_a_value(kernel, D, dtype, gap):
             put(kc, table, 0, j, h, (slice(None), 0.0))
         put(kc, table, 0, gap, h, (0, 8.3 * D ** 0.5 / 8 * 2.0 ** 5))          # 8.3 in the logit
     check(kernel, q, kc, vc, sc, table, q_lens, kv_lens)
+
+
+@pytest.mark.parametrize("D,dtype", SHAPES)
+def test_an_infinite_query_over_keys_that_it_hides(D, dtype):
+    """Decode: logits that are all -inf, beside the largest finite elements of the query against keys of the other sign,
+    give 0 and a log-sum of -inf; the other heads are as without."""
+    kv_lens, Hq, Hkv, page = [300, 40], 8, 2, 16
+    kc, vc, sc, table, _ = pool(kv_lens, page, Hkv, D, 161)
+    for s, m in enumerate(kv_lens):
+        for j in range(m):
+            for h in range(Hkv):
+                put(kc, table, s, j, h, (0, -2.0))
+                put(kc, table, s, j, h, (1, 3.0))
+    q = rand(gen_of(162), 2, Hq, D, dtype=dtype)
+
+    def call():
+        lse = torch.empty(2, Hq, device="cuda")
+        return moe.attn_decode_fp8(q, kc, vc, sc, table, ints(kv_lens), lse=lse), lse
+    want, lse = call()
+    q[1, 3] = 1
+    q[1, 3, 0], q[1, 3, 1] = math.inf, torch.finfo(dtype).max
+    got, lse1 = call()
+    assert bool((got[1, 3] == 0).all()) and float(lse1[1, 3]) == -math.inf
+    got[1, 3], lse1[1, 3] = want[1, 3], lse[1, 3]
+    assert torch.equal(got, want) and torch.equal(lse1, lse)
