@@ -231,10 +231,12 @@ def attn_decode(q, k_cache, v_cache, page_table, kv_lens, prefix_table=None, pre
 
 def attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal=True, scale=None,
                            out=None, lse=None, workspace=None, stream=None):
-    """``attn_prefill_paged`` over a cache in 8 bits (``alloc_fp8_cache``):
-    codes are multiplied as they are, sums and softmax statistics are fp32.
-    Elements of a query head below 2^-9.8 of its largest (f16: 2^-6.8) are
-    rounded, to 2^-17.8 of that; a head that holds an infinity gives NaN."""
+    """``attn_prefill_paged`` over a cache in 8 bits (``alloc_fp8_cache``); sums
+    and softmax statistics are fp32.  Keys are multiplied as codes; values are
+    exact for bf16, for f16 code times scale on f16's own grid; weights round to
+    the type of q, as over a 16-bit cache.  Elements of a query head below 2^-9.8
+    of its largest (f16: 2^-6.8) are rounded, to 2^-17.8 of that; a head that
+    holds an infinity gives NaN."""
     return _load().attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv_lens, causal, scale,
                                           out, lse, workspace, stream)
 
@@ -242,8 +244,12 @@ def attn_prefill_paged_fp8(q, k_cache, v_cache, scales, page_table, q_starts, kv
 def attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table=None, prefix_len=0, scale=None,
                     out=None, lse=None, workspace=None, stream=None):
     """``attn_decode`` over a cache in 8 bits (``alloc_fp8_cache``), its shared
-    prefix there too (with the roundings of ``attn_prefill_paged_fp8``): codes
-    are multiplied as they are, sums and softmax statistics are fp32."""
+    prefix there too (with the roundings of ``attn_prefill_paged_fp8``); sums and
+    softmax statistics are fp32.  Own keys and values are multiplied as codes.
+    Weights are f16 with their value's scale: those below 2^-10 of the largest of
+    the 16 keys that share it are off by up to 2^-21 of that, and keys may be lost
+    whose weight times scale is 2^-64 of another's.  Elements of a bf16 query head
+    below 2^-28 of its largest are rounded, to 2^-39 of that."""
     return _load().attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table, prefix_len, scale,
                                    out, lse, workspace, stream)
 

@@ -531,11 +531,19 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
 /*
  * moe_attn_prefill_paged and moe_attn_decode over a cache in 8 bits, with page
  * tables of at most 2^31 - 2^16 tokens (table_pages * page_size); queries
- * and outputs are bf16 or f16, codes are multiplied as they are, every sum and
- * softmax statistic is fp32.  Elements of a query head far below its largest
- * are rounded: prefill, those below 2^-9.8 of it (f16: 2^-6.8) to 2^-17.8 of it;
- * decode, bf16, those below 2^-28 of it to 2^-39.  In prefill a query head that
- * holds an infinity gives NaN.
+ * and outputs are bf16 or f16, every sum and softmax statistic is fp32.  Beside
+ * the output, these are rounded:
+ *   prefill, and a shared prefix's part of decode:
+ *     queries  elements below 2^-9.8 of their head's largest (f16: 2^-6.8) are off
+ *              by at most 2^-17.8 of it; a head that holds an infinity gives NaN
+ *     values   exact for bf16; for f16, code * scale on f16's grid (2^-24 below 2^-14)
+ *     weights  to the type of q, as over a 16-bit cache
+ *   decode, a row's own keys:
+ *     queries  bf16, elements below 2^-28 of their head's largest: off by 2^-39 of it
+ *     weights  to f16, with their value's scale: those below 2^-10 of the largest
+ *              of the 16 keys that share the scale are off by at most 2^-21 of it.
+ *              Keys may be lost whose weight times scale is 2^-64 of another's.
+ * Keys, and values in decode, are multiplied as codes, which is exact.
  */
 int moe_attn_prefill_paged_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,
                                const int32_t *page_table, int table_pages, const int32_t *q_starts,

@@ -233,3 +233,35 @@ def test_an_infinite_query_over_keys_that_it_hides(D, dtype):
     assert bool((got[1, 3] == 0).all()) and float(lse1[1, 3]) == -math.inf
     got[1, 3], lse1[1, 3] = want[1, 3], lse[1, 3]
     assert torch.equal(got, want) and torch.equal(lse1, lse)
+
+
+@pytest.mark.parametrize("D,dtype", SHAPES)
+def test_behind_a_prefix(D, dtype):
+    """Decode behind a shared prefix: rows of queries with an element 2^12 times the others, and one with an infinity,
+    whose head is NaN there and nowhere else."""
+    kv_lens, shared, Hq, Hkv, page = [300, 20, 0], 500, 8, 2, 16
+    kc, vc, sc, table, pre = pool(kv_lens, page, Hkv, D, 151, prefix=shared, spread=10)
+    q = rand(gen_of(152), 3, Hq, D, dtype=dtype)
+    high = torch.arange(Hq, device="cuda")
+    q[:, high, high * 5] = 2.0 ** 12
+    scale = 0.02 * D ** -0.5
+    ws = moe.alloc_attn_workspace(3, 3, Hq, Hkv, D)
+
+    def call():
+        lse = torch.empty(3, Hq, device="cuda")
+        out = moe.attn_decode_fp8(q, kc, vc, sc, table, ints(kv_lens), pre, shared, scale=scale, lse=lse, workspace=ws)
+        assert moe.read_status(ws) == 0
+        return out, lse
+    out, lse = call()
+    for b, n in enumerate(kv_lens):
+        k, v = rows(kc, vc, sc, table[b], n)
+        pk, pv = rows(kc, vc, sc, pre, shared)
+        k, v = torch.cat([pk, k], 1), torch.cat([pv, v], 1)
+        o, le, to, tl = attend(q[b:b + 1], k, v, scale, None, False, shared)
+        ref.check(out[b:b + 1], o, to, f"out of row {b}")
+        ref.check(lse[b:b + 1], le, tl, f"lse of row {b}")
+    q[1, 3, 7] = math.inf
+    got = call()[0]
+    assert bool(got[1, 3].isnan().all())
+    got[1, 3] = out[1, 3]
+    assert torch.equal(got, out)
