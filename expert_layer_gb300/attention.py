@@ -246,10 +246,9 @@ def attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_tab
     """``attn_decode`` over a cache in 8 bits (``alloc_fp8_cache``), its shared
     prefix there too (with the roundings of ``attn_prefill_paged_fp8``); sums and
     softmax statistics are fp32.  Own keys and values are multiplied as codes.
-    Weights are f16 with their value's scale: those below 2^-10 of the largest of
-    the 16 keys that share it are off by up to 2^-21 of that, and keys may be lost
-    whose weight times scale is 2^-64 of another's.  Elements of a bf16 query head
-    below 2^-28 of its largest are rounded, to 2^-39 of that."""
+    Weights round to f16: those below 2^-14 of the row's largest are off by up to
+    2^-25 of that.  Elements of a bf16 query head below 2^-28 of its largest are
+    rounded, to 2^-39 of that."""
     return _load().attn_decode_fp8(q, k_cache, v_cache, scales, page_table, kv_lens, prefix_table, prefix_len, scale,
                                    out, lse, workspace, stream)
 

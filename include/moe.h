@@ -537,12 +537,11 @@ int moe_attn_decode(const moe_heads *q, const moe_kv_cache *cache, const int32_t
  *     queries  elements below 2^-9.8 of their head's largest (f16: 2^-6.8) are off
  *              by at most 2^-17.8 of it; a head that holds an infinity gives NaN
  *     values   exact for bf16; for f16, code * scale on f16's grid (2^-24 below 2^-14)
- *     weights  to the type of q, as over a 16-bit cache
+ *     weights  to the type of q, as over a 16-bit cache (f16: as in decode)
  *   decode, a row's own keys:
  *     queries  bf16, elements below 2^-28 of their head's largest: off by 2^-39 of it
- *     weights  to f16, with their value's scale: those below 2^-10 of the largest
- *              of the 16 keys that share the scale are off by at most 2^-21 of it.
- *              Keys may be lost whose weight times scale is 2^-64 of another's.
+ *     weights  to f16; those below 2^-14 of the row's largest are off by at most
+ *              2^-25 of it
  * Keys, and values in decode, are multiplied as codes, which is exact.
  */
 int moe_attn_prefill_paged_fp8(const moe_heads *q, const moe_kv_cache_fp8 *cache,

@@ -32,10 +32,9 @@ def attend(q, k, v, scale, seen, prefill, shared=0):
 
     A logit's error as in attn_reference, with three more fp32 roundings of exponents below 2^6 (3 * 2^-19 ln 2) and, in
     prefill, the query parts' (cache8_reference).  P rounds once, in prefill to the element type, in decode to f16; f16
-    below 2^-14 is on a grid of 2^-24:
-      prefill, f16: a row's largest P is at least 1, so a weight e (1 for the largest) is off by min(e, 2^-25)
-      decode: the largest P of 16 keys is at least 2^-4, so by min(e, 2^-21 of the largest of its 16 keys, which share a
-        scale); bf16 queries come to f16, elements below 2^-28 of the largest off by 2^-39 of it
+    below 2^-14 is on a grid of 2^-24, and the P of a row's largest weight so far is at least 1 (in decode, with the scale
+    of the values at hand), so a weight e (1 for the largest) is off by min(e, 2^-25).  In decode bf16 queries come to
+    f16, elements below 2^-28 of the largest off by 2^-39 of it.
     Values are exact in bf16 and in decode; in f16 prefill on a grid of 2^-24, as the outputs are.
     shared: the first keys are a prefix's, which decode reads as prefill does."""
     n, Hq, D = q.shape
@@ -56,12 +55,9 @@ def attend(q, k, v, scale, seen, prefill, shared=0):
             s, off = s.masked_fill(~seen, -math.inf), off.masked_fill(~seen, 0.0)
         e = torch.exp(s - s.amax(1, keepdim=True))
         total = e.sum(1, keepdim=True)
-        lost = e.clamp(max=2.0 ** -25 if half else 0.0)
-        if not prefill:
-            own = e[:, shared:]
-            pad = torch.nn.functional.pad(own, (0, -own.shape[1] % 16)).view(n, -1, 16)
-            most = (2.0 ** -21 * pad.amax(2, keepdim=True)).expand_as(pad).reshape(n, -1)[:, :own.shape[1]]
-            lost[:, shared:] = torch.minimum(own, most)
+        lost = e.clamp(max=2.0 ** -25)
+        if not half:                                        # bf16 P has fp32's range
+            lost[:, :m if prefill else shared] = 0.0
         p, summed = e / total, (m + 16) * 2.0 ** -24
         out[:, h] = p @ vv
         lse[:, h] = (s.amax(1, keepdim=True) + total.log())[:, 0]
