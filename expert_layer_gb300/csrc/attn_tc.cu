@@ -67,8 +67,15 @@ template <bool kCodes>
 constexpr int kSoftRegs = kCodes ? 184 : 208;
 template <bool kCodes>
 constexpr int kLoadRegs = kCodes ? 72 : 88;
-static_assert(2 * kSoftRegs<false> + kLoadRegs<false> <= 3 * 168 && 2 * kSoftRegs<true> + 2 * kLoadRegs<true> <= 4 * 128,
+template <bool kCodes>
+constexpr int kLaunchRegs = kCodes ? 128 : 168;
+static_assert(2 * kSoftRegs<false> + kLoadRegs<false> <= 3 * kLaunchRegs<false> &&
+                  2 * kSoftRegs<true> + 2 * kLoadRegs<true> <= 4 * kLaunchRegs<true>,
               "the shares come from the launch's registers");
+// (setmaxnreg.dec above the launch's count, or .inc below it, is an illegal instruction)
+static_assert(kLoadRegs<false> <= kLaunchRegs<false> && kLaunchRegs<false> <= kSoftRegs<false> &&
+                  kLoadRegs<true> <= kLaunchRegs<true> && kLaunchRegs<true> <= kSoftRegs<true>,
+              "loads give registers up, the softmax draws on them");
 constexpr int kScaleSlots = 8;      // key blocks whose scales are kept
 constexpr int kScaleBlocks = kKeys / kScaleBlock;
 constexpr int kHalf = kKeys / 2;
