@@ -274,7 +274,7 @@ def kv_evict(k_cache, v_cache, page_table, kv_lens, weights, out_table, budget, 
     ``keep_first``, the last ``keep_last`` and those of largest ``weights``
     between (ties: the first; NaN counts as the smallest), copied in their order to the
     pages out_table[s] (int32 [n_seq, out_pages], none of them read by the
-    call).  The pages page_table[s] stay as they were.
+    call or there twice).  The pages page_table[s] stay as they were.
 
     Returns (new_lens int32 [n_seq], new_weights fp32 [n_seq, Hkv, budget],
     kept int32 [n_seq, Hkv, budget]): min(kv_lens, budget), the weights of the

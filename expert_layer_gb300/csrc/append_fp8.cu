@@ -18,10 +18,11 @@
 // page tables and lengths instead of a slot for each token: no atomics, no
 // second pass over the batch, the same bits every time.
 // Measured (32 + 2 x 4 heads of 128, norms): 256 sequences with a token each 5.2
-// us, 8 prompts of 700 to 1300 tokens 38.9 us = 4.2 TB/s.  Not kept: two warps to
-// a scale block, with its rows in registers, 41.7 us (64 registers, spilled) and
-// 44.9 (80), from shared memory 40.8 and 43.2; the blocks of k and v between those
-// of q 38.5 to 40.4.
+// us, 8 prompts of 700 to 1300 tokens 39.3 us = 4.2 TB/s, with DRAM 39% and the issue
+// slots 50% busy: the loads' latency, mostly.  Not kept: two warps to a scale block,
+// with its rows in registers, 41.7 us (64 registers) and 44.9 (80), from shared memory
+// 40.8 and 43.2; the blocks of k and v between those of q 38.5 to 40.4.  (64 registers
+// are a few short here too: 36 to 52 bytes spilled.)
 #include "attn.h"
 #include "attn_ptx.cuh"
 #include "rope_rows.cuh"

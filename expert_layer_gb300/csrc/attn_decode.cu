@@ -26,8 +26,8 @@
 // keys 167 us = 6.4 TB/s, 95% of a copy's rate; one of 131,001 keys 49.9 us, of
 // which it streams 38 at 6.9 TB/s; 64 of 1 to 8192 keys 26.8; 1024 of 90 keys
 // 46.9; 8 of 400 keys 9.5, the keys themselves 1 (the rest is start, join and
-// merge).  Over a cache in 8 bits 128 of 2000 to 8192 keys take 98 us = 6.0 TB/s,
-// in 16 bits 178; 8 of 100 to 700 keys (16 and 2 heads of 64) 8.1.
+// merge).  Over a cache in 8 bits 128 of 2000 to 8192 keys take 99 us = 5.9 TB/s,
+// in 16 bits 180; 8 of 100 to 700 keys (16 and 2 heads of 64) 7.9.
 #include "attn.h"
 #include "attn_ptx.cuh"
 

@@ -10,10 +10,12 @@
 // multiplied with both, for one warpgroup each (with one tile of keys a row tile
 // would be read for 512 cycles of work, 64 bytes a cycle and SM from L2).  Blocks
 // take equal ranges of the line of all units (attn_weights.cu).
-// Bound: exponentials, 32 a cycle and SM, and the products, 2 x 512 cycles for
-// each row tile (D = 128), run beside each other.  Measured: the last 64 rows of
-// four prompts of 4000 to 16,000 keys (32 query and 4 key-value heads of 128) 31.8
-// us, on mma.sync 111.
+// Measured: the last 64 rows of four prompts of 4000 to 16,000 keys (32 query and 4
+// key-value heads of 128) 31.8 us, on mma.sync 111.  Its exponentials (32 a cycle
+// and SM) are 6.5 us of that, its products (2 x 512 cycles for each row tile, D =
+// 128) 7, the start 5.5; neither pipe is its bound (tensor pipe 19% busy, issue slots
+// 21%).  A warp of the sums loads S and then sums it, an entry is read when its unit
+// ends, and 512 units are 3.4 uneven rounds of 152 SMs.
 #include "attn.h"
 #include "attn_ptx.cuh"
 #include "weights_line.cuh"

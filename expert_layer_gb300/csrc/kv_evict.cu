@@ -11,7 +11,7 @@
 // other pages rather than within them leaves every row free of the others', and
 // pages that sequences share as they were.
 // Bound: HBM for the copy (8 D bytes a kept key and head), latency for the first:
-// 64 sequences, 4 heads of 128, 16,384 keys at most, 1024 kept: 62 us, the copy 34
+// 64 sequences, 4 heads of 128, 16,384 keys at most, 1024 kept: 60 us, the copy 34
 // of them; the first kernel's time is the chain of a long item, up to 16 counts
 // with a barrier each (long and short items paired on the SMs: equal).  One kernel
 // for both: 90 us, rows wait for their search.

@@ -585,7 +585,8 @@ int moe_attn_key_weights(const moe_heads *q, const void *k_cache, int pages, int
  *   weights     [n_seq, Hkv, capacity] fp32; capacity, budget and n_seq * Hkv at
  *               most 2^31 - 2^16
  *   out_table   [n_seq, out_pages] int32, budget <= out_pages * page_size; none
- *               of these pages may be one that a sequence of the call reads
+ *               of these pages may be one that a sequence of the call reads, and
+ *               none may be there twice
  *   new_lens    [n_seq] int32 (out): m; may be kv_lens itself
  *   new_weights [n_seq, Hkv, budget] fp32 (out): weights of the kept keys, 0 from m on
  *   kept        [n_seq, Hkv, budget] int32 (out): their places before, -1 from m on
