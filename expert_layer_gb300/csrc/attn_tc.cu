@@ -461,7 +461,12 @@ __device__ __forceinline__ bool bad_arrays(const AttnArgs& a) {
 // f16 lies on it).  So P and V round as over a 16-bit cache, whatever the scales
 // of other keys.  (P in f16 with a tile's largest scale in its exponent, and the
 // values in f16 under that scale, lost what keys of small scales add beside a
-// large one, and let a row depend on keys that it does not see.)
+// large one, and let a row depend on keys that it does not see; in bf16 the outputs'
+// error against 64 bits was 1.7e-3 and is 2.3e-3, that over a 16-bit cache.)
+// Measured: 4096 rows over 8192 keys (32/4 heads of 128) 325 us, f16 328, heads of 64
+// 260 and 269; over a 16-bit cache 248, 254, 227, 227.  The four warps' work on a
+// tile of V beside the softmax is what is left (without it 297); with K made elements
+// too it was 408.
 template <int D, bool kF16, bool kPaged, bool kCodes>
 __global__ void __launch_bounds__(kThreads<kCodes>, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
